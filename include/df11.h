@@ -364,6 +364,137 @@ df11_status df11_nf12_decode(const void *host_header, const void *d_container, v
 df11_status df11_nf12_decode_batch(const void *const *host_headers, const void *const *d_containers,
                                    void *const *d_outs, int n_tensors, int hip_device, hipStream_t stream);
 
+/* ------------------------------------------- key-value cache and attention */
+
+/* For a consumer of the decoded weights that serves a model: a paged
+ * key-value cache, as BF16 words or in 8 bits, and attention over packed
+ * prompts and over the cache.  The layer loop decodes a layer's weights, the
+ * caller's products make queries, keys and values, and these calls keep the
+ * keys and values and attend to them.
+ *
+ * Every call takes DEVICE pointers, enqueues on `stream` of device
+ * `hip_device` and returns; none allocates, waits, or keeps anything for a
+ * later call.  Sizes and strides are checked on the host (DF11_E_ARG; a size
+ * that this build's launches cannot hold: DF11_E_UNSUPPORTED), and nothing is
+ * enqueued after an error.  Memory safety does not depend on the device
+ * arrays of indexes: a page number past the cache reads the last page, a
+ * length past the table's pages counts as theirs, a slot outside the cache is
+ * not written, and a sequence whose starts are not in order within the rows
+ * is passed over.
+ *
+ * Attention of query row i of a sequence, per query head h and its kv head
+ * h / (n_heads / n_kv_heads):
+ *   out = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * <q, k_j> - max)
+ * over the keys j that the row sees; a row that sees none, or whose scores
+ * are all minus infinity, is zero.  What is at a key that no row of the call
+ * sees (the rest of a page, another sequence's rows) does not matter, be it
+ * infinite or NaN.  Products are of BF16 operands (the weights p_j are rounded
+ * to BF16, as the values are); scores, maxima, sums and accumulators are in 32
+ * bits, and the result is rounded once.  Results do not depend on other work
+ * on the GPU: sums are taken in a fixed order. */
+
+/* Rows of heads in BF16: element (row, head, d) at data[row * row_stride +
+ * head * head_stride + d].  Strides in elements, multiples of 8, at least 0;
+ * data 16-byte aligned.  Rows that are written do not overlap. */
+typedef struct {
+    void *data;
+    int64_t row_stride, head_stride;
+} df11_rows;
+
+#define DF11_KV_BF16 0u
+#define DF11_KV_INT8 1u
+
+/* A paged cache in the caller's memory: k and v are n_pages x n_kv_heads x
+ * page_size x head_dim elements, BF16 words or (DF11_KV_INT8) signed bytes;
+ * with bytes, k_scale and v_scale are n_pages x n_kv_heads x page_size floats
+ * (else NULL), and element x stands for code * scale.  page_size: a power of
+ * two from 16 to 1024; head_dim: 64 or 128; all 16-byte aligned.  Slot
+ * page * page_size + i is position i of a page. */
+typedef struct {
+    void *k, *v;
+    float *k_scale, *v_scale;
+    uint32_t n_pages, page_size, n_kv_heads, head_dim, store, reserved;
+} df11_kv_cache;
+
+/* Page tables: pages[s * row_stride + i], i < width, is the page that holds
+ * positions i * page_size .. of sequence s (entries past its length are not
+ * read). */
+typedef struct {
+    const int32_t *pages;
+    int64_t row_stride;
+    uint32_t width, reserved;
+} df11_page_table;
+
+/* Write token t's keys and values (rows k, v of n_kv_heads heads) into slot
+ * slots[t] of the cache, t < n_tokens; a slot outside the cache (below zero,
+ * say) leaves its token out.  Slots are distinct.  In 8 bits, for each token
+ * and head: a = max |x| (2^-100 if that is larger), scale = a / 127, codes
+ * rint(x * (127 / a)), ties to even, in 32 bits; a row that holds an infinity
+ * or NaN reads back as NaN. */
+typedef struct {
+    df11_kv_cache cache;
+    df11_rows k, v;
+    const int64_t *slots;
+    uint64_t n_tokens;
+} df11_kv_write_args;
+df11_status df11_kv_write(const df11_kv_write_args *args, int hip_device, hipStream_t stream);
+
+/* Read back the first starts[s + 1] - starts[s] tokens of each sequence s <
+ * n_seqs as packed rows: position i of sequence s to row starts[s] + i of k
+ * and v (n_tokens rows).  8-bit codes times their scale are rounded to BF16. */
+typedef struct {
+    df11_kv_cache cache;
+    df11_page_table table;
+    df11_rows k, v;
+    const int32_t *starts;
+    uint64_t n_tokens;
+    uint32_t n_seqs, reserved;
+} df11_kv_read_args;
+df11_status df11_kv_read(const df11_kv_read_args *args, int hip_device, hipStream_t stream);
+
+/* Attention of one query row a sequence (row s of q, n_heads heads, a multiple
+ * of the cache's) over the first lens[s] positions of its pages, into row s of
+ * out.  scale > 0.  Long sequences are split over workgroups and joined, for
+ * which the call needs df11_attend_token_workspace bytes (0 for small calls;
+ * the function reads the sizes alone, no pointers) of 16-byte aligned device
+ * memory, that no other call uses meanwhile.  out may be q. */
+typedef struct {
+    df11_kv_cache cache;
+    df11_page_table table;
+    df11_rows q, out;
+    const int32_t *lens;
+    void *workspace;
+    uint64_t workspace_bytes;
+    uint32_t n_seqs, n_heads;
+    float scale;
+    uint32_t reserved;
+} df11_attend_token_args;
+uint64_t df11_attend_token_workspace(const df11_attend_token_args *args, int hip_device);
+df11_status df11_attend_token(const df11_attend_token_args *args, int hip_device, hipStream_t stream);
+
+#define DF11_ATTEND_CAUSAL 1u
+
+/* Attention of packed sequences: the queries of sequence s are rows
+ * q_starts[s] .. q_starts[s + 1] - 1 of q (n_q rows, n_heads heads), its keys
+ * and values rows k_starts[s] .. of k and v (n_k rows, n_kv_heads heads, a
+ * divisor of n_heads), the results the queries' rows of out.  With
+ * DF11_ATTEND_CAUSAL the queries are the last of their sequence: query i sees
+ * the keys j <= i + n_keys - n_queries (so a prompt's next piece attends to
+ * what came before, and with more queries than keys the first see none);
+ * otherwise all.  head_dim 64 or 128, scale > 0.  Workspace: as for
+ * df11_attend_token (few rows over many keys are split).  out may be q. */
+typedef struct {
+    df11_rows q, k, v, out;
+    const int32_t *q_starts, *k_starts;
+    void *workspace;
+    uint64_t workspace_bytes;
+    uint64_t n_q, n_k;
+    uint32_t n_seqs, n_heads, n_kv_heads, head_dim, flags;
+    float scale;
+} df11_attend_prompt_args;
+uint64_t df11_attend_prompt_workspace(const df11_attend_prompt_args *args, int hip_device);
+df11_status df11_attend_prompt(const df11_attend_prompt_args *args, int hip_device, hipStream_t stream);
+
 /* ------------------------------------------------------------------- misc */
 
 /* Text of the last non-OK status on this thread (never NULL). */

@@ -9,3 +9,5 @@ layout.
 from ._lib import (ABI_VERSION, FLAG_SHA256, DF11Error, Plan, bw_control, check, container_bound, decode,  # noqa: F401
                    decode_batch, encode, encode_device, encode_device_batch, lib, nf12_decode, nf12_decode_batch, nf12_encode, nf12_validate,
                    sha256, validate, validate_status, verify, verify_decoded, verify_status)
+from ._serve import (KVCache, attend_prompt, attend_token, kv_cache, kv_read, kv_write, prompt_workspace,  # noqa: F401
+                     token_workspace)

@@ -25,6 +25,10 @@ SOURCES = [
     ("nf12.cpp", ["-x", "c++", "-D__HIP_PLATFORM_AMD__", "-I/opt/rocm/include"]),
     ("nf12.hip", DEVICE),
     ("encode_gpu.hip", DEVICE),
+    ("serve.cpp", ["-x", "c++", "-D__HIP_PLATFORM_AMD__", "-I/opt/rocm/include"]),
+    ("kv_cache.hip", DEVICE),
+    ("attend_token.hip", DEVICE),
+    ("attend_prompt.hip", DEVICE),
 ]
 
 

@@ -64,6 +64,8 @@ EXPORTS = [
     "df11_status_str", "df11_abi_version", "df11_bw_control",
     "df11_nf12_bound", "df11_nf12_encode", "df11_nf12_validate", "df11_nf12_decode",
     "df11_nf12_decode_batch",
+    "df11_kv_write", "df11_kv_read", "df11_attend_token_workspace", "df11_attend_token",
+    "df11_attend_prompt_workspace", "df11_attend_prompt",
 ]
 
 
@@ -134,6 +136,13 @@ def lib():
     L.df11_nf12_decode_batch.argtypes = [ctypes.POINTER(vp), ctypes.POINTER(vp), ctypes.POINTER(vp),
                                          ctypes.c_int, ctypes.c_int, vp]
     L.df11_nf12_decode_batch.restype = ctypes.c_int
+    # (the serving calls take one argument struct: _serve.py packs its bytes)
+    for name in ("df11_kv_write", "df11_kv_read", "df11_attend_token", "df11_attend_prompt"):
+        getattr(L, name).argtypes = [ctypes.c_char_p, ctypes.c_int, vp]
+        getattr(L, name).restype = ctypes.c_int
+    for name in ("df11_attend_token_workspace", "df11_attend_prompt_workspace"):
+        getattr(L, name).argtypes = [ctypes.c_char_p, ctypes.c_int]
+        getattr(L, name).restype = u64
     _lib = L
     return L
 

@@ -1,0 +1,267 @@
+// Attention over packed prompts for gfx950, causal or not, with grouped heads.
+//
+// Query i of a sequence with n_q queries and n_k keys sees the keys below
+// lim_i = i + 1 + n_k - n_q (causal) or n_k.  s_j = <q_i, k_j>, p_j =
+// 2^(c s_j - m), c = scale log2(e), m the running maximum of c s_j, out = sum
+// p_j v_j / sum p_j; a row that sees no key is 0.  One pass over the keys:
+// when a step raises m, the sums are scaled by 2^(old - new).
+//
+// A workgroup takes 128 query rows of one head, its four waves 32 each, and
+// steps over the keys 64 at a time through LDS.  Matrix instructions, 32 x 32
+// x 16: S^T = K Q^T puts a query in each lane (column) with 16 keys of 32 in
+// its registers (the lane 32 away has the others), so that the row statistics
+// are per lane, and P^T is the second product's operand as it stands: O^T =
+// V^T P^T sums over keys in any order, so the key of operand slot (half h, j)
+// is 4h + j for j < 4 and 8 + 4h + j - 4 above.  V^T comes from row-major V in
+// LDS by transposing reads.  The matrix rate and, beside it, the exponentials
+// bound it.
+#include "serve_device.hpp"
+#include "serve_internal.hpp"
+
+namespace df11 {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr uint32_t kWaveRows = 32;
+
+// Byte offsets of 16-byte chunk `chunk` of key row `row` in the K and V tiles.
+// K: 32 rows are read at one chunk a time; V: four neighbouring rows, 32 bytes
+// of each, by a transposing read.  The exclusive or puts them into different
+// banks.
+template <int D>
+__device__ __forceinline__ uint32_t k_at(uint32_t row, uint32_t chunk) {
+    return D == 128 ? row * 256 + ((chunk ^ (row & 15)) << 4) : row * 128 + ((chunk ^ ((row >> 1) & 7)) << 4);
+}
+template <int D>
+__device__ __forceinline__ uint32_t v_at(uint32_t row, uint32_t chunk) {
+    return D == 128 ? row * 256 + ((chunk ^ ((row & 3) << 2)) << 4) : row * 128 + ((chunk ^ (((row >> 1) & 1) << 2)) << 4);
+}
+
+// x and the value 32 lanes away, in either order.
+__device__ __forceinline__ f32x2 both_halves(float x) {
+    const uint32_t a = __float_as_uint(x);
+    const auto r = __builtin_amdgcn_permlane32_swap(a, a, false, false);
+    return f32x2{__uint_as_float(r[0]), __uint_as_float(r[1])};
+}
+__device__ __forceinline__ float max_halves(float x) {
+    const f32x2 r = both_halves(x);
+    return fmaxf(r.x, r.y);
+}
+__device__ __forceinline__ float add_halves(float x) {
+    const f32x2 r = both_halves(x);
+    return r.x + r.y;
+}
+
+template <int D, bool kSplit>
+__global__ __launch_bounds__(kThreads) void attend_prompt_kernel(PromptArgs a) {
+    constexpr int kChunks = D / 8;                           // 16-byte chunks of a row
+    constexpr int kLoads = kPromptKeys * kChunks / kThreads; // chunks a thread stages
+    constexpr int kDTiles = D / 32;
+    constexpr int kDSteps = D / 16;
+    __shared__ __attribute__((aligned(16))) uint8_t kt[kPromptKeys * D * 2];
+    __shared__ __attribute__((aligned(16))) uint8_t vt[kPromptKeys * D * 2];
+
+    const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t col = lane & 31u, half = lane >> 5;
+
+    // (workgroups are dealt to the eight XCDs in turn: kv heads vary fastest,
+    // so that the heads that share one meet in one L2; the last rows of a
+    // causal prompt, which see the most keys, start first)
+    const uint32_t kv_head = blockIdx.x % a.kv_heads, rest = blockIdx.x / a.kv_heads;
+    const uint32_t head = kv_head * a.group + rest % a.group;
+    const uint32_t slot = a.tile_slots - 1 - rest / a.group;
+    uint32_t tile;
+    const uint32_t seq = sequence_of_slot(a.q_starts, a.n_seqs, slot, 7, &tile);
+    const int32_t q0 = a.q_starts[seq], q1 = a.q_starts[seq + 1], k0 = a.k_starts[seq], k1 = a.k_starts[seq + 1];
+    if (q0 < 0 || q1 < q0 || (uint32_t)q1 > a.n_q || k0 < 0 || k1 < k0 || (uint32_t)k1 > a.n_k) return;
+    const uint32_t n_q = q1 - q0, n_k = k1 - k0;
+    if ((uint64_t)tile * kPromptTile >= n_q) return;
+    const uint32_t row0 = tile * kPromptTile;                // of the sequence
+
+    // keys that a row sees
+    const auto limit = [&](uint32_t row) -> uint32_t {
+        if (!a.causal) return n_k;
+        const int64_t l = (int64_t)row + 1 + n_k - n_q;
+        return l < 0 ? 0 : l > n_k ? n_k : (uint32_t)l;
+    };
+    const uint32_t most_keys = limit(min(row0 + kPromptTile, n_q) - 1);
+    uint32_t key_begin = 0, key_end = most_keys;
+    if (kSplit) {
+        const uint32_t per = ((n_k + a.splits - 1) / a.splits + kPromptKeys - 1) / kPromptKeys * kPromptKeys;
+        const uint64_t b = (uint64_t)blockIdx.y * per;
+        key_begin = b < key_end ? (uint32_t)b : key_end;
+        key_end = b + per < key_end ? (uint32_t)(b + per) : key_end;
+    }
+    const uint32_t wave_first = row0 + wave * kWaveRows, row = wave_first + col;
+    const bool real = row < n_q;
+    // (rows past the last compute on zero queries, and are not stored)
+    const uint32_t lim = real ? limit(row) : n_k;
+    // the wave's rows all see the keys below `clear`, and none from wave_end on
+    const uint32_t clear = limit(wave_first);
+    const uint32_t wave_end = wave_first < n_q ? limit(min(wave_first + kWaveRows, n_q) - 1) : 0;
+
+    u32x4 q[kDSteps];
+#pragma unroll
+    for (int i = 0; i < kDSteps; ++i) {
+        q[i] = u32x4{0, 0, 0, 0};
+        if (real) q[i] = *reinterpret_cast<const u32x4 *>(a.q.data + (int64_t)(q0 + row) * a.q.row + head * a.q.head + 16 * i + 8 * half);
+    }
+
+    f32x16 o[kDTiles];
+#pragma unroll
+    for (int i = 0; i < kDTiles; ++i) o[i] = f32x16{};
+    float m = -__builtin_inff(), l = 0;
+
+    const uint16_t *const kp = a.k.data + (int64_t)k0 * a.k.row + kv_head * a.k.head;
+    const uint16_t *const vp = a.v.data + (int64_t)k0 * a.v.row + kv_head * a.v.head;
+
+    for (uint32_t key0 = key_begin; key0 < key_end; key0 += kPromptKeys) {
+        u32x4 kw[kLoads], vw[kLoads];
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const uint32_t at = i * kThreads + threadIdx.x, r = key0 + at / kChunks, c = at % kChunks;
+            kw[i] = vw[i] = u32x4{0, 0, 0, 0};               // (past the sequence: another one's rows)
+            if (r < n_k) {
+                kw[i] = *reinterpret_cast<const u32x4 *>(kp + r * a.k.row + 8 * c);
+                vw[i] = *reinterpret_cast<const u32x4 *>(vp + r * a.v.row + 8 * c);
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const uint32_t at = i * kThreads + threadIdx.x, r = at / kChunks, c = at % kChunks;
+            *reinterpret_cast<u32x4 *>(kt + k_at<D>(r, c)) = kw[i];
+            *reinterpret_cast<u32x4 *>(vt + v_at<D>(r, c)) = vw[i];
+        }
+        __syncthreads();
+        if (key0 >= wave_end) continue;
+
+        f32x16 s[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            s[t] = f32x16{};
+#pragma unroll
+            for (int i = 0; i < kDSteps; ++i) {
+                const u32x4 w = *reinterpret_cast<const u32x4 *>(kt + k_at<D>(32 * t + col, 2 * i + half));
+                s[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(w), as_bf16x8(q[i]), s[t], 0, 0, 0);
+            }
+        }
+        if (key0 + kPromptKeys > clear) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const uint32_t key = key0 + 32 * t + 8 * (i / 4) + 4 * half + i % 4;
+                    if (key >= lim) s[t][i] = -__builtin_inff();
+                }
+        }
+        float top = -__builtin_inff();
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = fmaxf(top, s[t][i]);
+        top = max_halves(top) * a.log2_scale;
+        const float next = fmaxf(m, top);
+        const float base = next == -__builtin_inff() ? 0.0f : next;
+        const float keep = exp2_fast(m - base);
+        m = next;
+        l *= keep;
+#pragma unroll
+        for (int i = 0; i < kDTiles; ++i) o[i] *= keep;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+            for (int st = 0; st < 2; ++st) {
+                u32x4 p;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float x = exp2_fast(__builtin_fmaf(s[t][8 * st + 2 * j], a.log2_scale, -base));
+                    const float y = exp2_fast(__builtin_fmaf(s[t][8 * st + 2 * j + 1], a.log2_scale, -base));
+                    l += x + y;
+                    p[j] = pack_bf16(x, y);
+                }
+#pragma unroll
+                for (int i = 0; i < kDTiles; ++i) {
+                    const uint32_t j = lane & 15u, r = 32 * t + 16 * st + 4 * half + (j >> 2);
+                    const uint32_t chunk = 4 * i + 2 * ((lane >> 4) & 1u) + ((j & 3) >> 1);
+                    const s16x4 b0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((DF11_LDS s16x4 *)(vt + v_at<D>(r, chunk) + 8 * (j & 1)));
+                    const s16x4 b1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((DF11_LDS s16x4 *)(vt + v_at<D>(r + 8, chunk) + 8 * (j & 1)));
+                    const u32x2 w0 = __builtin_bit_cast(u32x2, b0), w1 = __builtin_bit_cast(u32x2, b1);
+                    o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(u32x4{w0.x, w0.y, w1.x, w1.y}), as_bf16x8(p), o[i], 0, 0, 0);
+                }
+            }
+        }
+    }
+    l = add_halves(l);
+    if (!real) return;
+    if (kSplit) {
+        const uint64_t at = ((uint64_t)blockIdx.y * a.n_q + q0 + row) * a.heads + head;
+#pragma unroll
+        for (int i = 0; i < kDTiles; ++i)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                *reinterpret_cast<f32x4 *>(a.part + at * D + 32 * i + 8 * g + 4 * half) =
+                    f32x4{o[i][4 * g], o[i][4 * g + 1], o[i][4 * g + 2], o[i][4 * g + 3]};
+        if (half == 0) *reinterpret_cast<f32x2 *>(a.part_ml + 2 * at) = f32x2{m, l};
+        return;
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    uint16_t *const op = a.out.data + (int64_t)(q0 + row) * a.out.row + head * a.out.head;
+#pragma unroll
+    for (int i = 0; i < kDTiles; ++i)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+            *reinterpret_cast<u32x2 *>(op + 32 * i + 8 * g + 4 * half) =
+                u32x2{pack_bf16(o[i][4 * g] * inv, o[i][4 * g + 1] * inv), pack_bf16(o[i][4 * g + 2] * inv, o[i][4 * g + 3] * inv)};
+}
+
+// Joins the parts of a tile's rows for one head: out = sum_a w_a o_a / sum_a
+// w_a l_a with w_a = 2^(m_a - max m).  D / 4 lanes a row.
+constexpr uint32_t kJoinRows = 8;
+
+template <int D>
+__global__ __launch_bounds__(kJoinRows * D / 4) void join_prompt_kernel(PromptArgs a) {
+    constexpr uint32_t kLanes = D / 4;
+    const uint32_t head = blockIdx.x % a.heads;
+    uint32_t tile;
+    const uint32_t seq = sequence_of_slot(a.q_starts, a.n_seqs, blockIdx.x / a.heads, 7, &tile);
+    const int32_t q0 = a.q_starts[seq], q1 = a.q_starts[seq + 1], k0 = a.k_starts[seq], k1 = a.k_starts[seq + 1];
+    if (q0 < 0 || q1 < q0 || (uint32_t)q1 > a.n_q || k0 < 0 || k1 < k0 || (uint32_t)k1 > a.n_k) return;
+    const uint64_t in_seq = (uint64_t)tile * kPromptTile + blockIdx.y * kJoinRows + threadIdx.x / kLanes;
+    if (in_seq >= (uint32_t)(q1 - q0)) return;
+    const uint64_t unit = (q0 + in_seq) * a.heads + head, n_units = (uint64_t)a.n_q * a.heads;
+    const uint32_t d = threadIdx.x % kLanes * 4;
+    const f32x2 *const ml = reinterpret_cast<const f32x2 *>(a.part_ml) + unit;
+    float most = -__builtin_inff();
+    for (uint32_t i = 0; i < a.splits; ++i) most = fmaxf(most, ml[i * n_units].x);
+    const float base = most == -__builtin_inff() ? 0.0f : most;
+    f32x4 sum = {0, 0, 0, 0};
+    float l = 0;
+#pragma unroll 4
+    for (uint32_t i = 0; i < a.splits; ++i) {
+        const f32x2 p = ml[i * n_units];
+        const float w = exp2_fast(p.x - base);
+        l += w * p.y;
+        sum += *reinterpret_cast<const f32x4 *>(a.part + (i * n_units + unit) * D + d) * w;
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    *reinterpret_cast<u32x2 *>(a.out.data + (int64_t)(q0 + in_seq) * a.out.row + head * a.out.head + d) =
+        u32x2{pack_bf16(sum.x * inv, sum.y * inv), pack_bf16(sum.z * inv, sum.w * inv)};
+}
+
+}  // namespace
+
+hipError_t launch_attend_prompt(const PromptArgs &a, uint32_t head_dim, hipStream_t stream) {
+    const dim3 grid(a.tile_slots * a.heads, a.splits);
+    const auto kernel = head_dim == 64 ? (a.splits > 1 ? attend_prompt_kernel<64, true> : attend_prompt_kernel<64, false>)
+                                       : (a.splits > 1 ? attend_prompt_kernel<128, true> : attend_prompt_kernel<128, false>);
+    hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.splits == 1) return e;
+    hipLaunchKernelGGL(head_dim == 64 ? join_prompt_kernel<64> : join_prompt_kernel<128>,
+                       dim3(a.tile_slots * a.heads, kPromptTile / kJoinRows), dim3(kJoinRows * head_dim / 4), 0, stream, a);
+    return hipGetLastError();
+}
+
+}  // namespace df11

@@ -1,0 +1,295 @@
+// Attention of one new token of each sequence over the paged cache, for
+// gfx950.
+//
+// For query head h of kv head h / group: s_j = <q, k_j>, p_j = 2^(c s_j - m)
+// with c = scale log2(e) and m the running maximum of c s_j, out = sum p_j
+// v_j / sum p_j.  One pass over the keys: when a step raises m, the sums are
+// scaled by 2^(old - new).  Keys in 8 bits keep their codes as exact BF16
+// operands: a key's scale multiplies its score, a value's scale its weight.
+//
+// Every key and value is read once and used by `group` queries, so HBM
+// traffic bounds it.  A workgroup takes up to `range` keys of one kv head
+// (work along a long sequence is split over workgroups, and a second kernel
+// joins the parts); its four waves take 32 keys a step in turn, each with its
+// own maximum, sum and accumulators, joined through LDS at the end.
+//
+// Matrix instructions, 16 x 16 x 32: S^T = K Q^T puts a query in each lane
+// (column) and four keys in its registers, so that the row statistics are per
+// lane, and P^T is the second product's operand as it stands: O^T = V^T P^T
+// sums over keys in any order, so the key of operand slot (lane group c, j) is
+// 4c + j for j < 4 and 16 + 4c + j - 4 above, the keys that the lane holds.
+// V^T comes from row-major V in LDS by transposing reads.
+#include "serve_device.hpp"
+#include "serve_internal.hpp"
+
+namespace df11 {
+
+namespace {
+
+constexpr int kThreads = 64 * kTokenWaves;
+constexpr uint32_t kMostPages = kTokenRangeMax / 16;
+
+// Where 16-byte chunk `chunk` of key row `row` lies in a wave's V tile: the
+// transposing reads take 32 bytes of four neighbouring rows at a time, which
+// the exclusive or puts into different banks.
+template <int kRowBytes>
+__device__ __forceinline__ uint32_t v_at(uint32_t row, uint32_t chunk) {
+    if (kRowBytes == 256) return row * 256 + ((chunk ^ ((row & 3) << 2)) << 4);
+    if (kRowBytes == 128) return row * 128 + ((chunk ^ (((row >> 1) & 1) << 2)) << 4);
+    return row * 64 + (chunk << 4);
+}
+
+template <int D, bool kInt8>
+__global__ __launch_bounds__(kThreads) void attend_token_kernel(TokenArgs a) {
+    constexpr int kRow = kInt8 ? D : 2 * D;            // bytes of a stored row
+    constexpr int kChunks = kRow / 16;                 // 16-byte chunks of it
+    constexpr int kTileChunks = kTokenKeys * kChunks / 64;   // chunks a lane moves for 32 rows
+    constexpr int kDTiles = D / 16;
+    constexpr int kOStride = D + 4;
+    constexpr uint32_t kVBytes = kTokenKeys * kRow;
+    constexpr uint32_t kJoinBytes = kTokenWaves * 16 * kOStride * 4;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kTokenWaves * kVBytes > kJoinBytes ? kTokenWaves * kVBytes : kJoinBytes];
+    __shared__ uint32_t table[kMostPages];
+    __shared__ float ml[kTokenWaves][2][16];
+
+    const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t col = lane & 15u, grp = lane >> 4;
+    uint32_t at = blockIdx.x;
+    const uint32_t q_tile = at % a.q_tiles;
+    at /= a.q_tiles;
+    const uint32_t kv_head = at % a.c.kv_heads, seq = at / a.c.kv_heads;
+    const uint32_t split = blockIdx.y;
+
+    const uint32_t len = (uint32_t)min((int64_t)max(a.lens[seq], 0), (int64_t)a.t.width << a.c.shift);
+    const uint32_t begin = split * a.range;
+    if (begin >= len && split) return;
+    const uint32_t n = min(len - begin, a.range);      // this workgroup's keys
+
+    // the pages of the range
+    const int32_t *const pages = a.t.pages + seq * a.t.stride + (begin >> a.c.shift);
+    for (uint32_t i = threadIdx.x; i < ((n + (1u << a.c.shift) - 1) >> a.c.shift); i += kThreads)
+        table[i] = min((uint32_t)pages[i], a.c.n_pages - 1);
+
+    // queries: columns past the group are zero
+    const uint32_t in_group = q_tile * 16 + col;
+    const uint32_t head = kv_head * a.group + in_group;
+    const bool real = in_group < a.group;
+    u32x4 q[D / 32];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+        // words: step i holds d = 32 i + 8 grp ..; bytes: two steps share a
+        // 16-byte chunk, so steps 2t and 2t + 1 hold d = 64 t + 16 grp + 0 and 8 ..
+        const uint32_t d = kInt8 ? 64 * (i / 2) + 16 * grp + 8 * (i % 2) : 32 * i + 8 * grp;
+        q[i] = u32x4{0, 0, 0, 0};
+        if (real) q[i] = *reinterpret_cast<const u32x4 *>(a.q.data + seq * a.q.row + head * a.q.head + d);
+    }
+    __syncthreads();
+
+    const auto row_of = [&](uint32_t key) {            // of a key of the range
+        const uint32_t page = table[key >> a.c.shift];
+        return (((int64_t)page * a.c.kv_heads + kv_head) << a.c.shift) + (key & ((1u << a.c.shift) - 1));
+    };
+
+    f32x4 o[kDTiles];
+#pragma unroll
+    for (int i = 0; i < kDTiles; ++i) o[i] = f32x4{0, 0, 0, 0};
+    float m = -__builtin_inff(), l = 0;
+    uint8_t *const vt = lds + wave * kVBytes;
+
+    for (uint32_t key0 = wave * kTokenKeys; key0 < n; key0 += kTokenWaves * kTokenKeys) {
+        // V rows of the step into this wave's tile; rows past the end are zero
+        // (their weights are 0, and 0 times a stray infinity would be NaN)
+#pragma unroll
+        for (int i = 0; i < kTileChunks; ++i) {
+            const uint32_t at = i * 64 + lane, row = at / kChunks, chunk = at % kChunks;
+            u32x4 w = {0, 0, 0, 0};
+            if (key0 + row < n) w = *reinterpret_cast<const u32x4 *>(a.c.v + row_of(key0 + row) * kRow + 16 * chunk);
+            *reinterpret_cast<u32x4 *>(vt + v_at<kRow>(row, chunk)) = w;
+        }
+        // scores of two times 16 keys: lane has keys 16 t + 4 grp + i of query col
+        f32x4 s[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            s[t] = f32x4{0, 0, 0, 0};
+            const uint32_t key = key0 + 16 * t + col;
+            const uint8_t *const kp = a.c.k + (key < n ? row_of(key) * kRow : 0) + (kInt8 ? 16 : 16) * grp;
+#pragma unroll
+            for (int i = 0; i < kChunks / 4; ++i) {
+                u32x4 w = {0, 0, 0, 0};
+                if (key < n) w = *reinterpret_cast<const u32x4 *>(kp + 64 * i);
+                if (kInt8) {
+                    s[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(bf16_of_bytes8(u32x2{w.x, w.y})), as_bf16x8(q[2 * i]), s[t], 0, 0, 0);
+                    s[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(bf16_of_bytes8(u32x2{w.z, w.w})), as_bf16x8(q[2 * i + 1]), s[t], 0, 0, 0);
+                } else {
+                    s[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(w), as_bf16x8(q[i]), s[t], 0, 0, 0);
+                }
+            }
+        }
+        float vs[2][4];
+        float top = -__builtin_inff();
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const uint32_t key = key0 + 16 * t + 4 * grp;      // four keys of one page
+            f32x4 ks = {1, 1, 1, 1}, vv = {1, 1, 1, 1};
+            if (kInt8 && key < n) {
+                const int64_t r = row_of(key);
+                ks = *reinterpret_cast<const f32x4 *>(a.c.k_scale + r);
+                vv = *reinterpret_cast<const f32x4 *>(a.c.v_scale + r);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                s[t][i] = key + i < n ? s[t][i] * (a.log2_scale * ks[i]) : -__builtin_inff();
+                vs[t][i] = key + i < n ? vv[i] : 0.0f;
+                top = fmaxf(top, s[t][i]);
+            }
+        }
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float next = fmaxf(m, top);
+        const float base = next == -__builtin_inff() ? 0.0f : next;
+        const float keep = exp2_fast(m - base);
+        m = next;
+        l *= keep;
+#pragma unroll
+        for (int i = 0; i < kDTiles; ++i) o[i] *= keep;
+        // weights as the sum of two BF16 operands, for the product has matrix
+        // rate to spare: rounded once they would add as much error as the
+        // rounding of the result (0.0027 of the norm against 0.0017)
+        u32x4 p, p_low;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            float e[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                e[i] = exp2_fast(s[t][i] - base);
+                l += e[i];
+                if (kInt8) e[i] *= vs[t][i];
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t w = pack_bf16(e[2 * i], e[2 * i + 1]);
+                p[2 * t + i] = w;
+                p_low[2 * t + i] = pack_bf16(e[2 * i] - __uint_as_float(w << 16), e[2 * i + 1] - __uint_as_float(w & 0xFFFF0000u));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kDTiles; ++i) {
+            u32x4 w;
+            if (kInt8) {
+                // 8 rows x 16 bytes a transposing read: rows of the lane's slots are
+                // 4 grp + 0..3 and 16 + 4 grp + 0..3
+                const uint32_t j = lane & 15u, r = j >> 1;
+                const uint32_t row = (r < 4 ? 0 : 12) + 4 * grp + r;
+                const i32x2 b = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+                    (DF11_LDS i32x2 *)(vt + v_at<kRow>(row, i) + 8 * (j & 1)));
+                w = bf16_of_bytes8(u32x2{(uint32_t)b.x, (uint32_t)b.y});
+            } else {
+                const uint32_t j = lane & 15u, row = 4 * grp + (j >> 2), chunk = 2 * i + ((j & 3) >> 1);
+                const s16x4 b0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((DF11_LDS s16x4 *)(vt + v_at<kRow>(row, chunk) + 8 * (j & 1)));
+                const s16x4 b1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((DF11_LDS s16x4 *)(vt + v_at<kRow>(row + 16, chunk) + 8 * (j & 1)));
+                const u32x2 w0 = __builtin_bit_cast(u32x2, b0), w1 = __builtin_bit_cast(u32x2, b1);
+                w = u32x4{w0.x, w0.y, w1.x, w1.y};
+            }
+            o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(w), as_bf16x8(p), o[i], 0, 0, 0);
+            o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(w), as_bf16x8(p_low), o[i], 0, 0, 0);
+        }
+    }
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+
+    // join the waves
+    if (lane < 16) {
+        ml[wave][0][lane] = m;
+        ml[wave][1][lane] = l;
+    }
+    __syncthreads();                                   // (also: every wave is done with its V tile)
+    float *const parts = reinterpret_cast<float *>(lds);
+    float most = -__builtin_inff();
+#pragma unroll
+    for (int w = 0; w < (int)kTokenWaves; ++w) most = fmaxf(most, ml[w][0][col]);
+    const float base = most == -__builtin_inff() ? 0.0f : most;
+    const float weight = exp2_fast(m - base);
+#pragma unroll
+    for (int i = 0; i < kDTiles; ++i)
+        *reinterpret_cast<f32x4 *>(parts + (wave * 16 + col) * kOStride + 16 * i + 4 * grp) = o[i] * weight;
+    __syncthreads();
+    const uint32_t heads_here = min(16u, a.group - q_tile * 16);
+    for (uint32_t at = threadIdx.x; at < heads_here * (D / 4); at += kThreads) {
+        const uint32_t c = at / (D / 4), d = at % (D / 4) * 4;
+        f32x4 sum = {0, 0, 0, 0};
+        float most_c = -__builtin_inff(), l_c = 0;
+#pragma unroll
+        for (int w = 0; w < (int)kTokenWaves; ++w) most_c = fmaxf(most_c, ml[w][0][c]);
+        const float base_c = most_c == -__builtin_inff() ? 0.0f : most_c;
+#pragma unroll
+        for (int w = 0; w < (int)kTokenWaves; ++w) {
+            sum += *reinterpret_cast<const f32x4 *>(parts + (w * 16 + c) * kOStride + d);
+            l_c += ml[w][1][c] * exp2_fast(ml[w][0][c] - base_c);
+        }
+        const uint32_t h = kv_head * a.group + q_tile * 16 + c;
+        if (a.splits == 1) {
+            const float inv = l_c == 0.0f ? 0.0f : 1.0f / l_c;
+            *reinterpret_cast<u32x2 *>(a.out.data + seq * a.out.row + h * a.out.head + d) =
+                u32x2{pack_bf16(sum.x * inv, sum.y * inv), pack_bf16(sum.z * inv, sum.w * inv)};
+        } else {
+            const uint64_t at_part = ((uint64_t)seq * a.heads + h) * a.splits + split;
+            *reinterpret_cast<f32x4 *>(a.part + at_part * D + d) = sum;
+            if (d == 0) *reinterpret_cast<f32x2 *>(a.part_ml + 2 * at_part) = f32x2{most_c, l_c};
+        }
+    }
+}
+
+// Joins the parts of one query head: out = sum_a w_a o_a / sum_a w_a l_a with
+// w_a = 2^(m_a - max m).
+template <int D>
+__global__ __launch_bounds__(256) void join_token_kernel(TokenArgs a) {
+    __shared__ float sums[4][D];
+    __shared__ float ls[4];
+    const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t seq = blockIdx.x / a.heads, h = blockIdx.x % a.heads;
+    const uint32_t len = (uint32_t)min((int64_t)max(a.lens[seq], 0), (int64_t)a.t.width << a.c.shift);
+    const uint32_t n = max(1u, (len + a.range - 1) / a.range);     // parts that were written
+    const uint64_t first = (uint64_t)blockIdx.x * a.splits;
+    const f32x2 *const ml = reinterpret_cast<const f32x2 *>(a.part_ml) + first;
+    float most = -__builtin_inff();
+    for (uint32_t i = lane; i < n; i += 64) most = fmaxf(most, ml[i].x);
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) most = fmaxf(most, __shfl_xor(most, d));
+    const float base = most == -__builtin_inff() ? 0.0f : most;
+    float sum[D / 64] = {}, l = 0;
+#pragma unroll 4
+    for (uint32_t i = wave; i < n; i += 4) {
+        const float w = exp2_fast(ml[i].x - base);
+        l += w * ml[i].y;
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) sum[j] += w * a.part[(first + i) * D + (D / 64) * lane + j];
+    }
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j) sums[wave][(D / 64) * lane + j] = sum[j];
+    if (lane == 0) ls[wave] = l;
+    __syncthreads();
+    if (threadIdx.x < D / 2) {
+        const float total = ls[0] + ls[1] + ls[2] + ls[3];
+        const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+        const uint32_t d = 2 * threadIdx.x;
+        const float x = sums[0][d] + sums[1][d] + sums[2][d] + sums[3][d];
+        const float y = sums[0][d + 1] + sums[1][d + 1] + sums[2][d + 1] + sums[3][d + 1];
+        *reinterpret_cast<uint32_t *>(a.out.data + seq * a.out.row + h * a.out.head + d) = pack_bf16(x * inv, y * inv);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_attend_token(const TokenArgs &a, uint32_t head_dim, bool int8, hipStream_t stream) {
+    const dim3 grid(a.n_seqs * a.c.kv_heads * a.q_tiles, a.splits);
+    const auto kernel = head_dim == 64 ? (int8 ? attend_token_kernel<64, true> : attend_token_kernel<64, false>)
+                                       : (int8 ? attend_token_kernel<128, true> : attend_token_kernel<128, false>);
+    hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.splits == 1) return e;
+    hipLaunchKernelGGL(head_dim == 64 ? join_token_kernel<64> : join_token_kernel<128>, dim3(a.n_seqs * a.heads), dim3(256), 0,
+                       stream, a);
+    return hipGetLastError();
+}
+
+}  // namespace df11

@@ -1,0 +1,162 @@
+// The paged key-value cache for gfx950: tokens' keys and values written into
+// the cache's pages, as BF16 words or quantised to 8 bits on the way, and
+// sequences read back as packed BF16 rows.
+//
+// 8 bits: for each token and head, a = max |x| (at least 2^-100), scale =
+// a / 127, codes rint(x * (127 / a)): |x| <= a gives |code| <= 127 without a
+// clamp (a * fl(127 / a) is within 2^-23 of 127), and two correctly rounded
+// divisions a row.  The maximum is taken over the words' magnitude bits as
+// integers, where NaN is above infinity: a row that holds either gets a scale
+// of NaN or infinity and codes 0, and reads back as NaN.
+//
+// Both kernels are bound by HBM traffic: a lane moves 16 bytes of BF16 a step
+// (a row of 128 is 16 lanes), several steps in flight.
+#include "serve_device.hpp"
+#include "serve_internal.hpp"
+
+namespace df11 {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kUnroll = 4;
+constexpr uint32_t kReadShift = 6;    // 64 tokens of one head a workgroup
+
+// Maximum over the kLanes neighbouring lanes that hold a row, in each of them.
+template <int kLanes>
+__device__ __forceinline__ uint32_t row_max(uint32_t x) {
+    x = max(x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0xB1, 0xF, 0xF, true));    // lanes xor 1
+    x = max(x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x4E, 0xF, 0xF, true));    // lanes xor 2
+    x = max(x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x141, 0xF, 0xF, true));   // mirrored in 8
+    if (kLanes == 16) x = max(x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x140, 0xF, 0xF, true));   // in 16
+    return x;
+}
+
+__device__ __forceinline__ float low(uint32_t w) { return __builtin_bit_cast(float, w << 16); }
+__device__ __forceinline__ float high(uint32_t w) { return __builtin_bit_cast(float, w & 0xFFFF0000u); }
+
+// Two codes from two words, as the low bytes of a dword.
+__device__ __forceinline__ uint32_t codes2(uint32_t w, float inv) {
+    const int a = (int)__builtin_rintf(low(w) * inv), b = (int)__builtin_rintf(high(w) * inv);
+    return (uint32_t)(a & 255) | (uint32_t)(b & 255) << 8;
+}
+
+template <int D, bool kInt8>
+__global__ __launch_bounds__(kThreads) void kv_write_kernel(WriteArgs a) {
+    constexpr uint32_t kLanes = D / 8;
+    const bool is_v = blockIdx.y != 0;
+    const Rows &x = is_v ? a.v : a.k;
+    uint8_t *const store = is_v ? a.c.v : a.c.k;
+    float *const scales = is_v ? a.c.v_scale : a.c.k_scale;
+    const uint64_t n_units = (uint64_t)a.n_tokens * a.c.kv_heads * kLanes;
+    const uint64_t first = (uint64_t)blockIdx.x * (kThreads * kUnroll) + threadIdx.x;
+    u32x4 w[kUnroll];
+    int64_t slot[kUnroll];
+    uint32_t head[kUnroll];
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+        const uint64_t unit = first + (uint64_t)i * kThreads;
+        slot[i] = -1;
+        if (unit < n_units) {
+            const uint32_t r = (uint32_t)(unit / kLanes);
+            const uint32_t token = r / a.c.kv_heads;
+            head[i] = r - token * a.c.kv_heads;
+            slot[i] = a.slots[token];
+            w[i] = *reinterpret_cast<const u32x4 *>(x.data + token * x.row + head[i] * x.head + (unit % kLanes) * 8);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+        const uint32_t part = threadIdx.x % kLanes;
+        uint32_t m = 0;
+        if (kInt8) {
+            if (slot[i] >= 0) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) m = max(m, max(w[i][j] << 16 & 0x7FFF0000u, w[i][j] & 0x7FFF0000u));
+            }
+            m = row_max<kLanes>(m);
+        }
+        if (slot[i] < 0 || slot[i] >= a.c.n_slots) continue;   // (a row's lanes go together)
+        const int64_t page = slot[i] >> a.c.shift, pos = slot[i] & ((1 << a.c.shift) - 1);
+        const int64_t row = ((page * a.c.kv_heads + head[i]) << a.c.shift) + pos;
+        if (kInt8) {
+            const float top = __builtin_bit_cast(float, m > 0x0D800000u ? m : 0x0D800000u);   // 2^-100
+            const float inv = 127.0f / top;
+            u32x2 c;
+            c.x = codes2(w[i].x, inv) | codes2(w[i].y, inv) << 16;
+            c.y = codes2(w[i].z, inv) | codes2(w[i].w, inv) << 16;
+            *reinterpret_cast<u32x2 *>(store + row * D + 8 * part) = c;
+            if (part == 0) scales[row] = top / 127.0f;
+        } else {
+            *reinterpret_cast<u32x4 *>(store + 2 * (row * D + 8 * part)) = w[i];
+        }
+    }
+}
+
+template <int D, bool kInt8>
+__global__ __launch_bounds__(kThreads) void kv_read_kernel(ReadArgs a) {
+    constexpr uint32_t kLanes = D / 8;
+    constexpr int kSteps = (1 << kReadShift) * kLanes / kThreads;
+    uint32_t tile;
+    const uint32_t s = sequence_of_slot(a.starts, a.n_seqs, blockIdx.x, kReadShift, &tile);
+    const int32_t begin = a.starts[s], end = a.starts[s + 1];
+    if (begin < 0 || end < begin || (uint32_t)end > a.n_tokens) return;
+    const uint32_t n = min((uint32_t)(end - begin), a.t.width << a.c.shift);
+    if (tile > (n >> kReadShift)) return;
+    const bool is_v = blockIdx.z != 0;
+    const Rows &x = is_v ? a.v : a.k;
+    const uint8_t *const store = is_v ? a.c.v : a.c.k;
+    const float *const scales = is_v ? a.c.v_scale : a.c.k_scale;
+    const uint32_t head = blockIdx.y, part = threadIdx.x % kLanes;
+    const int32_t *const table = a.t.pages + s * a.t.stride;
+    u32x4 w[kSteps];
+    u32x2 c[kSteps];
+    float scale[kSteps];
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+        const uint32_t pos = (tile << kReadShift) + (threadIdx.x + i * kThreads) / kLanes;
+        if (pos >= n) continue;
+        const uint32_t page = min((uint32_t)table[pos >> a.c.shift], a.c.n_pages - 1);
+        const int64_t row = (((int64_t)page * a.c.kv_heads + head) << a.c.shift) + (pos & ((1u << a.c.shift) - 1));
+        if (kInt8) {
+            c[i] = *reinterpret_cast<const u32x2 *>(store + row * D + 8 * part);
+            scale[i] = scales[row];
+        } else {
+            w[i] = *reinterpret_cast<const u32x4 *>(store + 2 * (row * D + 8 * part));
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+        const uint32_t pos = (tile << kReadShift) + (threadIdx.x + i * kThreads) / kLanes;
+        if (pos >= n) continue;
+        if (kInt8) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t two = c[i][j / 2] >> (16 * (j % 2));
+                w[i][j] = pack_bf16((float)(int8_t)two * scale[i], (float)(int8_t)(two >> 8) * scale[i]);
+            }
+        }
+        *reinterpret_cast<u32x4 *>(x.data + (int64_t)(begin + pos) * x.row + head * x.head + 8 * part) = w[i];
+    }
+}
+
+}  // namespace
+
+hipError_t launch_kv_write(const WriteArgs &a, uint32_t head_dim, bool int8, hipStream_t stream) {
+    const uint64_t units = (uint64_t)a.n_tokens * a.c.kv_heads * (head_dim / 8);
+    const dim3 grid((uint32_t)((units + kThreads * kUnroll - 1) / (kThreads * kUnroll)), 2);
+    const auto kernel = head_dim == 64 ? (int8 ? kv_write_kernel<64, true> : kv_write_kernel<64, false>)
+                                       : (int8 ? kv_write_kernel<128, true> : kv_write_kernel<128, false>);
+    hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_kv_read(const ReadArgs &a, uint32_t head_dim, bool int8, hipStream_t stream) {
+    const dim3 grid((a.n_tokens >> kReadShift) + a.n_seqs, a.c.kv_heads, 2);
+    const auto kernel = head_dim == 64 ? (int8 ? kv_read_kernel<64, true> : kv_read_kernel<64, false>)
+                                       : (int8 ? kv_read_kernel<128, true> : kv_read_kernel<128, false>);
+    hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, a);
+    return hipGetLastError();
+}
+
+}  // namespace df11

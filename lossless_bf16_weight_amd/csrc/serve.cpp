@@ -1,0 +1,292 @@
+// Host side of the serving operators (key-value cache and attention, C ABI in
+// include/df11.h): argument checks, the split of the work, launches.
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+
+#include "serve_internal.hpp"
+
+using namespace df11;
+
+namespace {
+
+constexpr uint64_t kMostGroups = uint64_t(1) << 24;   // workgroups along x: threads stay below 2^32
+constexpr int64_t kMostStride = int64_t(1) << 32;
+
+struct Device {
+    int prev = -1;
+    hipError_t err = hipSuccess;
+    explicit Device(int dev) {
+        if (hipGetDevice(&prev) != hipSuccess) prev = -1;
+        if (prev != dev) err = hipSetDevice(dev);
+        else prev = -1;
+    }
+    ~Device() {
+        if (prev >= 0) (void)hipSetDevice(prev);
+    }
+};
+
+// Compute units of a device (256 where it cannot be asked: the split of the
+// work follows it, no result does).
+uint32_t compute_units(int dev) {
+    static std::atomic<int> known[64];
+    if (dev < 0 || dev >= 64) return 256;
+    int n = known[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0) {
+            (void)hipGetLastError();
+            return 256;
+        }
+        known[dev].store(n, std::memory_order_relaxed);
+    }
+    return (uint32_t)n;
+}
+
+uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
+
+bool misaligned(const void *p) { return ((uintptr_t)p & 15) != 0; }
+
+df11_status check_rows(const char *what, const df11_rows &r, uint64_t n, uint64_t heads, uint64_t d, bool written) {
+    if (n == 0) return DF11_OK;
+    if (!r.data || misaligned(r.data)) return report_error(DF11_E_ARG, "%s: NULL or not 16-byte aligned", what);
+    if (r.row_stride < 0 || r.head_stride < 0 || r.row_stride >= kMostStride || r.head_stride >= kMostStride ||
+        (r.row_stride | r.head_stride) & 7)
+        return report_error(DF11_E_ARG, "%s: strides must be multiples of 8 from 0 to below 2^32", what);
+    if (!written) return DF11_OK;
+    const uint64_t row = n > 1 ? (uint64_t)r.row_stride : ~uint64_t(0), head = heads > 1 ? (uint64_t)r.head_stride : ~uint64_t(0);
+    const bool heads_inside = head >= d && row >= (heads > 1 ? (heads - 1) * head : 0) + d;
+    const bool rows_inside = row >= d && head >= (n > 1 ? (n - 1) * row : 0) + d;
+    if (!heads_inside && !rows_inside) return report_error(DF11_E_ARG, "%s: rows that are written overlap", what);
+    return DF11_OK;
+}
+
+Rows rows_of(const df11_rows &r) { return Rows{(uint16_t *)r.data, r.row_stride, r.head_stride}; }
+
+df11_status check_cache_sizes(const df11_kv_cache &c) {
+    if (c.store > DF11_KV_INT8) return report_error(DF11_E_ARG, "cache: store %u", c.store);
+    if (c.head_dim != 64 && c.head_dim != 128) return report_error(DF11_E_UNSUPPORTED, "cache: head_dim %u, 64 and 128 are built", c.head_dim);
+    if (c.page_size < 16 || c.page_size > 1024 || (c.page_size & (c.page_size - 1)))
+        return report_error(DF11_E_ARG, "cache: page_size %u, a power of two from 16 to 1024 is needed", c.page_size);
+    if (c.n_pages == 0 || c.n_pages > 0x7FFFFFFFu || c.n_kv_heads == 0 || c.n_kv_heads > 65535)
+        return report_error(DF11_E_ARG, "cache: %u pages, %u kv heads", c.n_pages, c.n_kv_heads);
+    return DF11_OK;
+}
+
+df11_status check_cache(const df11_kv_cache &c) {
+    df11_status st = check_cache_sizes(c);
+    if (st) return st;
+    if (!c.k || !c.v || misaligned(c.k) || misaligned(c.v)) return report_error(DF11_E_ARG, "cache: pages NULL or not 16-byte aligned");
+    if (c.store == DF11_KV_INT8 && (!c.k_scale || !c.v_scale || misaligned(c.k_scale) || misaligned(c.v_scale)))
+        return report_error(DF11_E_ARG, "cache: scales NULL or not 16-byte aligned");
+    return DF11_OK;
+}
+
+CacheView view_of(const df11_kv_cache &c) {
+    const uint32_t shift = (uint32_t)__builtin_ctz(c.page_size);
+    return CacheView{(uint8_t *)c.k, (uint8_t *)c.v, c.k_scale, c.v_scale, (int64_t)c.n_pages << shift, c.n_pages, shift, c.n_kv_heads};
+}
+
+df11_status check_table(const df11_page_table &t, const df11_kv_cache &c) {
+    if (!t.pages || ((uintptr_t)t.pages & 3)) return report_error(DF11_E_ARG, "page table: NULL or misaligned");
+    if (t.row_stride < 0) return report_error(DF11_E_ARG, "page table: negative stride");
+    if (t.width == 0) return report_error(DF11_E_ARG, "page table: no entries");
+    if ((uint64_t)t.width * c.page_size > (uint64_t(1) << 28))
+        return report_error(DF11_E_UNSUPPORTED, "page table: more than 2^28 positions a sequence");
+    return DF11_OK;
+}
+
+Tables tables_of(const df11_page_table &t) { return Tables{t.pages, t.row_stride, t.width}; }
+
+bool bad_index(const void *p, size_t size) { return !p || ((uintptr_t)p & (size - 1)); }
+
+df11_status launched(hipError_t e, const char *what) {
+    return e == hipSuccess ? DF11_OK : report_error(DF11_E_HIP, "%s launch: %s", what, hipGetErrorString(e));
+}
+
+float log2_scale(float scale) { return (float)((double)scale * 1.4426950408889634074); }
+
+// How attend_token splits: keys a workgroup takes and workgroups along a
+// sequence.  Four workgroups a compute unit keep enough bytes in flight;
+// longer ranges leave fewer parts to join.
+struct TokenSplit {
+    uint32_t q_tiles, range, splits;
+};
+
+TokenSplit token_split(const df11_attend_token_args &a, int dev) {
+    TokenSplit s;
+    const uint64_t most = (uint64_t)a.table.width * a.cache.page_size;
+    s.q_tiles = (uint32_t)ceil_div(a.n_heads / a.cache.n_kv_heads, 16);
+    const uint64_t units = (uint64_t)a.n_seqs * a.cache.n_kv_heads * s.q_tiles;
+    const uint64_t step = std::max(kTokenKeys * kTokenWaves, a.cache.page_size);
+    const uint64_t want = std::max<uint64_t>(1, 4 * compute_units(dev) / std::max<uint64_t>(units, 1));
+    const uint64_t range = ceil_div(ceil_div(most, want), step) * step;
+    s.range = (uint32_t)std::min<uint64_t>(std::max<uint64_t>(range, 2 * step), kTokenRangeMax);
+    s.splits = (uint32_t)ceil_div(most, s.range);
+    return s;
+}
+
+uint64_t token_bytes(const df11_attend_token_args &a, const TokenSplit &s) {
+    return s.splits == 1 ? 0 : (uint64_t)a.n_seqs * a.n_heads * s.splits * (a.cache.head_dim + 2) * sizeof(float);
+}
+
+df11_status check_token_sizes(const df11_attend_token_args &a) {
+    df11_status st = check_cache_sizes(a.cache);
+    if (st) return st;
+    if (a.n_heads == 0 || a.n_heads % a.cache.n_kv_heads) return report_error(DF11_E_ARG, "%u heads over %u kv heads", a.n_heads, a.cache.n_kv_heads);
+    if ((uint64_t)a.n_seqs * a.n_heads > kMostGroups) return report_error(DF11_E_UNSUPPORTED, "%u sequences of %u heads", a.n_seqs, a.n_heads);
+    return DF11_OK;
+}
+
+// How attend_prompt splits the keys: few tiles of query rows (a piece of a
+// prompt behind a long prefix) leave compute units idle otherwise.
+uint32_t prompt_tile_slots(const df11_attend_prompt_args &a) { return (uint32_t)(a.n_q / kPromptTile + a.n_seqs); }
+
+uint32_t prompt_splits(const df11_attend_prompt_args &a, int dev) {
+    if (a.n_q == 0 || a.n_seqs == 0) return 1;
+    const uint64_t tiles = ceil_div(a.n_q, kPromptTile) * a.n_heads, keys = a.n_k / a.n_seqs;
+    const uint64_t want = 2 * compute_units(dev) / std::max<uint64_t>(tiles, 1);
+    return (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>({want, keys / 512, 32}));
+}
+
+uint64_t prompt_bytes(const df11_attend_prompt_args &a, uint32_t splits) {
+    return splits == 1 ? 0 : (uint64_t)splits * a.n_q * a.n_heads * (a.head_dim + 2) * sizeof(float);
+}
+
+df11_status check_prompt_sizes(const df11_attend_prompt_args &a) {
+    if (a.head_dim != 64 && a.head_dim != 128) return report_error(DF11_E_UNSUPPORTED, "head_dim %u, 64 and 128 are built", a.head_dim);
+    if (a.n_kv_heads == 0 || a.n_heads == 0 || a.n_heads % a.n_kv_heads) return report_error(DF11_E_ARG, "%u heads over %u kv heads", a.n_heads, a.n_kv_heads);
+    if (a.n_q > 0x7FFFFFFFu || a.n_k > 0x7FFFFFFFu) return report_error(DF11_E_UNSUPPORTED, "2^31 rows or more");
+    if (((uint64_t)a.n_q / kPromptTile + a.n_seqs) * a.n_heads > kMostGroups) return report_error(DF11_E_UNSUPPORTED, "%llu rows of %u heads", (unsigned long long)a.n_q, a.n_heads);
+    return DF11_OK;
+}
+
+df11_status check_workspace(const void *p, uint64_t have, uint64_t need) {
+    if (need == 0) return DF11_OK;
+    if (!p || misaligned(p)) return report_error(DF11_E_ARG, "workspace: NULL or not 16-byte aligned");
+    if (have < need) return report_error(DF11_E_ARG, "workspace: %llu bytes, %llu needed", (unsigned long long)have, (unsigned long long)need);
+    return DF11_OK;
+}
+
+df11_status check_scale(float s) {
+    return std::isfinite(s) && s > 0 ? DF11_OK : report_error(DF11_E_ARG, "scale: a finite number above 0 is needed");
+}
+
+}  // namespace
+
+#define TRY(expr)                    \
+    do {                             \
+        df11_status st_ = (expr);    \
+        if (st_) return st_;         \
+    } while (0)
+
+#define ON_DEVICE(dev)                                                                                     \
+    Device guard(dev);                                                                                     \
+    if (guard.err != hipSuccess) return report_error(DF11_E_HIP, "hipSetDevice(%d): %s", dev, hipGetErrorString(guard.err))
+
+extern "C" df11_status df11_kv_write(const df11_kv_write_args *a, int hip_device, hipStream_t stream) {
+    if (!a) return report_error(DF11_E_ARG, "kv_write: NULL arguments");
+    TRY(check_cache(a->cache));
+    const uint32_t d = a->cache.head_dim, heads = a->cache.n_kv_heads;
+    if (a->n_tokens > (uint64_t(1) << 30) / heads) return report_error(DF11_E_UNSUPPORTED, "kv_write: %llu tokens", (unsigned long long)a->n_tokens);
+    TRY(check_rows("k", a->k, a->n_tokens, heads, d, false));
+    TRY(check_rows("v", a->v, a->n_tokens, heads, d, false));
+    if (a->n_tokens == 0) return DF11_OK;
+    if (bad_index(a->slots, 8)) return report_error(DF11_E_ARG, "kv_write: slots NULL or misaligned");
+    ON_DEVICE(hip_device);
+    const WriteArgs w{view_of(a->cache), rows_of(a->k), rows_of(a->v), a->slots, (uint32_t)a->n_tokens};
+    return launched(launch_kv_write(w, d, a->cache.store == DF11_KV_INT8, stream), "kv_write");
+}
+
+extern "C" df11_status df11_kv_read(const df11_kv_read_args *a, int hip_device, hipStream_t stream) {
+    if (!a) return report_error(DF11_E_ARG, "kv_read: NULL arguments");
+    TRY(check_cache(a->cache));
+    const uint32_t d = a->cache.head_dim, heads = a->cache.n_kv_heads;
+    if (a->n_tokens > 0x7FFFFFFFu || a->n_tokens / 64 + a->n_seqs > kMostGroups)
+        return report_error(DF11_E_UNSUPPORTED, "kv_read: %llu tokens of %u sequences", (unsigned long long)a->n_tokens, a->n_seqs);
+    TRY(check_rows("k", a->k, a->n_tokens, heads, d, true));
+    TRY(check_rows("v", a->v, a->n_tokens, heads, d, true));
+    if (a->n_tokens == 0 || a->n_seqs == 0) return DF11_OK;
+    TRY(check_table(a->table, a->cache));
+    if (bad_index(a->starts, 4)) return report_error(DF11_E_ARG, "kv_read: starts NULL or misaligned");
+    ON_DEVICE(hip_device);
+    const ReadArgs r{view_of(a->cache), tables_of(a->table), rows_of(a->k), rows_of(a->v), a->starts, a->n_seqs, (uint32_t)a->n_tokens};
+    return launched(launch_kv_read(r, d, a->cache.store == DF11_KV_INT8, stream), "kv_read");
+}
+
+extern "C" uint64_t df11_attend_token_workspace(const df11_attend_token_args *a, int hip_device) {
+    if (!a || a->n_seqs == 0 || check_token_sizes(*a) || a->table.width == 0) return 0;
+    return token_bytes(*a, token_split(*a, hip_device));
+}
+
+extern "C" df11_status df11_attend_token(const df11_attend_token_args *a, int hip_device, hipStream_t stream) {
+    if (!a) return report_error(DF11_E_ARG, "attend_token: NULL arguments");
+    TRY(check_token_sizes(*a));
+    TRY(check_cache(a->cache));
+    TRY(check_scale(a->scale));
+    const uint32_t d = a->cache.head_dim;
+    TRY(check_rows("q", a->q, a->n_seqs, a->n_heads, d, false));
+    TRY(check_rows("out", a->out, a->n_seqs, a->n_heads, d, true));
+    if (a->n_seqs == 0) return DF11_OK;
+    TRY(check_table(a->table, a->cache));
+    if (bad_index(a->lens, 4)) return report_error(DF11_E_ARG, "attend_token: lens NULL or misaligned");
+    const TokenSplit s = token_split(*a, hip_device);
+    TRY(check_workspace(a->workspace, a->workspace_bytes, token_bytes(*a, s)));
+    ON_DEVICE(hip_device);
+    TokenArgs t{};
+    t.c = view_of(a->cache);
+    t.t = tables_of(a->table);
+    t.q = rows_of(a->q);
+    t.out = rows_of(a->out);
+    t.lens = a->lens;
+    t.log2_scale = log2_scale(a->scale);
+    t.n_seqs = a->n_seqs;
+    t.heads = a->n_heads;
+    t.group = a->n_heads / a->cache.n_kv_heads;
+    t.q_tiles = s.q_tiles;
+    t.range = s.range;
+    t.splits = s.splits;
+    t.part = (float *)a->workspace;
+    t.part_ml = t.part + (uint64_t)a->n_seqs * a->n_heads * s.splits * d;
+    return launched(launch_attend_token(t, d, a->cache.store == DF11_KV_INT8, stream), "attend_token");
+}
+
+extern "C" uint64_t df11_attend_prompt_workspace(const df11_attend_prompt_args *a, int hip_device) {
+    if (!a || check_prompt_sizes(*a)) return 0;
+    return prompt_bytes(*a, prompt_splits(*a, hip_device));
+}
+
+extern "C" df11_status df11_attend_prompt(const df11_attend_prompt_args *a, int hip_device, hipStream_t stream) {
+    if (!a) return report_error(DF11_E_ARG, "attend_prompt: NULL arguments");
+    TRY(check_prompt_sizes(*a));
+    TRY(check_scale(a->scale));
+    if (a->flags & ~DF11_ATTEND_CAUSAL) return report_error(DF11_E_ARG, "attend_prompt: flags %u", a->flags);
+    TRY(check_rows("q", a->q, a->n_q, a->n_heads, a->head_dim, false));
+    TRY(check_rows("k", a->k, a->n_k, a->n_kv_heads, a->head_dim, false));
+    TRY(check_rows("v", a->v, a->n_k, a->n_kv_heads, a->head_dim, false));
+    TRY(check_rows("out", a->out, a->n_q, a->n_heads, a->head_dim, true));
+    if (a->n_q == 0 || a->n_seqs == 0) return DF11_OK;
+    if (bad_index(a->q_starts, 4) || bad_index(a->k_starts, 4)) return report_error(DF11_E_ARG, "attend_prompt: starts NULL or misaligned");
+    const uint32_t splits = prompt_splits(*a, hip_device);
+    TRY(check_workspace(a->workspace, a->workspace_bytes, prompt_bytes(*a, splits)));
+    ON_DEVICE(hip_device);
+    PromptArgs p{};
+    p.q = rows_of(a->q);
+    p.k = rows_of(a->k);
+    p.v = rows_of(a->v);
+    p.out = rows_of(a->out);
+    p.q_starts = a->q_starts;
+    p.k_starts = a->k_starts;
+    p.log2_scale = log2_scale(a->scale);
+    p.n_seqs = a->n_seqs;
+    p.n_q = (uint32_t)a->n_q;
+    p.n_k = (uint32_t)a->n_k;
+    p.heads = a->n_heads;
+    p.kv_heads = a->n_kv_heads;
+    p.group = a->n_heads / a->n_kv_heads;
+    p.causal = a->flags & DF11_ATTEND_CAUSAL;
+    p.tile_slots = prompt_tile_slots(*a);
+    p.splits = splits;
+    p.part = (float *)a->workspace;
+    p.part_ml = p.part + (uint64_t)splits * a->n_q * a->n_heads * a->head_dim;
+    return launched(launch_attend_prompt(p, a->head_dim, stream), "attend_prompt");
+}

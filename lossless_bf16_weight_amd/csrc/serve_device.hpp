@@ -1,0 +1,70 @@
+// Device code that the serving kernels share: vector types, the matrix
+// instructions' operand types, BF16 packing, and the search of a tile's
+// sequence.
+#pragma once
+#include <hip/hip_runtime.h>
+
+namespace df11 {
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+#define DF11_LDS __attribute__((address_space(3)))
+
+__device__ __forceinline__ bf16x8 as_bf16x8(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
+
+// Two floats rounded to BF16 (nearest, ties to even), a in the low half.
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
+}
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// The four signed bytes of w as BF16 words (exact: |code| <= 128 has eight
+// significant bits, so the float's upper half is the whole value).
+__device__ __forceinline__ u32x2 bf16_of_bytes(uint32_t w) {
+    const uint32_t a = __builtin_bit_cast(uint32_t, (float)(int8_t)w);
+    const uint32_t b = __builtin_bit_cast(uint32_t, (float)(int8_t)(w >> 8));
+    const uint32_t c = __builtin_bit_cast(uint32_t, (float)(int8_t)(w >> 16));
+    const uint32_t d = __builtin_bit_cast(uint32_t, (float)(int8_t)(w >> 24));
+    return u32x2{__builtin_amdgcn_perm(b, a, 0x07060302u), __builtin_amdgcn_perm(d, c, 0x07060302u)};
+}
+
+__device__ __forceinline__ u32x4 bf16_of_bytes8(u32x2 w) {
+    const u32x2 lo = bf16_of_bytes(w.x), hi = bf16_of_bytes(w.y);
+    return u32x4{lo.x, lo.y, hi.x, hi.y};
+}
+
+// Tiles over packed sequences.  With tiles of 2^shift rows, sequence s is
+// given the tile slots from (starts[s] >> shift) + s up to the next
+// sequence's: at least as many as its tiles, and no prefix sum is needed.
+// Finds the sequence of slot t with a 64-way search (one load for up to 64
+// sequences); the same in every lane of the wave.  Returns the slot's tile
+// number within the sequence through *tile.
+__device__ __forceinline__ uint32_t sequence_of_slot(const int32_t *starts, uint32_t n_seqs, uint32_t t,
+                                                     uint32_t shift, uint32_t *tile) {
+    const uint32_t lane = threadIdx.x & 63u;
+    uint32_t lo = 0, n = n_seqs;
+    while (n > 1) {
+        const uint32_t step = (n + 63u) >> 6;
+        const uint32_t at = lane * step;
+        bool below = false;
+        if (at < n) below = ((uint32_t)starts[lo + at] >> shift) + lo + at <= t;
+        const uint32_t c = (uint32_t)__builtin_popcountll(__ballot(below));
+        const uint32_t skip = (c ? c - 1 : 0) * step;
+        lo += skip;
+        n = n - skip < step ? n - skip : step;
+    }
+    lo = __builtin_amdgcn_readfirstlane(lo);
+    *tile = t - (((uint32_t)starts[lo] >> shift) + lo);
+    return lo;
+}
+
+}  // namespace df11
