@@ -43,7 +43,8 @@ template <int D, bool kInt8>
 __global__ __launch_bounds__(kThreads) void attend_token_kernel(TokenArgs a) {
     constexpr int kRow = kInt8 ? D : 2 * D;            // bytes of a stored row
     constexpr int kChunks = kRow / 16;                 // 16-byte chunks of it
-    constexpr int kTileChunks = kTokenKeys * kChunks / 64;   // chunks a lane moves for 32 rows
+    constexpr int kVLoads = kTokenKeys * kChunks / 64;   // chunks a lane loads of a step's V rows
+    constexpr int kKLoads = kChunks / 4;               // and of each half of its K rows
     constexpr int kDTiles = D / 16;
     constexpr int kOStride = D + 4;
     constexpr uint32_t kVBytes = kTokenKeys * kRow;
@@ -96,27 +97,63 @@ __global__ __launch_bounds__(kThreads) void attend_token_kernel(TokenArgs a) {
     float m = -__builtin_inff(), l = 0;
     uint8_t *const vt = lds + wave * kVBytes;
 
-    for (uint32_t key0 = wave * kTokenKeys; key0 < n; key0 += kTokenWaves * kTokenKeys) {
-        // V rows of the step into this wave's tile; rows past the end are zero
-        // (their weights are 0, and 0 times a stray infinity would be NaN)
+    // A step's 32 rows of K and V, held in registers from one step before:
+    // the loads of the next step are in flight while this one is computed.
+    // Rows past the end repeat the last one (their scores are masked; their V
+    // rows are cleared below).
+    u32x4 kw[2][kKLoads], vw[kVLoads];
+    f32x4 ks[2], vs[2];
+    const auto load_v = [&](uint32_t key0) {
 #pragma unroll
-        for (int i = 0; i < kTileChunks; ++i) {
+        for (int i = 0; i < kVLoads; ++i) {
             const uint32_t at = i * 64 + lane, row = at / kChunks, chunk = at % kChunks;
-            u32x4 w = {0, 0, 0, 0};
-            if (key0 + row < n) w = *reinterpret_cast<const u32x4 *>(a.c.v + row_of(key0 + row) * kRow + 16 * chunk);
-            *reinterpret_cast<u32x4 *>(vt + v_at<kRow>(row, chunk)) = w;
+            vw[i] = *reinterpret_cast<const u32x4 *>(a.c.v + row_of(min(key0 + row, n - 1)) * kRow + 16 * chunk);
         }
+    };
+    const auto load_k = [&](uint32_t key0) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const uint8_t *const kp = a.c.k + row_of(min(key0 + 16 * t + col, n - 1)) * kRow + 16 * grp;
+#pragma unroll
+            for (int i = 0; i < kKLoads; ++i) kw[t][i] = *reinterpret_cast<const u32x4 *>(kp + 64 * i);
+        }
+    };
+    const auto load_scales = [&](uint32_t key0) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {       // four keys of one page
+            const int64_t r = row_of(min(key0 + 16 * t + 4 * grp, n - 1) & ~3u);
+            ks[t] = *reinterpret_cast<const f32x4 *>(a.c.k_scale + r);
+            vs[t] = *reinterpret_cast<const f32x4 *>(a.c.v_scale + r);
+        }
+    };
+    uint32_t key0 = wave * kTokenKeys;
+    if (key0 < n) {
+        load_v(key0);
+        load_k(key0);
+        if (kInt8) load_scales(key0);
+    }
+    for (; key0 < n; key0 += kTokenWaves * kTokenKeys) {
+        const uint32_t next_key = min(key0 + kTokenWaves * kTokenKeys, n - 1);   // (past the end: loads that nobody uses)
+        if (key0 + kTokenKeys > n) {
+            // weights of rows past the end are 0, and 0 times an infinity would be NaN
+#pragma unroll
+            for (int i = 0; i < kVLoads; ++i)
+                if (key0 + (i * 64 + lane) / kChunks >= n) vw[i] = u32x4{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int i = 0; i < kVLoads; ++i) {
+            const uint32_t at = i * 64 + lane;
+            *reinterpret_cast<u32x4 *>(vt + v_at<kRow>(at / kChunks, at % kChunks)) = vw[i];
+        }
+        load_v(next_key);
         // scores of two times 16 keys: lane has keys 16 t + 4 grp + i of query col
         f32x4 s[2];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             s[t] = f32x4{0, 0, 0, 0};
-            const uint32_t key = key0 + 16 * t + col;
-            const uint8_t *const kp = a.c.k + (key < n ? row_of(key) * kRow : 0) + (kInt8 ? 16 : 16) * grp;
 #pragma unroll
-            for (int i = 0; i < kChunks / 4; ++i) {
-                u32x4 w = {0, 0, 0, 0};
-                if (key < n) w = *reinterpret_cast<const u32x4 *>(kp + 64 * i);
+            for (int i = 0; i < kKLoads; ++i) {
+                const u32x4 w = kw[t][i];
                 if (kInt8) {
                     s[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(bf16_of_bytes8(u32x2{w.x, w.y})), as_bf16x8(q[2 * i]), s[t], 0, 0, 0);
                     s[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(bf16_of_bytes8(u32x2{w.z, w.w})), as_bf16x8(q[2 * i + 1]), s[t], 0, 0, 0);
@@ -125,24 +162,20 @@ __global__ __launch_bounds__(kThreads) void attend_token_kernel(TokenArgs a) {
                 }
             }
         }
-        float vs[2][4];
+        f32x4 v_scale[2];
         float top = -__builtin_inff();
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            const uint32_t key = key0 + 16 * t + 4 * grp;      // four keys of one page
-            f32x4 ks = {1, 1, 1, 1}, vv = {1, 1, 1, 1};
-            if (kInt8 && key < n) {
-                const int64_t r = row_of(key);
-                ks = *reinterpret_cast<const f32x4 *>(a.c.k_scale + r);
-                vv = *reinterpret_cast<const f32x4 *>(a.c.v_scale + r);
-            }
+            const uint32_t key = key0 + 16 * t + 4 * grp;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                s[t][i] = key + i < n ? s[t][i] * (a.log2_scale * ks[i]) : -__builtin_inff();
-                vs[t][i] = key + i < n ? vv[i] : 0.0f;
+                s[t][i] = key + i < n ? s[t][i] * (kInt8 ? a.log2_scale * ks[t][i] : a.log2_scale) : -__builtin_inff();
+                if (kInt8) v_scale[t][i] = key + i < n ? vs[t][i] : 0.0f;
                 top = fmaxf(top, s[t][i]);
             }
         }
+        load_k(next_key);
+        if (kInt8) load_scales(next_key);
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
         const float next = fmaxf(m, top);
@@ -163,7 +196,7 @@ __global__ __launch_bounds__(kThreads) void attend_token_kernel(TokenArgs a) {
             for (int i = 0; i < 4; ++i) {
                 e[i] = exp2_fast(s[t][i] - base);
                 l += e[i];
-                if (kInt8) e[i] *= vs[t][i];
+                if (kInt8) e[i] *= v_scale[t][i];
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
