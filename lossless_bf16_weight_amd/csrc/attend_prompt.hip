@@ -54,7 +54,7 @@ __device__ __forceinline__ float add_halves(float x) {
 }
 
 template <int D, bool kSplit>
-__global__ __launch_bounds__(kThreads) void attend_prompt_kernel(PromptArgs a) {
+__global__ __launch_bounds__(kThreads, 2) void attend_prompt_kernel(PromptArgs a) {
     constexpr int kChunks = D / 8;                           // 16-byte chunks of a row
     constexpr int kLoads = kPromptKeys * kChunks / kThreads; // chunks a thread stages
     constexpr int kDTiles = D / 32;
