@@ -24,6 +24,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr uint32_t kWaveRows = 32;
+constexpr float kSlack = 8.0f;
 
 // Byte offsets of 16-byte chunk `chunk` of key row `row` in the K and V tiles.
 // K: 32 rows are read at one chunk a time; V: four neighbouring rows, 32 bytes
@@ -162,13 +163,18 @@ __global__ __launch_bounds__(kThreads, 2) void attend_prompt_kernel(PromptArgs a
 #pragma unroll
             for (int i = 0; i < 16; ++i) top = fmaxf(top, s[t][i]);
         top = max_halves(top) * a.log2_scale;
-        const float next = fmaxf(m, top);
-        const float base = next == -__builtin_inff() ? 0.0f : next;
-        const float keep = exp2_fast(m - base);
-        m = next;
-        l *= keep;
+        // The base m is raised when a row's maximum passes it by more than 8,
+        // and only then are the sums scaled: weights stay below 2^8, which
+        // neither 32 bits nor the rounding of the weights minds.
+        if (__any(top > m + kSlack)) {
+            const float next = fmaxf(m, top);
+            const float keep = exp2_fast(m - (next == -__builtin_inff() ? 0.0f : next));
+            m = next;
+            l *= keep;
 #pragma unroll
-        for (int i = 0; i < kDTiles; ++i) o[i] *= keep;
+            for (int i = 0; i < kDTiles; ++i) o[i] *= keep;
+        }
+        const float base = m == -__builtin_inff() ? 0.0f : m;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
 #pragma unroll
