@@ -481,7 +481,8 @@ df11_status df11_attend_token(const df11_attend_token_args *args, int hip_device
  * DF11_ATTEND_CAUSAL the queries are the last of their sequence: query i sees
  * the keys j <= i + n_keys - n_queries (so a prompt's next piece attends to
  * what came before, and with more queries than keys the first see none);
- * otherwise all.  head_dim 64 or 128, scale > 0.  Workspace: as for
+ * otherwise all.  head_dim 64 or 128, scale > 0, row strides of k and v
+ * below 2^24 - 2.  Workspace: as for
  * df11_attend_token (few rows over many keys are split).  out may be q. */
 typedef struct {
     df11_rows q, k, v, out;

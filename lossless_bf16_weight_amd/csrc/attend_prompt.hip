@@ -26,18 +26,30 @@ constexpr int kThreads = 256;
 constexpr uint32_t kWaveRows = 32;
 constexpr float kSlack = 8.0f;
 
-// Byte offsets of 16-byte chunk `chunk` of key row `row` in the K and V tiles.
-// K: 32 rows are read at one chunk a time; V: four neighbouring rows, 32 bytes
-// of each, by a transposing read.  The exclusive or puts them into different
-// banks.
+// The K and V tiles in LDS: 16-byte chunk `chunk` of key row `row` lies at
+// place k_chunk (v_chunk) of its row, and the other way round.  K: 32 rows are
+// read at one chunk a time; V: four neighbouring rows, 32 bytes of each, by a
+// transposing read.  The exclusive or puts them into different banks.
+template <int D>
+__device__ __forceinline__ uint32_t k_chunk(uint32_t row, uint32_t chunk) {
+    return D == 128 ? chunk ^ (row & 15) : chunk ^ ((row >> 1) & 7);
+}
+template <int D>
+__device__ __forceinline__ uint32_t v_chunk(uint32_t row, uint32_t chunk) {
+    return D == 128 ? chunk ^ ((row & 3) << 2) : chunk ^ (((row >> 1) & 1) << 2);
+}
 template <int D>
 __device__ __forceinline__ uint32_t k_at(uint32_t row, uint32_t chunk) {
-    return D == 128 ? row * 256 + ((chunk ^ (row & 15)) << 4) : row * 128 + ((chunk ^ ((row >> 1) & 7)) << 4);
+    return row * (2 * D) + (k_chunk<D>(row, chunk) << 4);
 }
 template <int D>
 __device__ __forceinline__ uint32_t v_at(uint32_t row, uint32_t chunk) {
-    return D == 128 ? row * 256 + ((chunk ^ ((row & 3) << 2)) << 4) : row * 128 + ((chunk ^ (((row >> 1) & 1) << 2)) << 4);
+    return row * (2 * D) + (v_chunk<D>(row, chunk) << 4);
 }
+
+// Size of the K and V descriptors, and an offset that is outside (the host
+// keeps a tile's rows within it).
+constexpr uint32_t kOutOfRange = 0x80000000u;
 
 // x and the value 32 lanes away, in either order.
 __device__ __forceinline__ f32x2 both_halves(float x) {
@@ -60,8 +72,8 @@ __global__ __launch_bounds__(kThreads, 2) void attend_prompt_kernel(PromptArgs a
     constexpr int kLoads = kPromptKeys * kChunks / kThreads; // chunks a thread stages
     constexpr int kDTiles = D / 32;
     constexpr int kDSteps = D / 16;
-    __shared__ __attribute__((aligned(16))) uint8_t kt[kPromptKeys * D * 2];
-    __shared__ __attribute__((aligned(16))) uint8_t vt[kPromptKeys * D * 2];
+    __shared__ __attribute__((aligned(16))) uint8_t kt0[kPromptKeys * D * 2], kt1[kPromptKeys * D * 2];
+    __shared__ __attribute__((aligned(16))) uint8_t vt0[kPromptKeys * D * 2], vt1[kPromptKeys * D * 2];
 
     const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t col = lane & 31u, half = lane >> 5;
@@ -117,26 +129,36 @@ __global__ __launch_bounds__(kThreads, 2) void attend_prompt_kernel(PromptArgs a
     const uint16_t *const kp = a.k.data + (int64_t)k0 * a.k.row + kv_head * a.k.head;
     const uint16_t *const vp = a.v.data + (int64_t)k0 * a.v.row + kv_head * a.v.head;
 
-    for (uint32_t key0 = key_begin; key0 < key_end; key0 += kPromptKeys) {
-        u32x4 kw[kLoads], vw[kLoads];
+    // A step's K and V rows go from memory into LDS without passing through
+    // registers, one step ahead: the chunk that lane `at` of the tile holds is
+    // the one that belongs there.  A thread's chunks are 16 (or 32) rows apart
+    // and share their place in the row, so that one offset serves all; rows
+    // past the sequence (another one's) are out of the descriptor's range and
+    // arrive as zeros.
+    constexpr uint32_t kRowsALoad = kThreads / kChunks;
+    const uint32_t tile_row = threadIdx.x / kChunks, place = threadIdx.x % kChunks;
+    const uint32_t k_offset = 2 * (tile_row * (uint32_t)a.k.row + 8 * k_chunk<D>(tile_row, place));
+    const uint32_t v_offset = 2 * (tile_row * (uint32_t)a.v.row + 8 * v_chunk<D>(tile_row, place));
+    const auto load = [&](uint32_t key0, uint8_t *kt, uint8_t *vt) {
+        const __amdgpu_buffer_rsrc_t kr = __builtin_amdgcn_make_buffer_rsrc((void *)(kp + key0 * a.k.row), 0, kOutOfRange, 0x00020000);
+        const __amdgpu_buffer_rsrc_t vr = __builtin_amdgcn_make_buffer_rsrc((void *)(vp + key0 * a.v.row), 0, kOutOfRange, 0x00020000);
+        const uint32_t left = n_k - key0;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            const uint32_t at = i * kThreads + threadIdx.x, r = key0 + at / kChunks, c = at % kChunks;
-            kw[i] = vw[i] = u32x4{0, 0, 0, 0};               // (past the sequence: another one's rows)
-            if (r < n_k) {
-                kw[i] = *reinterpret_cast<const u32x4 *>(kp + r * a.k.row + 8 * c);
-                vw[i] = *reinterpret_cast<const u32x4 *>(vp + r * a.v.row + 8 * c);
-            }
+            const bool in = tile_row + i * kRowsALoad < left;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(kr, (DF11_LDS void *)(kt + (i * kThreads + wave * 64) * 16), 16,
+                                                     in ? k_offset : kOutOfRange, 2 * i * kRowsALoad * (uint32_t)a.k.row, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(vr, (DF11_LDS void *)(vt + (i * kThreads + wave * 64) * 16), 16,
+                                                     in ? v_offset : kOutOfRange, 2 * i * kRowsALoad * (uint32_t)a.v.row, 0, 0);
         }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const uint32_t at = i * kThreads + threadIdx.x, r = at / kChunks, c = at % kChunks;
-            *reinterpret_cast<u32x4 *>(kt + k_at<D>(r, c)) = kw[i];
-            *reinterpret_cast<u32x4 *>(vt + v_at<D>(r, c)) = vw[i];
-        }
-        __syncthreads();
-        if (key0 >= wave_end) continue;
+    };
+    const auto arrived = [&] {
+        __builtin_amdgcn_s_waitcnt(0x0F70);        // vmcnt(0): this wave's rows
+        __syncthreads();                           // and the others'; and all are done with the step before
+    };
+
+    const auto step = [&](uint32_t key0, const uint8_t *kt, const uint8_t *vt) {
+        if (key0 >= wave_end) return;
 
         f32x16 s[2];
 #pragma unroll
@@ -198,6 +220,16 @@ __global__ __launch_bounds__(kThreads, 2) void attend_prompt_kernel(PromptArgs a
                 }
             }
         }
+    };
+    if (key_begin < key_end) load(key_begin, kt0, vt0);
+    for (uint32_t key0 = key_begin; key0 < key_end; key0 += 2 * kPromptKeys) {
+        arrived();
+        if (key0 + kPromptKeys < key_end) load(key0 + kPromptKeys, kt1, vt1);
+        step(key0, kt0, vt0);
+        if (key0 + kPromptKeys >= key_end) break;
+        arrived();
+        if (key0 + 2 * kPromptKeys < key_end) load(key0 + 2 * kPromptKeys, kt0, vt0);
+        step(key0 + kPromptKeys, kt1, vt1);
     }
     l = add_halves(l);
     if (!real) return;

@@ -12,6 +12,8 @@ namespace {
 
 constexpr uint64_t kMostGroups = uint64_t(1) << 24;   // workgroups along x: threads stay below 2^32
 constexpr int64_t kMostStride = int64_t(1) << 32;
+// a step's key rows lie within 2^31 bytes of the first (attend_prompt.hip's descriptors)
+constexpr int64_t kMostKeyStride = ((int64_t(1) << 31) - 256) / (2 * kPromptKeys);
 
 struct Device {
     int prev = -1;
@@ -264,6 +266,8 @@ extern "C" df11_status df11_attend_prompt(const df11_attend_prompt_args *a, int 
     TRY(check_rows("k", a->k, a->n_k, a->n_kv_heads, a->head_dim, false));
     TRY(check_rows("v", a->v, a->n_k, a->n_kv_heads, a->head_dim, false));
     TRY(check_rows("out", a->out, a->n_q, a->n_heads, a->head_dim, true));
+    if (a->k.row_stride > kMostKeyStride || a->v.row_stride > kMostKeyStride)
+        return report_error(DF11_E_UNSUPPORTED, "k, v: rows more than %lld elements apart", (long long)kMostKeyStride);
     if (a->n_q == 0 || a->n_seqs == 0) return DF11_OK;
     if (bad_index(a->q_starts, 4) || bad_index(a->k_starts, 4)) return report_error(DF11_E_ARG, "attend_prompt: starts NULL or misaligned");
     const uint32_t splits = prompt_splits(*a, hip_device);

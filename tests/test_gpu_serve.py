@@ -418,13 +418,20 @@ def test_offsets_past_32_bits():
     df11.attend_token(q, cache, pages, torch.tensor([n], dtype=torch.int32, device=DEV), out)
     want = U.prompt64(q, k, v, [1], [n], True, d ** -0.5)
     U.within(out, *want, "token")
-    far = cache.k.view(-1)[:40 * (2 ** 25 + 8)]      # rows 2^25 + 8 elements apart
-    kf = torch.as_strided(far, (n, hk, d), (2 ** 25 + 8, d, 1))
+    m, stride = 130, 2 ** 24 - 8                     # key rows 32 MB apart, 4.3 GB in all
+    k, v = _rand((m, hk, d), 75, 1.5), _rand((m, hk, d), 76)
+    kf, vf = (torch.as_strided(x.view(-1), (m, hk, d), (stride, d, 1)) for x in cache[:2])
     kf.copy_(k)
-    qs = _rand((n, 16, d), 74)
-    os = torch.empty_like(qs)
-    df11.attend_prompt(qs, kf, v, s, s, os)
-    U.within(os, *U.prompt64(qs, k, v, [n], [n], True, d ** -0.5), "prompt")
+    vf.copy_(v)
+    qs = torch.as_strided(cache.k.view(-1), (m, 1, d), (stride, d, 1), 2 ** 20)
+    qs.copy_(_rand((m, 1, d), 74))
+    os = torch.as_strided(cache.v.view(-1), (m, 1, d), (stride, d, 1), 2 ** 20)
+    s = U.starts_of([m]).to(DEV)
+    df11.attend_prompt(qs, kf[:, :1], vf[:, :1], s, s, os)
+    U.within(os, *U.prompt64(qs, k[:, :1], v[:, :1], [m], [m], True, d ** -0.5), "prompt")
+    with pytest.raises(df11.DF11Error):
+        wide = torch.as_strided(cache.k.view(-1), (m, 1, d), (2 ** 24, d, 1))
+        df11.attend_prompt(qs, wide, wide, s, s, os)
 
 
 # ------------------------------------------------------- streams, graphs, order
