@@ -29,32 +29,38 @@ namespace {
 constexpr int kThreads = 64 * kTokenWaves;
 constexpr uint32_t kMostPages = kTokenRangeMax / 16;
 
-// Where 16-byte chunk `chunk` of key row `row` lies in a wave's V tile: the
-// transposing reads take 32 bytes of four neighbouring rows at a time, which
-// the exclusive or puts into different banks.
+// Where 16-byte chunk `chunk` of key row `row` lies in a wave's tile of 32
+// rows.  The exclusive or puts what is read together into different banks of
+// a 256-byte line.  K: 16 rows at one chunk.  V, by transposing reads of 16
+// elements of a row: words, two chunks of rows 0 .. 7 (8 .. 15, ...); bytes,
+// one chunk of rows 0 .. 7 and 16 .. 23 (8 .. 15 and 24 .. 31).
 template <int kRowBytes>
+__device__ __forceinline__ uint32_t k_at(uint32_t row, uint32_t chunk) {
+    return row * kRowBytes + ((chunk ^ (row / (256 / kRowBytes) & (kRowBytes / 16 - 1))) << 4);
+}
+template <int kRowBytes, bool kInt8>
 __device__ __forceinline__ uint32_t v_at(uint32_t row, uint32_t chunk) {
-    if (kRowBytes == 256) return row * 256 + ((chunk ^ ((row & 3) << 2)) << 4);
-    if (kRowBytes == 128) return row * 128 + ((chunk ^ (((row >> 1) & 1) << 2)) << 4);
-    return row * 64 + (chunk << 4);
+    uint32_t x;
+    if (kInt8) x = kRowBytes == 128 ? (row >> 1 & 3) | (row >> 4 & 1) << 2 : (row >> 2 & 1) | (row >> 4 & 1) << 1;
+    else x = kRowBytes == 256 ? (row & 7) << 1 : (row >> 1 & 3) << 1;
+    return row * kRowBytes + ((chunk ^ x) << 4);
 }
 
 template <int D, bool kInt8>
-__global__ __launch_bounds__(kThreads) void attend_token_kernel(TokenArgs a) {
+__global__ __launch_bounds__(kThreads, 3) void attend_token_kernel(TokenArgs a) {
     constexpr int kRow = kInt8 ? D : 2 * D;            // bytes of a stored row
     constexpr int kChunks = kRow / 16;                 // 16-byte chunks of it
-    constexpr int kVLoads = kTokenKeys * kChunks / 64;   // chunks a lane loads of a step's V rows
-    constexpr int kKLoads = kChunks / 4;               // and of each half of its K rows
+    constexpr int kLoads = kTokenKeys * kChunks / 64;  // chunks a lane loads of a step's K rows, and of its V rows
     constexpr int kDTiles = D / 16;
     constexpr int kOStride = D + 4;
-    constexpr uint32_t kVBytes = kTokenKeys * kRow;
+    constexpr uint32_t kTileBytes = kTokenKeys * kRow;
     constexpr uint32_t kJoinBytes = kTokenWaves * 16 * kOStride * 4;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[kTokenWaves * kVBytes > kJoinBytes ? kTokenWaves * kVBytes : kJoinBytes];
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kTokenWaves * kTileBytes > kJoinBytes ? kTokenWaves * kTileBytes : kJoinBytes];
     __shared__ uint32_t table[kMostPages];
     __shared__ float ml[kTokenWaves][2][16];
 
-    const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const uint32_t col = lane & 15u, grp = lane >> 4;
+    const uint32_t lane0 = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t lane = lane0, col = lane & 15u, grp = lane >> 4;
     uint32_t at = blockIdx.x;
     const uint32_t q_tile = at % a.q_tiles;
     at /= a.q_tiles;
@@ -86,74 +92,74 @@ __global__ __launch_bounds__(kThreads) void attend_token_kernel(TokenArgs a) {
     }
     __syncthreads();
 
-    const auto row_of = [&](uint32_t key) {            // of a key of the range
-        const uint32_t page = table[key >> a.c.shift];
-        return (((int64_t)page * a.c.kv_heads + kv_head) << a.c.shift) + (key & ((1u << a.c.shift) - 1));
+    // a key's row in the pages (the host keeps their number below 2^32)
+    const uint32_t in_page = (1u << a.c.shift) - 1;
+    const auto row_of = [&](uint32_t key) -> uint32_t {
+        return ((table[key >> a.c.shift] * a.c.kv_heads + kv_head) << a.c.shift) + (key & in_page);
     };
 
     f32x4 o[kDTiles];
 #pragma unroll
     for (int i = 0; i < kDTiles; ++i) o[i] = f32x4{0, 0, 0, 0};
     float m = -__builtin_inff(), l = 0;
-    uint8_t *const vt = lds + wave * kVBytes;
+    uint8_t *const tile = lds + wave * kTileBytes;
 
     // A step's 32 rows of K and V, held in registers from one step before:
     // the loads of the next step are in flight while this one is computed.
-    // Rows past the end repeat the last one (their scores are masked; their V
-    // rows are cleared below).
-    u32x4 kw[2][kKLoads], vw[kVLoads];
+    // 16 (8, 4) lanes load a row, whole lines that nobody reads again; the
+    // wave's tile in LDS, first K's and then V's, hands them to the lanes that
+    // compute.  Rows past the end repeat the last one (their scores are
+    // masked, their V rows are cleared below).
+    u32x4 kw[kLoads], vw[kLoads];
     f32x4 ks[2], vs[2];
-    const auto load_v = [&](uint32_t key0) {
+    uint32_t rows[kLoads];
+    const auto find_rows = [&](uint32_t key0) {
 #pragma unroll
-        for (int i = 0; i < kVLoads; ++i) {
-            const uint32_t at = i * 64 + lane, row = at / kChunks, chunk = at % kChunks;
-            vw[i] = *reinterpret_cast<const u32x4 *>(a.c.v + row_of(min(key0 + row, n - 1)) * kRow + 16 * chunk);
-        }
+        for (int i = 0; i < kLoads; ++i) rows[i] = row_of(min(key0 + (i * 64 + lane) / kChunks, n - 1));
     };
-    const auto load_k = [&](uint32_t key0) {
+    const uint8_t *const k_pages = a.c.k + 16 * (lane % kChunks), *const v_pages = a.c.v + 16 * (lane % kChunks);
+    const auto load = [&](const uint8_t *pages, u32x4 *w) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const uint8_t *const kp = a.c.k + row_of(min(key0 + 16 * t + col, n - 1)) * kRow + 16 * grp;
-#pragma unroll
-            for (int i = 0; i < kKLoads; ++i) kw[t][i] = *reinterpret_cast<const u32x4 *>(kp + 64 * i);
-        }
+        for (int i = 0; i < kLoads; ++i)
+            w[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(pages + (uint64_t)rows[i] * kRow));
     };
     const auto load_scales = [&](uint32_t key0) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {       // four keys of one page
-            const int64_t r = row_of(min(key0 + 16 * t + 4 * grp, n - 1) & ~3u);
+            const uint32_t r = row_of(min(key0 + 16 * t + 4 * grp, n - 1) & ~3u);
             ks[t] = *reinterpret_cast<const f32x4 *>(a.c.k_scale + r);
             vs[t] = *reinterpret_cast<const f32x4 *>(a.c.v_scale + r);
         }
     };
     uint32_t key0 = wave * kTokenKeys;
     if (key0 < n) {
-        load_v(key0);
-        load_k(key0);
+        find_rows(key0);
+        load(k_pages, kw);
+        load(v_pages, vw);
         if (kInt8) load_scales(key0);
     }
     for (; key0 < n; key0 += kTokenWaves * kTokenKeys) {
         const uint32_t next_key = min(key0 + kTokenWaves * kTokenKeys, n - 1);   // (past the end: loads that nobody uses)
-        if (key0 + kTokenKeys > n) {
-            // weights of rows past the end are 0, and 0 times an infinity would be NaN
+        // (the tile's addresses are computed anew in each step: kept in
+        // registers over the loop they would cost a wave of occupancy)
+        uint32_t lane = lane0;
+        asm volatile("" : "+v"(lane));
+        const uint32_t col = lane & 15u, grp = lane >> 4;
 #pragma unroll
-            for (int i = 0; i < kVLoads; ++i)
-                if (key0 + (i * 64 + lane) / kChunks >= n) vw[i] = u32x4{0, 0, 0, 0};
-        }
-#pragma unroll
-        for (int i = 0; i < kVLoads; ++i) {
+        for (int i = 0; i < kLoads; ++i) {
             const uint32_t at = i * 64 + lane;
-            *reinterpret_cast<u32x4 *>(vt + v_at<kRow>(at / kChunks, at % kChunks)) = vw[i];
+            *reinterpret_cast<u32x4 *>(tile + k_at<kRow>(at / kChunks, at % kChunks)) = kw[i];
         }
-        load_v(next_key);
+        find_rows(next_key);
+        load(k_pages, kw);
         // scores of two times 16 keys: lane has keys 16 t + 4 grp + i of query col
         f32x4 s[2];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             s[t] = f32x4{0, 0, 0, 0};
 #pragma unroll
-            for (int i = 0; i < kKLoads; ++i) {
-                const u32x4 w = kw[t][i];
+            for (int i = 0; i < kChunks / 4; ++i) {
+                const u32x4 w = *reinterpret_cast<const u32x4 *>(tile + k_at<kRow>(16 * t + col, 4 * i + grp));
                 if (kInt8) {
                     s[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(bf16_of_bytes8(u32x2{w.x, w.y})), as_bf16x8(q[2 * i]), s[t], 0, 0, 0);
                     s[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(bf16_of_bytes8(u32x2{w.z, w.w})), as_bf16x8(q[2 * i + 1]), s[t], 0, 0, 0);
@@ -162,6 +168,18 @@ __global__ __launch_bounds__(kThreads) void attend_token_kernel(TokenArgs a) {
                 }
             }
         }
+        if (key0 + kTokenKeys > n) {
+            // weights of rows past the end are 0, and 0 times an infinity would be NaN
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i)
+                if (key0 + (i * 64 + lane) / kChunks >= n) vw[i] = u32x4{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const uint32_t at = i * 64 + lane;
+            *reinterpret_cast<u32x4 *>(tile + v_at<kRow, kInt8>(at / kChunks, at % kChunks)) = vw[i];
+        }
+        load(v_pages, vw);
         f32x4 v_scale[2];
         float top = -__builtin_inff();
 #pragma unroll
@@ -174,7 +192,6 @@ __global__ __launch_bounds__(kThreads) void attend_token_kernel(TokenArgs a) {
                 top = fmaxf(top, s[t][i]);
             }
         }
-        load_k(next_key);
         if (kInt8) load_scales(next_key);
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
@@ -214,12 +231,12 @@ __global__ __launch_bounds__(kThreads) void attend_token_kernel(TokenArgs a) {
                 const uint32_t j = lane & 15u, r = j >> 1;
                 const uint32_t row = (r < 4 ? 0 : 12) + 4 * grp + r;
                 const i32x2 b = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-                    (DF11_LDS i32x2 *)(vt + v_at<kRow>(row, i) + 8 * (j & 1)));
+                    (DF11_LDS i32x2 *)(tile + v_at<kRow, kInt8>(row, i) + 8 * (j & 1)));
                 w = bf16_of_bytes8(u32x2{(uint32_t)b.x, (uint32_t)b.y});
             } else {
                 const uint32_t j = lane & 15u, row = 4 * grp + (j >> 2), chunk = 2 * i + ((j & 3) >> 1);
-                const s16x4 b0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((DF11_LDS s16x4 *)(vt + v_at<kRow>(row, chunk) + 8 * (j & 1)));
-                const s16x4 b1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((DF11_LDS s16x4 *)(vt + v_at<kRow>(row + 16, chunk) + 8 * (j & 1)));
+                const s16x4 b0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((DF11_LDS s16x4 *)(tile + v_at<kRow, kInt8>(row, chunk) + 8 * (j & 1)));
+                const s16x4 b1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((DF11_LDS s16x4 *)(tile + v_at<kRow, kInt8>(row + 16, chunk) + 8 * (j & 1)));
                 const u32x2 w0 = __builtin_bit_cast(u32x2, b0), w1 = __builtin_bit_cast(u32x2, b1);
                 w = u32x4{w0.x, w0.y, w1.x, w1.y};
             }
@@ -235,7 +252,7 @@ __global__ __launch_bounds__(kThreads) void attend_token_kernel(TokenArgs a) {
         ml[wave][0][lane] = m;
         ml[wave][1][lane] = l;
     }
-    __syncthreads();                                   // (also: every wave is done with its V tile)
+    __syncthreads();                                   // (also: every wave is done with its tile)
     float *const parts = reinterpret_cast<float *>(lds);
     float most = -__builtin_inff();
 #pragma unroll

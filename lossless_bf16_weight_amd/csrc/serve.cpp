@@ -71,6 +71,8 @@ df11_status check_cache_sizes(const df11_kv_cache &c) {
         return report_error(DF11_E_ARG, "cache: page_size %u, a power of two from 16 to 1024 is needed", c.page_size);
     if (c.n_pages == 0 || c.n_pages > 0x7FFFFFFFu || c.n_kv_heads == 0 || c.n_kv_heads > 65535)
         return report_error(DF11_E_ARG, "cache: %u pages, %u kv heads", c.n_pages, c.n_kv_heads);
+    if ((uint64_t)c.n_pages * c.n_kv_heads * c.page_size > 0xFFFFFFFFull)
+        return report_error(DF11_E_UNSUPPORTED, "cache: 2^32 rows or more");
     return DF11_OK;
 }
 
