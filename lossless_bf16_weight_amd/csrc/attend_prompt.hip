@@ -24,7 +24,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr uint32_t kWaveRows = 32;
-constexpr float kSlack = 8.0f;
 
 // The K and V tiles in LDS: 16-byte chunk `chunk` of key row `row` lies at
 // place k_chunk (v_chunk) of its row, and the other way round.  K: 32 rows are
@@ -50,21 +49,6 @@ __device__ __forceinline__ uint32_t v_at(uint32_t row, uint32_t chunk) {
 // Size of the K and V descriptors, and an offset that is outside (the host
 // keeps a tile's rows within it).
 constexpr uint32_t kOutOfRange = 0x80000000u;
-
-// x and the value 32 lanes away, in either order.
-__device__ __forceinline__ f32x2 both_halves(float x) {
-    const uint32_t a = __float_as_uint(x);
-    const auto r = __builtin_amdgcn_permlane32_swap(a, a, false, false);
-    return f32x2{__uint_as_float(r[0]), __uint_as_float(r[1])};
-}
-__device__ __forceinline__ float max_halves(float x) {
-    const f32x2 r = both_halves(x);
-    return fmaxf(r.x, r.y);
-}
-__device__ __forceinline__ float add_halves(float x) {
-    const f32x2 r = both_halves(x);
-    return r.x + r.y;
-}
 
 template <int D, bool kSplit>
 __global__ __launch_bounds__(kThreads, 2) void attend_prompt_kernel(PromptArgs a) {
@@ -184,10 +168,8 @@ __global__ __launch_bounds__(kThreads, 2) void attend_prompt_kernel(PromptArgs a
         for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int i = 0; i < 16; ++i) top = fmaxf(top, s[t][i]);
-        top = max_halves(top) * a.log2_scale;
-        // The base m is raised when a row's maximum passes it by more than 8,
-        // and only then are the sums scaled: weights stay below 2^8, which
-        // neither 32 bits nor the rounding of the weights minds.
+        const f32x2 halves = with_lane_32(top);
+        top = fmaxf(halves.x, halves.y) * a.log2_scale;
         if (__any(top > m + kSlack)) {
             const float next = fmaxf(m, top);
             const float keep = exp2_fast(m - (next == -__builtin_inff() ? 0.0f : next));
@@ -231,7 +213,8 @@ __global__ __launch_bounds__(kThreads, 2) void attend_prompt_kernel(PromptArgs a
         if (key0 + 2 * kPromptKeys < key_end) load(key0 + 2 * kPromptKeys, kt0, vt0);
         step(key0 + kPromptKeys, kt1, vt1);
     }
-    l = add_halves(l);
+    const f32x2 l_halves = with_lane_32(l);
+    l = l_halves.x + l_halves.y;
     if (!real) return;
     if (kSplit) {
         const uint64_t at = ((uint64_t)blockIdx.y * a.n_q + q0 + row) * a.heads + head;

@@ -58,6 +58,7 @@ __global__ __launch_bounds__(kThreads, 3) void attend_token_kernel(TokenArgs a) 
     __shared__ __attribute__((aligned(16))) uint8_t lds[kTokenWaves * kTileBytes > kJoinBytes ? kTokenWaves * kTileBytes : kJoinBytes];
     __shared__ uint32_t table[kMostPages];
     __shared__ float ml[kTokenWaves][2][16];
+    __shared__ u32x4 q[D / 32][64];
 
     const uint32_t lane0 = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t lane = lane0, col = lane & 15u, grp = lane >> 4;
@@ -72,31 +73,29 @@ __global__ __launch_bounds__(kThreads, 3) void attend_token_kernel(TokenArgs a) 
     if (begin >= len && split) return;
     const uint32_t n = min(len - begin, a.range);      // this workgroup's keys
 
-    // the pages of the range
+    // the first row of this head in each page of the range (the host keeps the
+    // number of rows below 2^32)
     const int32_t *const pages = a.t.pages + seq * a.t.stride + (begin >> a.c.shift);
     for (uint32_t i = threadIdx.x; i < ((n + (1u << a.c.shift) - 1) >> a.c.shift); i += kThreads)
-        table[i] = min((uint32_t)pages[i], a.c.n_pages - 1);
+        table[i] = (min((uint32_t)pages[i], a.c.n_pages - 1) * a.c.kv_heads + kv_head) << a.c.shift;
 
     // queries: columns past the group are zero
     const uint32_t in_group = q_tile * 16 + col;
     const uint32_t head = kv_head * a.group + in_group;
     const bool real = in_group < a.group;
-    u32x4 q[D / 32];
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
+    // (in LDS, in the order of the operands' lanes, for the registers are full)
+    for (uint32_t i = wave; i < D / 32; i += kTokenWaves) {
         // words: step i holds d = 32 i + 8 grp ..; bytes: two steps share a
         // 16-byte chunk, so steps 2t and 2t + 1 hold d = 64 t + 16 grp + 0 and 8 ..
         const uint32_t d = kInt8 ? 64 * (i / 2) + 16 * grp + 8 * (i % 2) : 32 * i + 8 * grp;
-        q[i] = u32x4{0, 0, 0, 0};
-        if (real) q[i] = *reinterpret_cast<const u32x4 *>(a.q.data + seq * a.q.row + head * a.q.head + d);
+        u32x4 w = {0, 0, 0, 0};
+        if (real) w = *reinterpret_cast<const u32x4 *>(a.q.data + seq * a.q.row + head * a.q.head + d);
+        q[i][lane] = w;
     }
     __syncthreads();
 
-    // a key's row in the pages (the host keeps their number below 2^32)
     const uint32_t in_page = (1u << a.c.shift) - 1;
-    const auto row_of = [&](uint32_t key) -> uint32_t {
-        return ((table[key >> a.c.shift] * a.c.kv_heads + kv_head) << a.c.shift) + (key & in_page);
-    };
+    const auto row_of = [&](uint32_t key) -> uint32_t { return table[key >> a.c.shift] + (key & in_page); };
 
     f32x4 o[kDTiles];
 #pragma unroll
@@ -152,6 +151,7 @@ __global__ __launch_bounds__(kThreads, 3) void attend_token_kernel(TokenArgs a) 
         }
         find_rows(next_key);
         load(k_pages, kw);
+        __builtin_amdgcn_sched_barrier(0);     // (loads of V moved up past here would not fit in registers)
         // scores of two times 16 keys: lane has keys 16 t + 4 grp + i of query col
         f32x4 s[2];
 #pragma unroll
@@ -161,10 +161,10 @@ __global__ __launch_bounds__(kThreads, 3) void attend_token_kernel(TokenArgs a) 
             for (int i = 0; i < kChunks / 4; ++i) {
                 const u32x4 w = *reinterpret_cast<const u32x4 *>(tile + k_at<kRow>(16 * t + col, 4 * i + grp));
                 if (kInt8) {
-                    s[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(bf16_of_bytes8(u32x2{w.x, w.y})), as_bf16x8(q[2 * i]), s[t], 0, 0, 0);
-                    s[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(bf16_of_bytes8(u32x2{w.z, w.w})), as_bf16x8(q[2 * i + 1]), s[t], 0, 0, 0);
+                    s[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(bf16_of_bytes8(u32x2{w.x, w.y})), as_bf16x8(q[2 * i][lane]), s[t], 0, 0, 0);
+                    s[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(bf16_of_bytes8(u32x2{w.z, w.w})), as_bf16x8(q[2 * i + 1][lane]), s[t], 0, 0, 0);
                 } else {
-                    s[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(w), as_bf16x8(q[i]), s[t], 0, 0, 0);
+                    s[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(w), as_bf16x8(q[i][lane]), s[t], 0, 0, 0);
                 }
             }
         }
@@ -193,15 +193,18 @@ __global__ __launch_bounds__(kThreads, 3) void attend_token_kernel(TokenArgs a) 
             }
         }
         if (kInt8) load_scales(next_key);
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
-        const float next = fmaxf(m, top);
-        const float base = next == -__builtin_inff() ? 0.0f : next;
-        const float keep = exp2_fast(m - base);
-        m = next;
-        l *= keep;
+        f32x2 two = with_lane_16(top);
+        two = with_lane_32(fmaxf(two.x, two.y));
+        top = fmaxf(two.x, two.y);
+        if (__any(top > m + kSlack)) {
+            const float next = fmaxf(m, top);
+            const float keep = exp2_fast(m - (next == -__builtin_inff() ? 0.0f : next));
+            m = next;
+            l *= keep;
 #pragma unroll
-        for (int i = 0; i < kDTiles; ++i) o[i] *= keep;
+            for (int i = 0; i < kDTiles; ++i) o[i] *= keep;
+        }
+        const float base = m == -__builtin_inff() ? 0.0f : m;
         // weights as the sum of two BF16 operands, for the product has matrix
         // rate to spare: rounded once they would add as much error as the
         // rounding of the result (0.0027 of the norm against 0.0017)
@@ -244,8 +247,9 @@ __global__ __launch_bounds__(kThreads, 3) void attend_token_kernel(TokenArgs a) 
             o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(w), as_bf16x8(p_low), o[i], 0, 0, 0);
         }
     }
-    l += __shfl_xor(l, 16);
-    l += __shfl_xor(l, 32);
+    f32x2 two = with_lane_16(l);
+    two = with_lane_32(two.x + two.y);
+    l = two.x + two.y;
 
     // join the waves
     if (lane < 16) {

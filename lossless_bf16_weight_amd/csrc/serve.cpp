@@ -110,7 +110,8 @@ df11_status launched(hipError_t e, const char *what) {
 float log2_scale(float scale) { return (float)((double)scale * 1.4426950408889634074); }
 
 // How attend_token splits: keys a workgroup takes and workgroups along a
-// sequence.  Four workgroups a compute unit keep enough bytes in flight;
+// sequence.  Three are resident on a compute unit at a time; eight for each
+// level out sequences of unequal lengths (of the longest, table-wide one), and
 // longer ranges leave fewer parts to join.
 struct TokenSplit {
     uint32_t q_tiles, range, splits;
@@ -122,7 +123,7 @@ TokenSplit token_split(const df11_attend_token_args &a, int dev) {
     s.q_tiles = (uint32_t)ceil_div(a.n_heads / a.cache.n_kv_heads, 16);
     const uint64_t units = (uint64_t)a.n_seqs * a.cache.n_kv_heads * s.q_tiles;
     const uint64_t step = std::max(kTokenKeys * kTokenWaves, a.cache.page_size);
-    const uint64_t want = std::max<uint64_t>(1, 4 * compute_units(dev) / std::max<uint64_t>(units, 1));
+    const uint64_t want = std::max<uint64_t>(1, 8 * compute_units(dev) / std::max<uint64_t>(units, 1));
     const uint64_t range = ceil_div(ceil_div(most, want), step) * step;
     s.range = (uint32_t)std::min<uint64_t>(std::max<uint64_t>(range, 2 * step), kTokenRangeMax);
     s.splits = (uint32_t)ceil_div(most, s.range);

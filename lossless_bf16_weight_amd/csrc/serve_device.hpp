@@ -27,6 +27,24 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// x and the value 32 (16) lanes away, in either order.
+__device__ __forceinline__ f32x2 with_lane_32(float x) {
+    const uint32_t a = __float_as_uint(x);
+    const auto r = __builtin_amdgcn_permlane32_swap(a, a, false, false);
+    return f32x2{__uint_as_float(r[0]), __uint_as_float(r[1])};
+}
+__device__ __forceinline__ f32x2 with_lane_16(float x) {
+    const uint32_t a = __float_as_uint(x);
+    const auto r = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+    return f32x2{__uint_as_float(r[0]), __uint_as_float(r[1])};
+}
+
+// Softmax sums are kept against a base that is raised only when a row's
+// maximum passes it by more than this: weights stay below 2^8, which neither
+// 32 bits nor the rounding of the weights minds, and most steps then need not
+// scale the sums.
+constexpr float kSlack = 8.0f;
+
 // The four signed bytes of w as BF16 words (exact: |code| <= 128 has eight
 // significant bits, so the float's upper half is the whole value).
 __device__ __forceinline__ u32x2 bf16_of_bytes(uint32_t w) {
