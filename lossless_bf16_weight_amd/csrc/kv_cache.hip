@@ -19,8 +19,8 @@ namespace df11 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;
-constexpr uint32_t kReadShift = 6;    // 64 tokens of one head a workgroup
+constexpr int kWriteUnroll = 2, kReadUnroll = 4;
+constexpr uint32_t kReadShift = 4;    // 16 tokens a workgroup
 
 // Maximum over the kLanes neighbouring lanes that hold a row, in each of them.
 template <int kLanes>
@@ -49,12 +49,12 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(WriteArgs a) {
     uint8_t *const store = is_v ? a.c.v : a.c.k;
     float *const scales = is_v ? a.c.v_scale : a.c.k_scale;
     const uint64_t n_units = (uint64_t)a.n_tokens * a.c.kv_heads * kLanes;
-    const uint64_t first = (uint64_t)blockIdx.x * (kThreads * kUnroll) + threadIdx.x;
-    u32x4 w[kUnroll];
-    int64_t slot[kUnroll];
-    uint32_t head[kUnroll];
+    const uint64_t first = (uint64_t)blockIdx.x * (kThreads * kWriteUnroll) + threadIdx.x;
+    u32x4 w[kWriteUnroll];
+    int64_t slot[kWriteUnroll];
+    uint32_t head[kWriteUnroll];
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
+    for (int i = 0; i < kWriteUnroll; ++i) {
         const uint64_t unit = first + (uint64_t)i * kThreads;
         slot[i] = -1;
         if (unit < n_units) {
@@ -62,11 +62,11 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(WriteArgs a) {
             const uint32_t token = r / a.c.kv_heads;
             head[i] = r - token * a.c.kv_heads;
             slot[i] = a.slots[token];
-            w[i] = *reinterpret_cast<const u32x4 *>(x.data + token * x.row + head[i] * x.head + (unit % kLanes) * 8);
+            w[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(x.data + token * x.row + head[i] * x.head + (unit % kLanes) * 8));
         }
     }
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
+    for (int i = 0; i < kWriteUnroll; ++i) {
         const uint32_t part = threadIdx.x % kLanes;
         uint32_t m = 0;
         if (kInt8) {
@@ -93,50 +93,57 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(WriteArgs a) {
     }
 }
 
+// A workgroup reads back 16 tokens of all heads: it writes whole rows, and
+// reads 16 neighbouring rows of each head's part of a page.
 template <int D, bool kInt8>
 __global__ __launch_bounds__(kThreads) void kv_read_kernel(ReadArgs a) {
     constexpr uint32_t kLanes = D / 8;
-    constexpr int kSteps = (1 << kReadShift) * kLanes / kThreads;
     uint32_t tile;
     const uint32_t s = sequence_of_slot(a.starts, a.n_seqs, blockIdx.x, kReadShift, &tile);
     const int32_t begin = a.starts[s], end = a.starts[s + 1];
     if (begin < 0 || end < begin || (uint32_t)end > a.n_tokens) return;
     const uint32_t n = min((uint32_t)(end - begin), a.t.width << a.c.shift);
-    if (tile > (n >> kReadShift)) return;
-    const bool is_v = blockIdx.z != 0;
+    if (tile > n >> kReadShift) return;
+    const uint32_t pos0 = tile << kReadShift, rows = min(n - pos0, 1u << kReadShift) * a.c.kv_heads;
+    if (rows == 0) return;
+    const bool is_v = blockIdx.y != 0;
     const Rows &x = is_v ? a.v : a.k;
     const uint8_t *const store = is_v ? a.c.v : a.c.k;
     const float *const scales = is_v ? a.c.v_scale : a.c.k_scale;
-    const uint32_t head = blockIdx.y, part = threadIdx.x % kLanes;
-    const int32_t *const table = a.t.pages + s * a.t.stride;
-    u32x4 w[kSteps];
-    u32x2 c[kSteps];
-    float scale[kSteps];
+    const uint32_t part = threadIdx.x % kLanes;
+    // (16 positions from a multiple of 16 lie in one page)
+    const uint32_t page = min((uint32_t)a.t.pages[s * a.t.stride + (pos0 >> a.c.shift)], a.c.n_pages - 1);
+    const uint32_t in_page = pos0 & ((1u << a.c.shift) - 1);
+    for (uint32_t r0 = threadIdx.x / kLanes; r0 < rows; r0 += kReadUnroll * kThreads / kLanes) {
+        u32x4 w[kReadUnroll];
+        u32x2 c[kReadUnroll];
+        float scale[kReadUnroll];
+        uint32_t pos[kReadUnroll], head[kReadUnroll];
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-        const uint32_t pos = (tile << kReadShift) + (threadIdx.x + i * kThreads) / kLanes;
-        if (pos >= n) continue;
-        const uint32_t page = min((uint32_t)table[pos >> a.c.shift], a.c.n_pages - 1);
-        const int64_t row = (((int64_t)page * a.c.kv_heads + head) << a.c.shift) + (pos & ((1u << a.c.shift) - 1));
-        if (kInt8) {
-            c[i] = *reinterpret_cast<const u32x2 *>(store + row * D + 8 * part);
-            scale[i] = scales[row];
-        } else {
-            w[i] = *reinterpret_cast<const u32x4 *>(store + 2 * (row * D + 8 * part));
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-        const uint32_t pos = (tile << kReadShift) + (threadIdx.x + i * kThreads) / kLanes;
-        if (pos >= n) continue;
-        if (kInt8) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t two = c[i][j / 2] >> (16 * (j % 2));
-                w[i][j] = pack_bf16((float)(int8_t)two * scale[i], (float)(int8_t)(two >> 8) * scale[i]);
+        for (int i = 0; i < kReadUnroll; ++i) {
+            const uint32_t r = min(r0 + i * (kThreads / kLanes), rows - 1);
+            pos[i] = r / a.c.kv_heads;
+            head[i] = r - pos[i] * a.c.kv_heads;
+            const uint64_t row = (((uint64_t)page * a.c.kv_heads + head[i]) << a.c.shift) + in_page + pos[i];
+            if (kInt8) {
+                c[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x2 *>(store + row * D + 8 * part));
+                scale[i] = scales[row];
+            } else {
+                w[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(store + 2 * (row * D + 8 * part)));
             }
         }
-        *reinterpret_cast<u32x4 *>(x.data + (int64_t)(begin + pos) * x.row + head * x.head + 8 * part) = w[i];
+#pragma unroll
+        for (int i = 0; i < kReadUnroll; ++i) {
+            if (r0 + i * (kThreads / kLanes) >= rows) continue;
+            if (kInt8) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t two = c[i][j / 2] >> (16 * (j % 2));
+                    w[i][j] = pack_bf16((float)(int8_t)two * scale[i], (float)(int8_t)(two >> 8) * scale[i]);
+                }
+            }
+            *reinterpret_cast<u32x4 *>(x.data + (int64_t)(begin + pos0 + pos[i]) * x.row + head[i] * x.head + 8 * part) = w[i];
+        }
     }
 }
 
@@ -144,7 +151,7 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(ReadArgs a) {
 
 hipError_t launch_kv_write(const WriteArgs &a, uint32_t head_dim, bool int8, hipStream_t stream) {
     const uint64_t units = (uint64_t)a.n_tokens * a.c.kv_heads * (head_dim / 8);
-    const dim3 grid((uint32_t)((units + kThreads * kUnroll - 1) / (kThreads * kUnroll)), 2);
+    const dim3 grid((uint32_t)((units + kThreads * kWriteUnroll - 1) / (kThreads * kWriteUnroll)), 2);
     const auto kernel = head_dim == 64 ? (int8 ? kv_write_kernel<64, true> : kv_write_kernel<64, false>)
                                        : (int8 ? kv_write_kernel<128, true> : kv_write_kernel<128, false>);
     hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, a);
@@ -152,7 +159,7 @@ hipError_t launch_kv_write(const WriteArgs &a, uint32_t head_dim, bool int8, hip
 }
 
 hipError_t launch_kv_read(const ReadArgs &a, uint32_t head_dim, bool int8, hipStream_t stream) {
-    const dim3 grid((a.n_tokens >> kReadShift) + a.n_seqs, a.c.kv_heads, 2);
+    const dim3 grid((a.n_tokens >> kReadShift) + a.n_seqs, 2);
     const auto kernel = head_dim == 64 ? (int8 ? kv_read_kernel<64, true> : kv_read_kernel<64, false>)
                                        : (int8 ? kv_read_kernel<128, true> : kv_read_kernel<128, false>);
     hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, a);

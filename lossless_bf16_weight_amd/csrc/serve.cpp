@@ -110,9 +110,14 @@ df11_status launched(hipError_t e, const char *what) {
 float log2_scale(float scale) { return (float)((double)scale * 1.4426950408889634074); }
 
 // How attend_token splits: keys a workgroup takes and workgroups along a
-// sequence.  Three are resident on a compute unit at a time; eight for each
-// level out sequences of unequal lengths (of the longest, table-wide one), and
-// longer ranges leave fewer parts to join.
+// sequence, from the longest length that the table holds.  A step of the four
+// waves is 128 keys and takes 1.3 us when little else runs, the join 2.7 us:
+// one sequence of 1024 keys takes 7.7 us in parts of 128 keys and 10 us in
+// parts of 384; 256 keys take 6.1 us in one part and 7.5 us in two.  Where the
+// units fill the compute units, the three workgroups for each that run at a
+// time are enough (16 sequences of 1024 keys: 14.9 us; with four 17.3 us), in
+// parts of at most 2048 keys, for lengths are unequal (48 sequences in 8 bits:
+// 138 us, in parts of 4096 147 us).
 struct TokenSplit {
     uint32_t q_tiles, range, splits;
 };
@@ -123,9 +128,9 @@ TokenSplit token_split(const df11_attend_token_args &a, int dev) {
     s.q_tiles = (uint32_t)ceil_div(a.n_heads / a.cache.n_kv_heads, 16);
     const uint64_t units = (uint64_t)a.n_seqs * a.cache.n_kv_heads * s.q_tiles;
     const uint64_t step = std::max(kTokenKeys * kTokenWaves, a.cache.page_size);
-    const uint64_t want = std::max<uint64_t>(1, 8 * compute_units(dev) / std::max<uint64_t>(units, 1));
+    const uint64_t want = std::max<uint64_t>(1, 3 * compute_units(dev) / std::max<uint64_t>(units, 1));
     const uint64_t range = ceil_div(ceil_div(most, want), step) * step;
-    s.range = (uint32_t)std::min<uint64_t>(std::max<uint64_t>(range, 2 * step), kTokenRangeMax);
+    s.range = (uint32_t)std::min<uint64_t>(most <= 2 * step ? 2 * step : range, kTokenRangeMax);
     s.splits = (uint32_t)ceil_div(most, s.range);
     return s;
 }
@@ -206,7 +211,7 @@ extern "C" df11_status df11_kv_read(const df11_kv_read_args *a, int hip_device, 
     if (!a) return report_error(DF11_E_ARG, "kv_read: NULL arguments");
     TRY(check_cache(a->cache));
     const uint32_t d = a->cache.head_dim, heads = a->cache.n_kv_heads;
-    if (a->n_tokens > 0x7FFFFFFFu || a->n_tokens / 64 + a->n_seqs > kMostGroups)
+    if (a->n_tokens > 0x7FFFFFFFu || a->n_tokens / 16 + a->n_seqs > kMostGroups)
         return report_error(DF11_E_UNSUPPORTED, "kv_read: %llu tokens of %u sequences", (unsigned long long)a->n_tokens, a->n_seqs);
     TRY(check_rows("k", a->k, a->n_tokens, heads, d, true));
     TRY(check_rows("v", a->v, a->n_tokens, heads, d, true));
