@@ -116,8 +116,9 @@ float log2_scale(float scale) { return (float)((double)scale * 1.442695040888963
 // parts of 384; 256 keys take 6.1 us in one part and 7.5 us in two.  Where the
 // units fill the compute units, the three workgroups for each that run at a
 // time are enough (16 sequences of 1024 keys: 14.9 us; with four 17.3 us), in
-// parts of at most 2048 keys, for lengths are unequal (48 sequences in 8 bits:
-// 138 us, in parts of 4096 147 us).
+// parts of at most 1280 keys: lengths are unequal, and no more parts than
+// compute units leave some of these idle (sequences of 100001 and 7640 keys:
+// 78 us, in parts of 2048 91 us; shorter parts of 512 84 us).
 struct TokenSplit {
     uint32_t q_tiles, range, splits;
 };
@@ -130,7 +131,8 @@ TokenSplit token_split(const df11_attend_token_args &a, int dev) {
     const uint64_t step = std::max(kTokenKeys * kTokenWaves, a.cache.page_size);
     const uint64_t want = std::max<uint64_t>(1, 3 * compute_units(dev) / std::max<uint64_t>(units, 1));
     const uint64_t range = ceil_div(ceil_div(most, want), step) * step;
-    s.range = (uint32_t)std::min<uint64_t>(most <= 2 * step ? 2 * step : range, kTokenRangeMax);
+    const uint64_t longest = std::max<uint64_t>(kTokenRangeMax / step, 1) * step;   // (ranges begin with a page)
+    s.range = (uint32_t)(most <= 2 * step ? 2 * step : std::min(range, longest));
     s.splits = (uint32_t)ceil_div(most, s.range);
     return s;
 }

@@ -68,7 +68,7 @@ constexpr uint32_t kPromptTile = 128;    // query rows a workgroup takes
 constexpr uint32_t kPromptKeys = 64;     // keys a step
 constexpr uint32_t kTokenKeys = 32;      // keys a wave's step
 constexpr uint32_t kTokenWaves = 4;
-constexpr uint32_t kTokenRangeMax = 2048;
+constexpr uint32_t kTokenRangeMax = 1280;  // keys a workgroup takes of a long sequence
 
 hipError_t launch_kv_write(const WriteArgs &a, uint32_t head_dim, bool int8, hipStream_t stream);
 hipError_t launch_kv_read(const ReadArgs &a, uint32_t head_dim, bool int8, hipStream_t stream);
