@@ -6,8 +6,10 @@
 // p_j v_j / sum p_j; a row that sees no key is 0.  One pass over the keys:
 // when a step raises m, the sums are scaled by 2^(old - new).
 //
-// A workgroup takes 128 query rows of one head, its four waves 32 each, and
-// steps over the keys 64 at a time through LDS.  Matrix instructions, 32 x 32
+// The queries of the heads that share a kv head are the rows of one matrix:
+// row r is query r / group of head r % group.  A workgroup takes 128 rows of a
+// kv head, its four waves 32 each, and steps over the keys 64 at a time
+// through LDS.  Matrix instructions, 32 x 32
 // x 16: S^T = K Q^T puts a query in each lane (column) with 16 keys of 32 in
 // its registers (the lane 32 away has the others), so that the row statistics
 // are per lane, and P^T is the second product's operand as it stands: O^T =
@@ -63,26 +65,25 @@ __global__ __launch_bounds__(kThreads, 2) void attend_prompt_kernel(PromptArgs a
     const uint32_t col = lane & 31u, half = lane >> 5;
 
     // (workgroups are dealt to the eight XCDs in turn: kv heads vary fastest,
-    // so that the heads that share one meet in one L2; the last rows of a
-    // causal prompt, which see the most keys, start first)
-    const uint32_t kv_head = blockIdx.x % a.kv_heads, rest = blockIdx.x / a.kv_heads;
-    const uint32_t head = kv_head * a.group + rest % a.group;
-    const uint32_t slot = a.tile_slots - 1 - rest / a.group;
+    // so that the tiles of one meet in one L2; the last rows of a causal
+    // prompt, which see the most keys, start first)
+    const uint32_t kv_head = blockIdx.x % a.kv_heads;
+    const uint32_t slot = a.tile_slots - 1 - blockIdx.x / a.kv_heads;
     uint32_t tile;
-    const uint32_t seq = sequence_of_slot(a.q_starts, a.n_seqs, slot, 7, &tile);
+    const uint32_t seq = sequence_of_slot(a.q_starts, a.n_seqs, slot, a.group, 7, &tile);
     const int32_t q0 = a.q_starts[seq], q1 = a.q_starts[seq + 1], k0 = a.k_starts[seq], k1 = a.k_starts[seq + 1];
     if (q0 < 0 || q1 < q0 || (uint32_t)q1 > a.n_q || k0 < 0 || k1 < k0 || (uint32_t)k1 > a.n_k) return;
-    const uint32_t n_q = q1 - q0, n_k = k1 - k0;
-    if ((uint64_t)tile * kPromptTile >= n_q) return;
-    const uint32_t row0 = tile * kPromptTile;                // of the sequence
+    const uint32_t n_q = q1 - q0, n_k = k1 - k0, n_rows = n_q * a.group;
+    if (tile > n_rows / kPromptTile || tile * kPromptTile >= n_rows) return;
+    const uint32_t row0 = tile * kPromptTile;
 
-    // keys that a row sees
-    const auto limit = [&](uint32_t row) -> uint32_t {
+    // keys that a query sees
+    const auto limit = [&](uint32_t query) -> uint32_t {
         if (!a.causal) return n_k;
-        const int64_t l = (int64_t)row + 1 + n_k - n_q;
+        const int64_t l = (int64_t)query + 1 + n_k - n_q;
         return l < 0 ? 0 : l > n_k ? n_k : (uint32_t)l;
     };
-    const uint32_t most_keys = limit(min(row0 + kPromptTile, n_q) - 1);
+    const uint32_t most_keys = limit((min(row0 + kPromptTile, n_rows) - 1) / a.group);
     uint32_t key_begin = 0, key_end = most_keys;
     if (kSplit) {
         const uint32_t per = ((n_k + a.splits - 1) / a.splits + kPromptKeys - 1) / kPromptKeys * kPromptKeys;
@@ -91,18 +92,19 @@ __global__ __launch_bounds__(kThreads, 2) void attend_prompt_kernel(PromptArgs a
         key_end = b + per < key_end ? (uint32_t)(b + per) : key_end;
     }
     const uint32_t wave_first = row0 + wave * kWaveRows, row = wave_first + col;
-    const bool real = row < n_q;
+    const bool real = row < n_rows;
+    const uint32_t query = row / a.group, head = kv_head * a.group + row % a.group;
     // (rows past the last compute on zero queries, and are not stored)
-    const uint32_t lim = real ? limit(row) : n_k;
+    const uint32_t lim = real ? limit(query) : n_k;
     // the wave's rows all see the keys below `clear`, and none from wave_end on
-    const uint32_t clear = limit(wave_first);
-    const uint32_t wave_end = wave_first < n_q ? limit(min(wave_first + kWaveRows, n_q) - 1) : 0;
+    const uint32_t clear = limit(wave_first / a.group);
+    const uint32_t wave_end = wave_first < n_rows ? limit((min(wave_first + kWaveRows, n_rows) - 1) / a.group) : 0;
 
     u32x4 q[kDSteps];
 #pragma unroll
     for (int i = 0; i < kDSteps; ++i) {
         q[i] = u32x4{0, 0, 0, 0};
-        if (real) q[i] = *reinterpret_cast<const u32x4 *>(a.q.data + (int64_t)(q0 + row) * a.q.row + head * a.q.head + 16 * i + 8 * half);
+        if (real) q[i] = *reinterpret_cast<const u32x4 *>(a.q.data + (int64_t)(q0 + query) * a.q.row + head * a.q.head + 16 * i + 8 * half);
     }
 
     f32x16 o[kDTiles];
@@ -146,14 +148,22 @@ __global__ __launch_bounds__(kThreads, 2) void attend_prompt_kernel(PromptArgs a
 
         f32x16 s[2];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            s[t] = f32x16{};
+        for (int t = 0; t < 2; ++t) s[t] = f32x16{};
 #pragma unroll
-            for (int i = 0; i < kDSteps; ++i) {
+        for (int i = 0; i < kDSteps; ++i)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
                 const u32x4 w = *reinterpret_cast<const u32x4 *>(kt + k_at<D>(32 * t + col, 2 * i + half));
                 s[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(w), as_bf16x8(q[i]), s[t], 0, 0, 0);
             }
+        // (four reads of K ahead of the products)
+        __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+#pragma unroll
+        for (int i = 0; i < 2 * kDSteps - 4; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
         }
+        __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
         if (key0 + kPromptKeys > clear) {
 #pragma unroll
             for (int t = 0; t < 2; ++t)
@@ -217,7 +227,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_prompt_kernel(PromptArgs a
     l = l_halves.x + l_halves.y;
     if (!real) return;
     if (kSplit) {
-        const uint64_t at = ((uint64_t)blockIdx.y * a.n_q + q0 + row) * a.heads + head;
+        const uint64_t at = ((uint64_t)blockIdx.y * a.n_q + q0 + query) * a.heads + head;
 #pragma unroll
         for (int i = 0; i < kDTiles; ++i)
 #pragma unroll
@@ -228,7 +238,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_prompt_kernel(PromptArgs a
         return;
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    uint16_t *const op = a.out.data + (int64_t)(q0 + row) * a.out.row + head * a.out.head;
+    uint16_t *const op = a.out.data + (int64_t)(q0 + query) * a.out.row + head * a.out.head;
 #pragma unroll
     for (int i = 0; i < kDTiles; ++i)
 #pragma unroll
@@ -237,21 +247,22 @@ __global__ __launch_bounds__(kThreads, 2) void attend_prompt_kernel(PromptArgs a
                 u32x2{pack_bf16(o[i][4 * g] * inv, o[i][4 * g + 1] * inv), pack_bf16(o[i][4 * g + 2] * inv, o[i][4 * g + 3] * inv)};
 }
 
-// Joins the parts of a tile's rows for one head: out = sum_a w_a o_a / sum_a
-// w_a l_a with w_a = 2^(m_a - max m).  D / 4 lanes a row.
+// Joins the parts of a tile's rows: out = sum_a w_a o_a / sum_a w_a l_a with
+// w_a = 2^(m_a - max m).  D / 4 lanes a row.
 constexpr uint32_t kJoinRows = 8;
 
 template <int D>
 __global__ __launch_bounds__(kJoinRows * D / 4) void join_prompt_kernel(PromptArgs a) {
     constexpr uint32_t kLanes = D / 4;
-    const uint32_t head = blockIdx.x % a.heads;
+    const uint32_t kv_head = blockIdx.x % a.kv_heads;
     uint32_t tile;
-    const uint32_t seq = sequence_of_slot(a.q_starts, a.n_seqs, blockIdx.x / a.heads, 7, &tile);
+    const uint32_t seq = sequence_of_slot(a.q_starts, a.n_seqs, blockIdx.x / a.kv_heads, a.group, 7, &tile);
     const int32_t q0 = a.q_starts[seq], q1 = a.q_starts[seq + 1], k0 = a.k_starts[seq], k1 = a.k_starts[seq + 1];
     if (q0 < 0 || q1 < q0 || (uint32_t)q1 > a.n_q || k0 < 0 || k1 < k0 || (uint32_t)k1 > a.n_k) return;
-    const uint64_t in_seq = (uint64_t)tile * kPromptTile + blockIdx.y * kJoinRows + threadIdx.x / kLanes;
-    if (in_seq >= (uint32_t)(q1 - q0)) return;
-    const uint64_t unit = (q0 + in_seq) * a.heads + head, n_units = (uint64_t)a.n_q * a.heads;
+    const uint64_t row = (uint64_t)tile * kPromptTile + blockIdx.y * kJoinRows + threadIdx.x / kLanes;
+    if (row >= (uint64_t)(q1 - q0) * a.group) return;
+    const uint32_t in_seq = (uint32_t)row / a.group, head = kv_head * a.group + (uint32_t)row % a.group;
+    const uint64_t unit = (uint64_t)(q0 + in_seq) * a.heads + head, n_units = (uint64_t)a.n_q * a.heads;
     const uint32_t d = threadIdx.x % kLanes * 4;
     const f32x2 *const ml = reinterpret_cast<const f32x2 *>(a.part_ml) + unit;
     float most = -__builtin_inff();
@@ -274,14 +285,14 @@ __global__ __launch_bounds__(kJoinRows * D / 4) void join_prompt_kernel(PromptAr
 }  // namespace
 
 hipError_t launch_attend_prompt(const PromptArgs &a, uint32_t head_dim, hipStream_t stream) {
-    const dim3 grid(a.tile_slots * a.heads, a.splits);
+    const dim3 grid(a.tile_slots * a.kv_heads, a.splits);
     const auto kernel = head_dim == 64 ? (a.splits > 1 ? attend_prompt_kernel<64, true> : attend_prompt_kernel<64, false>)
                                        : (a.splits > 1 ? attend_prompt_kernel<128, true> : attend_prompt_kernel<128, false>);
     hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.splits == 1) return e;
     hipLaunchKernelGGL(head_dim == 64 ? join_prompt_kernel<64> : join_prompt_kernel<128>,
-                       dim3(a.tile_slots * a.heads, kPromptTile / kJoinRows), dim3(kJoinRows * head_dim / 4), 0, stream, a);
+                       dim3(a.tile_slots * a.kv_heads, kPromptTile / kJoinRows), dim3(kJoinRows * head_dim / 4), 0, stream, a);
     return hipGetLastError();
 }
 

@@ -99,7 +99,7 @@ template <int D, bool kInt8>
 __global__ __launch_bounds__(kThreads) void kv_read_kernel(ReadArgs a) {
     constexpr uint32_t kLanes = D / 8;
     uint32_t tile;
-    const uint32_t s = sequence_of_slot(a.starts, a.n_seqs, blockIdx.x, kReadShift, &tile);
+    const uint32_t s = sequence_of_slot(a.starts, a.n_seqs, blockIdx.x, 1, kReadShift, &tile);
     const int32_t begin = a.starts[s], end = a.starts[s + 1];
     if (begin < 0 || end < begin || (uint32_t)end > a.n_tokens) return;
     const uint32_t n = min((uint32_t)(end - begin), a.t.width << a.c.shift);

@@ -151,11 +151,11 @@ df11_status check_token_sizes(const df11_attend_token_args &a) {
 
 // How attend_prompt splits the keys: few tiles of query rows (a piece of a
 // prompt behind a long prefix) leave compute units idle otherwise.
-uint32_t prompt_tile_slots(const df11_attend_prompt_args &a) { return (uint32_t)(a.n_q / kPromptTile + a.n_seqs); }
+uint64_t prompt_tile_slots(const df11_attend_prompt_args &a) { return a.n_q * (a.n_heads / a.n_kv_heads) / kPromptTile + a.n_seqs; }
 
 uint32_t prompt_splits(const df11_attend_prompt_args &a, int dev) {
     if (a.n_q == 0 || a.n_seqs == 0) return 1;
-    const uint64_t tiles = ceil_div(a.n_q, kPromptTile) * a.n_heads, keys = a.n_k / a.n_seqs;
+    const uint64_t tiles = ceil_div(a.n_q * a.n_heads, kPromptTile), keys = a.n_k / a.n_seqs;
     const uint64_t want = 2 * compute_units(dev) / std::max<uint64_t>(tiles, 1);
     return (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>({want, keys / 512, 32}));
 }
@@ -168,7 +168,7 @@ df11_status check_prompt_sizes(const df11_attend_prompt_args &a) {
     if (a.head_dim != 64 && a.head_dim != 128) return report_error(DF11_E_UNSUPPORTED, "head_dim %u, 64 and 128 are built", a.head_dim);
     if (a.n_kv_heads == 0 || a.n_heads == 0 || a.n_heads % a.n_kv_heads) return report_error(DF11_E_ARG, "%u heads over %u kv heads", a.n_heads, a.n_kv_heads);
     if (a.n_q > 0x7FFFFFFFu || a.n_k > 0x7FFFFFFFu) return report_error(DF11_E_UNSUPPORTED, "2^31 rows or more");
-    if (((uint64_t)a.n_q / kPromptTile + a.n_seqs) * a.n_heads > kMostGroups) return report_error(DF11_E_UNSUPPORTED, "%llu rows of %u heads", (unsigned long long)a.n_q, a.n_heads);
+    if (a.n_q * (a.n_heads / a.n_kv_heads) > 0x7FFFFFFFu || prompt_tile_slots(a) * a.n_kv_heads > kMostGroups) return report_error(DF11_E_UNSUPPORTED, "%llu rows of %u heads", (unsigned long long)a.n_q, a.n_heads);
     return DF11_OK;
 }
 
@@ -298,7 +298,7 @@ extern "C" df11_status df11_attend_prompt(const df11_attend_prompt_args *a, int 
     p.kv_heads = a->n_kv_heads;
     p.group = a->n_heads / a->n_kv_heads;
     p.causal = a->flags & DF11_ATTEND_CAUSAL;
-    p.tile_slots = prompt_tile_slots(*a);
+    p.tile_slots = (uint32_t)prompt_tile_slots(*a);
     p.splits = splits;
     p.part = (float *)a->workspace;
     p.part_ml = p.part + (uint64_t)splits * a->n_q * a->n_heads * a->head_dim;

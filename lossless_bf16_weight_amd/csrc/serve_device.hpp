@@ -60,28 +60,29 @@ __device__ __forceinline__ u32x4 bf16_of_bytes8(u32x2 w) {
     return u32x4{lo.x, lo.y, hi.x, hi.y};
 }
 
-// Tiles over packed sequences.  With tiles of 2^shift rows, sequence s is
-// given the tile slots from (starts[s] >> shift) + s up to the next
-// sequence's: at least as many as its tiles, and no prefix sum is needed.
+// Tiles over packed sequences of starts[s + 1] - starts[s] times `each` rows.
+// With tiles of 2^shift rows, sequence s is given the tile slots from
+// (starts[s] * each >> shift) + s up to the next sequence's: at least as many
+// as its tiles, and no prefix sum is needed.
 // Finds the sequence of slot t with a 64-way search (one load for up to 64
 // sequences); the same in every lane of the wave.  Returns the slot's tile
 // number within the sequence through *tile.
 __device__ __forceinline__ uint32_t sequence_of_slot(const int32_t *starts, uint32_t n_seqs, uint32_t t,
-                                                     uint32_t shift, uint32_t *tile) {
+                                                     uint32_t each, uint32_t shift, uint32_t *tile) {
     const uint32_t lane = threadIdx.x & 63u;
     uint32_t lo = 0, n = n_seqs;
     while (n > 1) {
         const uint32_t step = (n + 63u) >> 6;
         const uint32_t at = lane * step;
         bool below = false;
-        if (at < n) below = ((uint32_t)starts[lo + at] >> shift) + lo + at <= t;
+        if (at < n) below = ((uint32_t)starts[lo + at] * each >> shift) + lo + at <= t;
         const uint32_t c = (uint32_t)__builtin_popcountll(__ballot(below));
         const uint32_t skip = (c ? c - 1 : 0) * step;
         lo += skip;
         n = n - skip < step ? n - skip : step;
     }
     lo = __builtin_amdgcn_readfirstlane(lo);
-    *tile = t - (((uint32_t)starts[lo] >> shift) + lo);
+    *tile = t - (((uint32_t)starts[lo] * each >> shift) + lo);
     return lo;
 }
 

@@ -64,7 +64,7 @@ struct PromptArgs {
     float *part, *part_ml;     // [split][row][head][head_dim], then [..][2]
 };
 
-constexpr uint32_t kPromptTile = 128;    // query rows a workgroup takes
+constexpr uint32_t kPromptTile = 128;    // rows (queries of the heads of a kv head) a workgroup takes
 constexpr uint32_t kPromptKeys = 64;     // keys a step
 constexpr uint32_t kTokenKeys = 32;      // keys a wave's step
 constexpr uint32_t kTokenWaves = 4;
