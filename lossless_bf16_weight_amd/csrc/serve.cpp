@@ -297,6 +297,10 @@ extern "C" df11_status df11_attend_prompt(const df11_attend_prompt_args *a, int 
     p.heads = a->n_heads;
     p.kv_heads = a->n_kv_heads;
     p.group = a->n_heads / a->n_kv_heads;
+    // (with 2^shift < group <= 2^(shift + 1) and the multiplier rounded up from
+    // 2^(32 + shift) / group, the quotient is exact for x < 2^31)
+    p.group_shift = p.group > 1 ? 31 - (uint32_t)__builtin_clz(p.group - 1) : 0;
+    p.group_magic = p.group > 1 ? (uint32_t)((((uint64_t)1 << (32 + p.group_shift)) + p.group - 1) / p.group) : 0;
     p.causal = a->flags & DF11_ATTEND_CAUSAL;
     p.tile_slots = (uint32_t)prompt_tile_slots(*a);
     p.splits = splits;

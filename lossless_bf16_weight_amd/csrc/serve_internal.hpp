@@ -60,6 +60,7 @@ struct PromptArgs {
     const int32_t *q_starts, *k_starts;
     float log2_scale;
     uint32_t n_seqs, n_q, n_k, heads, kv_heads, group, causal;
+    uint32_t group_magic, group_shift;   // x / group = (x * group_magic >> 32) >> group_shift for group > 1, x < 2^31
     uint32_t tile_slots, splits;
     float *part, *part_ml;     // [split][row][head][head_dim], then [..][2]
 };
