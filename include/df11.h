@@ -386,12 +386,12 @@ df11_status df11_nf12_decode_batch(const void *const *host_headers, const void *
  * h / (n_heads / n_kv_heads):
  *   out = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * <q, k_j> - max)
  * over the keys j that the row sees; a row that sees none, or whose scores
- * are all minus infinity, is zero.  What is at a key that no row of the call
- * sees (the rest of a page, another sequence's rows) does not matter, be it
- * infinite or NaN.  Products are of BF16 operands (the weights p_j are rounded
- * to BF16, as the values are); scores, maxima, sums and accumulators are in 32
- * bits, and the result is rounded once.  Results do not depend on other work
- * on the GPU: sums are taken in a fixed order. */
+ * are all minus infinity, is zero.  What a row does not see (a later key, the
+ * rest of a page, another sequence's rows) does not reach it, be it infinite
+ * or NaN.  Products are of BF16 operands (attend_prompt rounds the weights p_j
+ * to BF16; attend_token takes them as the sum of two); scores, maxima, sums
+ * and accumulators are in 32 bits, and the result is rounded once.  Results do
+ * not depend on other work on the GPU: sums are taken in a fixed order. */
 
 /* Rows of heads in BF16: element (row, head, d) at data[row * row_stride +
  * head * head_stride + d].  Strides in elements, multiples of 8, at least 0;

@@ -17,6 +17,8 @@
 // is 4h + j for j < 4 and 8 + 4h + j - 4 above.  V^T comes from row-major V in
 // LDS by transposing reads.  The matrix rate and, beside it, the exponentials
 // bound it.
+#include <type_traits>
+
 #include "serve_device.hpp"
 #include "serve_internal.hpp"
 
@@ -94,7 +96,7 @@ __device__ __forceinline__ bool pick_tile(const PromptArgs &a, uint32_t slot, ui
 }
 
 template <int D, bool kSplit>
-__global__ __launch_bounds__(kThreads, 2) void attend_prompt_kernel(PromptArgs a) {
+__global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void attend_prompt_kernel(PromptArgs a) {
     constexpr int kChunks = D / 8;                           // 16-byte chunks of a row
     constexpr int kLoads = kPromptKeys * kChunks / kThreads; // chunks a thread stages
     constexpr int kDTiles = D / 32;
@@ -145,9 +147,13 @@ __global__ __launch_bounds__(kThreads, 2) void attend_prompt_kernel(PromptArgs a
     }
 
     f32x16 o[kDTiles];
+    float m, l;
+    const auto start = [&] {
 #pragma unroll
-    for (int i = 0; i < kDTiles; ++i) o[i] = f32x16{};
-    float m = -__builtin_inff(), l = 0;
+        for (int i = 0; i < kDTiles; ++i) o[i] = f32x16{};
+        m = -__builtin_inff();
+        l = 0;
+    };
 
     const uint16_t *const kp = a.k.data + (int64_t)k0 * a.k.row + kv_head * a.k.head;
     const uint16_t *const vp = a.v.data + (int64_t)k0 * a.v.row + kv_head * a.v.head;
@@ -180,7 +186,10 @@ __global__ __launch_bounds__(kThreads, 2) void attend_prompt_kernel(PromptArgs a
         __syncthreads();                           // and the others'; and all are done with the step before
     };
 
-    const auto step = [&](uint32_t key0, const uint8_t *kt, const uint8_t *vt) {
+    // One step's keys.  kCareful: values that are infinite or NaN at keys which
+    // only some rows see do not reach the others.
+    const auto step = [&](auto careful, uint32_t key0, const uint8_t *kt, const uint8_t *vt) {
+        constexpr bool kCareful = decltype(careful)::value;
         if (key0 >= wave_end) return;
 
         f32x16 s[2];
@@ -245,20 +254,72 @@ __global__ __launch_bounds__(kThreads, 2) void attend_prompt_kernel(PromptArgs a
                     const s16x4 b0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((DF11_LDS s16x4 *)(vt + v_at<D>(r, chunk) + 8 * (j & 1)));
                     const s16x4 b1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((DF11_LDS s16x4 *)(vt + v_at<D>(r + 8, chunk) + 8 * (j & 1)));
                     const u32x2 w0 = __builtin_bit_cast(u32x2, b0), w1 = __builtin_bit_cast(u32x2, b1);
-                    o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(u32x4{w0.x, w0.y, w1.x, w1.y}), as_bf16x8(p), o[i], 0, 0, 0);
+                    u32x4 w = {w0.x, w0.y, w1.x, w1.y};
+                    if (kCareful) {
+                        // Values that are not finite leave the product (0 times
+                        // one of them is not 0) and are counted apart, over the
+                        // keys that the row sees: ones where they are +inf or
+                        // NaN, and where they are -inf or NaN.
+                        u32x4 seen, up, down;
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            seen[x] = up[x] = down[x] = 0;
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                const uint32_t key = key0 + 32 * t + 16 * st + 8 * (x / 2) + 4 * half + 2 * (x % 2) + y;
+                                const uint32_t h = w[x] >> (16 * y) & 0xFFFFu, one = 0x3F80u << (16 * y);
+                                const bool odd = (h & 0x7F80u) == 0x7F80u, nan = odd && (h & 0x7Fu);
+                                if (key < lim) seen[x] |= one;
+                                if (nan || h == 0x7F80u) up[x] |= one;
+                                if (nan || h == 0xFF80u) down[x] |= one;
+                                if (odd) w[x] &= 0xFFFF0000u >> (16 * y);
+                            }
+                        }
+                        f32x16 n = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(up), as_bf16x8(seen), f32x16{}, 0, 0, 0);
+#pragma unroll
+                        for (int x = 0; x < 16; ++x)
+                            if (n[x] > 0) o[i][x] += __builtin_inff();
+                        __builtin_amdgcn_sched_barrier(0);
+                        n = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(down), as_bf16x8(seen), f32x16{}, 0, 0, 0);
+#pragma unroll
+                        for (int x = 0; x < 16; ++x)
+                            if (n[x] > 0) o[i][x] -= __builtin_inff();
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                    o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(w), as_bf16x8(p), o[i], 0, 0, 0);
                 }
             }
         }
     };
+    start();
     if (key_begin < key_end) load(key_begin, kt0, vt0);
     for (uint32_t key0 = key_begin; key0 < key_end; key0 += 2 * kPromptKeys) {
         arrived();
         if (key0 + kPromptKeys < key_end) load(key0 + kPromptKeys, kt1, vt1);
-        step(key0, kt0, vt0);
+        step(std::false_type{}, key0, kt0, vt0);
         if (key0 + kPromptKeys >= key_end) break;
         arrived();
         if (key0 + 2 * kPromptKeys < key_end) load(key0 + 2 * kPromptKeys, kt0, vt0);
-        step(key0 + kPromptKeys, kt1, vt1);
+        step(std::false_type{}, key0 + kPromptKeys, kt1, vt1);
+    }
+    if (a.causal) {
+        // A result that is not finite may come from a value that its row does
+        // not see: the product of its weight, 0, with an infinity is NaN.  Then
+        // the workgroup takes its keys once more, with care.
+        float most = 0;       // (NaN where one is)
+#pragma unroll
+        for (int i = 0; i < kDTiles; ++i)
+#pragma unroll
+            for (int x = 0; x < 16; ++x) most = __builtin_elementwise_maximum(most, __builtin_fabsf(o[i][x]));
+        if (__syncthreads_or(!(most < __builtin_inff()))) {
+            start();
+            for (uint32_t key0 = key_begin; key0 < key_end; key0 += kPromptKeys) {
+                load(key0, kt0, vt0);
+                arrived();
+                step(std::true_type{}, key0, kt0, vt0);
+                __syncthreads();
+            }
+        }
     }
     const f32x2 l_halves = with_lane_32(l);
     l = l_halves.x + l_halves.y;

@@ -88,11 +88,13 @@ def token64(q, cache, pages, lens, scale):
 
 
 def within(got, out, bound, what):
-    """Every element of got (BF16) within the bound of out; NaN where out is."""
+    """Every element of got (BF16) within the bound of out; NaN or infinite
+    where out is."""
     got = got.double().cpu()
-    nan = torch.isnan(out)
-    assert torch.equal(torch.isnan(got), nan), (what, "NaN in other places")
-    off = ((got - out).abs() - bound)[~nan]
+    odd = ~torch.isfinite(out)
+    assert torch.equal(torch.isnan(got), torch.isnan(out)), (what, "NaN in other places")
+    assert torch.equal(got[odd & ~torch.isnan(out)], out[odd & ~torch.isnan(out)]), (what, "infinities in other places")
+    off = ((got - out).abs() - bound)[~odd]
     assert off.numel() == 0 or float(off.max()) <= 1e-30, (what, float(off.max()), int((off > 0).sum()), off.numel())
 
 

@@ -142,6 +142,37 @@ def test_prompt_other_sequences_do_not_matter(bad, split):
     assert not bool(torch.isfinite(out[30:80].float()).any())
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("split", [False, True])
+def test_prompt_masked_values_do_not_matter(split, d):
+    """Causal rows before a key whose value (or key) is infinite or NaN are
+    what they are without it, in the same step of keys too; the rows that see
+    it get what the definition gives."""
+    log(f"prompt masked infinities, split {split}, head_dim {d}")
+    n, m, h, hk = (70, 1200, 4, 1) if split else (200, 200, 3, 1)
+    q, k, v = _prompt_inputs([n], [m], h, hk, d, 25)
+    a, b = U.starts_of([n]).to(DEV), U.starts_of([m]).to(DEV)
+    assert (df11.prompt_workspace(n, m, 1, h, hk, d) > 0) == split
+    out = torch.empty_like(q)
+    first = m - n
+    for at, value in ((first + 40, math.inf), (first + 41, -math.inf), (first + 62, math.nan), (m - 1, math.nan), (m - 3, math.inf)):
+        bad = v.clone()
+        bad[at, 0, d // 2] = value
+        bad[at, 0, 3] = -value
+        df11.attend_prompt(q, k, bad, a, b, out)
+        U.within(out, *U.prompt64(q, k, bad, [n], [m], True, d ** -0.5), ("value", at, value))
+        assert torch.isfinite(out[:at - first].float()).all() and not torch.isfinite(out[at - first:, :, 3].float()).any()
+    bad = v.clone()       # both infinities at one place: NaN from the second on
+    bad[first + 20, 0, 5], bad[first + 50, 0, 5] = math.inf, -math.inf
+    df11.attend_prompt(q, k, bad, a, b, out)
+    U.within(out, *U.prompt64(q, k, bad, [n], [m], True, d ** -0.5), "both")
+    bad = k.clone()
+    bad[first + 45] = math.nan
+    df11.attend_prompt(q, bad, v, a, b, out)
+    U.within(out[:45], *(x[:45] for x in U.prompt64(q, k, v, [n], [m], True, d ** -0.5)), "key")
+    assert torch.isnan(out[45:].float()).all()
+
+
 def test_prompt_starts_out_of_order():
     """Sequences whose starts are not in order within the rows are passed
     over: their rows keep what they held."""
