@@ -12,13 +12,13 @@ from __future__ import annotations
 
 import struct
 from functools import lru_cache
-from typing import TYPE_CHECKING, NamedTuple, Optional
+from typing import NamedTuple, Optional
+
+import torch
 
 from ._lib import OK, _raise, lib
 
-if TYPE_CHECKING:
-    import torch
-
+BF16, INT8, F32, I32, I64 = torch.bfloat16, torch.int8, torch.float32, torch.int32, torch.int64
 KV_BF16, KV_INT8 = 0, 1
 ATTEND_CAUSAL = 1
 
@@ -38,15 +38,14 @@ class KVCache(NamedTuple):
     n_kv_heads, page_size] (an element is code * scale).  page_size is a power
     of two from 16 to 1024, head_dim 64 or 128.  Slot page * page_size + i is
     position i of a page."""
-    k: "torch.Tensor"
-    v: "torch.Tensor"
-    k_scale: "Optional[torch.Tensor]" = None
-    v_scale: "Optional[torch.Tensor]" = None
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: Optional[torch.Tensor] = None
+    v_scale: Optional[torch.Tensor] = None
 
 
 def kv_cache(n_pages: int, n_kv_heads: int, page_size: int, head_dim: int, int8: bool = False, device="cuda") -> KVCache:
     """A cache of zeros, of BF16 words or (int8) of 8-bit codes and scales."""
-    import torch
     shape = (n_pages, n_kv_heads, page_size, head_dim)
     dtype = torch.int8 if int8 else torch.bfloat16
     k, v = (torch.zeros(shape, dtype=dtype, device=device) for _ in range(2))
@@ -56,22 +55,21 @@ def kv_cache(n_pages: int, n_kv_heads: int, page_size: int, head_dim: int, int8:
 
 
 def _cache_fields(c: KVCache):
-    import torch
     k, v, ks, vs = c
     if not isinstance(k, torch.Tensor) or not isinstance(v, torch.Tensor) or not k.is_cuda or k.dim() != 4:
         raise ValueError("cache: CUDA tensors [n_pages, n_kv_heads, page_size, head_dim] are needed")
     dev, shape, dtype = k.get_device(), k.shape, k.dtype
-    if v.shape != shape or v.dtype != dtype or v.get_device() != dev:
+    if v.shape != shape or v.dtype is not dtype or v.get_device() != dev:
         raise ValueError("cache: k and v differ in shape, dtype or device")
     if not (k.is_contiguous() and v.is_contiguous()):
         raise ValueError("cache: the pages must be contiguous")
-    if dtype == torch.bfloat16:
+    if dtype is BF16:
         if ks is not None or vs is not None:
             raise ValueError("cache: scales go with int8 pages")
         a, b, store = 0, 0, KV_BF16
-    elif dtype == torch.int8:
+    elif dtype is INT8:
         for s in (ks, vs):
-            if s is None or s.shape != shape[:3] or s.dtype != torch.float32 or s.get_device() != dev or not s.is_contiguous():
+            if s is None or s.shape != shape[:3] or s.dtype is not F32 or s.get_device() != dev or not s.is_contiguous():
                 raise ValueError("cache: int8 pages need contiguous float32 scales [n_pages, n_kv_heads, page_size]")
         a, b, store = ks.data_ptr(), vs.data_ptr(), KV_INT8
     else:
@@ -82,8 +80,7 @@ def _cache_fields(c: KVCache):
 
 def _rows(x: torch.Tensor, what: str, dev: int, d: int, n: int = -1, heads: int = -1):
     """(n, heads, fields) of a [rows, heads, head_dim] BF16 tensor."""
-    import torch
-    if not isinstance(x, torch.Tensor) or x.dtype != torch.bfloat16 or x.dim() != 3 or x.get_device() != dev:
+    if not isinstance(x, torch.Tensor) or x.dtype is not BF16 or x.dim() != 3 or x.get_device() != dev:
         raise ValueError(f"{what}: a bfloat16 tensor [rows, heads, head_dim] on cuda:{dev} is needed")
     rows, h, dim = x.shape
     s0, s1, s2 = x.stride()
@@ -95,31 +92,33 @@ def _rows(x: torch.Tensor, what: str, dev: int, d: int, n: int = -1, heads: int 
 
 
 def _index(x: torch.Tensor, what: str, dev: int, dtype, n: int):
-    import torch
-    if not isinstance(x, torch.Tensor) or x.dtype != dtype or x.dim() != 1 or x.get_device() != dev or not x.is_contiguous() or x.shape[0] != n:
+    if not isinstance(x, torch.Tensor) or x.dtype is not dtype or x.dim() != 1 or x.get_device() != dev or x.shape[0] != n or not x.is_contiguous():
         raise ValueError(f"{what}: a contiguous {dtype} tensor [{n}] on cuda:{dev} is needed")
     return x.data_ptr()
 
 
 def _table(pages: torch.Tensor, dev: int, n: int):
-    import torch
-    if not isinstance(pages, torch.Tensor) or pages.dtype != torch.int32 or pages.dim() != 2 or pages.get_device() != dev or pages.shape[0] != n or (
+    if not isinstance(pages, torch.Tensor) or pages.dtype is not I32 or pages.dim() != 2 or pages.get_device() != dev or pages.shape[0] != n or (
             pages.shape[1] > 1 and pages.stride(1) != 1):
         raise ValueError(f"pages: an int32 tensor [{n}, entries] on cuda:{dev} with contiguous rows is needed")
     return pages.data_ptr(), pages.stride(0) if n > 1 else 0, pages.shape[1], 0
+
+
+@lru_cache(maxsize=None)
+def _device(dev: int) -> torch.device:
+    return torch.device("cuda", dev)
 
 
 def _workspace(need: int, given, dev: int, stream):
     """Pointer, bytes and the tensor that holds them (kept until the launch)."""
     if need == 0:
         return 0, 0, None
-    import torch
     if given is None:
         if stream is None:
-            given = torch.empty(need, dtype=torch.uint8, device=f"cuda:{dev}")
+            given = torch.empty(need, dtype=torch.uint8, device=_device(dev))
         else:
             with torch.cuda.stream(stream):    # (the allocator reuses it in this stream's order)
-                given = torch.empty(need, dtype=torch.uint8, device=f"cuda:{dev}")
+                given = torch.empty(need, dtype=torch.uint8, device=_device(dev))
     elif given.get_device() != dev or not given.is_contiguous():
         raise ValueError(f"workspace: a contiguous tensor on cuda:{dev} is needed")
     return given.data_ptr(), given.numel() * given.element_size(), given
@@ -127,7 +126,6 @@ def _workspace(need: int, given, dev: int, stream):
 
 def _launch(fn, args: bytes, dev: int, stream):
     if stream is None:
-        import torch
         handle = torch._C._cuda_getCurrentRawStream(dev)   # (torch.cuda.current_stream(dev).cuda_stream, 1 us sooner)
     else:
         handle = stream.cuda_stream
@@ -141,11 +139,10 @@ def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tens
     head_dim] bfloat16) into slot slots[t] (int64) of the cache, quantised on
     the way where its pages are int8.  A slot outside the cache, such as -1,
     leaves its token out; the others are distinct."""
-    import torch
     dev, heads, d, c = _cache_fields(cache)
     n, _, kr = _rows(k, "k", dev, d, heads=heads)
     _, _, vr = _rows(v, "v", dev, d, n, heads)
-    _launch(lib().df11_kv_write, _WRITE.pack(*c, *kr, *vr, _index(slots, "slots", dev, torch.int64, n), n), dev, stream)
+    _launch(lib().df11_kv_write, _WRITE.pack(*c, *kr, *vr, _index(slots, "slots", dev, I64, n), n), dev, stream)
 
 
 def kv_read(cache: KVCache, pages: torch.Tensor, starts: torch.Tensor, k_out: torch.Tensor, v_out: torch.Tensor, stream=None):
@@ -153,13 +150,12 @@ def kv_read(cache: KVCache, pages: torch.Tensor, starts: torch.Tensor, k_out: to
     packed bfloat16 rows starts[s] .. of k_out and v_out ([tokens, n_kv_heads,
     head_dim]).  pages: int32 [sequences, entries], starts: int32 [sequences +
     1]."""
-    import torch
     dev, heads, d, c = _cache_fields(cache)
     n, _, kr = _rows(k_out, "k_out", dev, d, heads=heads)
     _, _, vr = _rows(v_out, "v_out", dev, d, n, heads)
     seqs = pages.shape[0]
     _launch(lib().df11_kv_read, _READ.pack(*c, *_table(pages, dev, seqs), *kr, *vr,
-                                           _index(starts, "starts", dev, torch.int32, seqs + 1), n, seqs, 0), dev, stream)
+                                           _index(starts, "starts", dev, I32, seqs + 1), n, seqs, 0), dev, stream)
 
 
 @lru_cache(maxsize=4096)
@@ -178,12 +174,11 @@ def attend_token(q: torch.Tensor, cache: KVCache, pages: torch.Tensor, lens: tor
     (int32 [sequences, entries]).  scale: 1 / sqrt(head_dim) by default.
     workspace: at least token_workspace() bytes that no other call uses
     meanwhile; by default taken from torch's allocator."""
-    import torch
     dev, hk, d, c = _cache_fields(cache)
     n, h, qr = _rows(q, "q", dev, d)
     _, _, orow = _rows(out, "out", dev, d, n, h)
     t = _table(pages, dev, n)
-    at = _index(lens, "lens", dev, torch.int32, n)
+    at = _index(lens, "lens", dev, I32, n)
     p, size, keep = _workspace(token_workspace(n, h, hk, d, c[5], t[2], dev), workspace, dev, stream)
     _launch(lib().df11_attend_token, _TOKEN.pack(*c, *t, *qr, *orow, at, p, size, n, h, d ** -0.5 if scale is None else scale, 0),
             dev, stream)
@@ -204,7 +199,6 @@ def attend_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_starts: t
     rows of out.  causal: the queries are the last of their sequence, query i
     sees the keys j <= i + n_keys - n_queries.  A row that sees no key is zero.
     starts: int32 [sequences + 1].  scale, workspace: as for attend_token."""
-    import torch
     if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 3:
         raise ValueError("q: a CUDA tensor [rows, heads, head_dim] is needed")
     dev, d = q.get_device(), q.shape[2]
@@ -215,7 +209,7 @@ def attend_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_starts: t
     seqs = q_starts.shape[0] - 1
     if seqs < 0:
         raise ValueError("q_starts: one entry more than sequences is needed")
-    a, b = _index(q_starts, "q_starts", dev, torch.int32, seqs + 1), _index(k_starts, "k_starts", dev, torch.int32, seqs + 1)
+    a, b = _index(q_starts, "q_starts", dev, I32, seqs + 1), _index(k_starts, "k_starts", dev, I32, seqs + 1)
     p, size, keep = _workspace(prompt_workspace(n, m, seqs, h, hk, d, dev), workspace, dev, stream)
     _launch(lib().df11_attend_prompt, _PROMPT.pack(*qr, *kr, *vr, *orow, a, b, p, size, n, m, seqs, h, hk, d,
                                                    ATTEND_CAUSAL if causal else 0, d ** -0.5 if scale is None else scale), dev, stream)
