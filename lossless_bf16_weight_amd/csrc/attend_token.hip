@@ -94,9 +94,6 @@ __global__ __launch_bounds__(kThreads, 3) void attend_token_kernel(TokenArgs a) 
     }
     __syncthreads();
 
-    const uint32_t in_page = (1u << a.c.shift) - 1;
-    const auto row_of = [&](uint32_t key) -> uint32_t { return table[key >> a.c.shift] + (key & in_page); };
-
     f32x4 o[kDTiles];
 #pragma unroll
     for (int i = 0; i < kDTiles; ++i) o[i] = f32x4{0, 0, 0, 0};
@@ -105,40 +102,44 @@ __global__ __launch_bounds__(kThreads, 3) void attend_token_kernel(TokenArgs a) 
 
     // A step's 32 rows of K and V, held in registers from one step before:
     // the loads of the next step are in flight while this one is computed.
-    // 16 (8, 4) lanes load a row, whole lines that nobody reads again; the
-    // wave's tile in LDS, first K's and then V's, hands them to the lanes that
-    // compute.  Rows past the end repeat the last one (their scores are
-    // masked, their V rows are cleared below).
+    // Each half of them, 16 rows, lies in one page, whole lines that nobody
+    // reads again; the wave's tile in LDS, first K's and then V's, hands them
+    // to the lanes that compute.  Rows past the end are what the page holds
+    // (their scores are masked, their V rows cleared below), halves past the
+    // end repeat the last one.
     u32x4 kw[kLoads], vw[kLoads];
     f32x4 ks[2], vs[2];
-    uint32_t rows[kLoads];
+    uint32_t half_row[2];
+    const uint32_t in_page = (1u << a.c.shift) - 1, last_half = (n - 1) & ~15u;
     const auto find_rows = [&](uint32_t key0) {
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) rows[i] = row_of(min(key0 + (i * 64 + lane) / kChunks, n - 1));
+        for (int t = 0; t < 2; ++t) {
+            const uint32_t key = min(key0 + 16 * t, last_half);
+            half_row[t] = __builtin_amdgcn_readfirstlane(table[key >> a.c.shift] + (key & in_page));
+        }
     };
-    const uint8_t *const k_pages = a.c.k + 16 * (lane % kChunks), *const v_pages = a.c.v + 16 * (lane % kChunks);
     const auto load = [&](const uint8_t *pages, u32x4 *w) {
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i)
-            w[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(pages + (uint64_t)rows[i] * kRow));
+        for (int i = 0; i < kLoads; ++i) {
+            const u32x4 *const half = reinterpret_cast<const u32x4 *>(pages + (uint64_t)half_row[2 * i / kLoads] * kRow);
+            w[i] = __builtin_nontemporal_load(half + i % (kLoads / 2) * 64 + lane);
+        }
     };
-    const auto load_scales = [&](uint32_t key0) {
+    const auto load_scales = [&] {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {       // four keys of one page
-            const uint32_t r = row_of(min(key0 + 16 * t + 4 * grp, n - 1) & ~3u);
-            ks[t] = *reinterpret_cast<const f32x4 *>(a.c.k_scale + r);
-            vs[t] = *reinterpret_cast<const f32x4 *>(a.c.v_scale + r);
+        for (int t = 0; t < 2; ++t) {
+            ks[t] = reinterpret_cast<const f32x4 *>(a.c.k_scale + half_row[t])[grp];
+            vs[t] = reinterpret_cast<const f32x4 *>(a.c.v_scale + half_row[t])[grp];
         }
     };
     uint32_t key0 = wave * kTokenKeys;
     if (key0 < n) {
         find_rows(key0);
-        load(k_pages, kw);
-        load(v_pages, vw);
-        if (kInt8) load_scales(key0);
+        load(a.c.k, kw);
+        load(a.c.v, vw);
+        if (kInt8) load_scales();
     }
     for (; key0 < n; key0 += kTokenWaves * kTokenKeys) {
-        const uint32_t next_key = min(key0 + kTokenWaves * kTokenKeys, n - 1);   // (past the end: loads that nobody uses)
         // (the tile's addresses are computed anew in each step: kept in
         // registers over the loop they would cost a wave of occupancy)
         uint32_t lane = lane0;
@@ -149,8 +150,8 @@ __global__ __launch_bounds__(kThreads, 3) void attend_token_kernel(TokenArgs a) 
             const uint32_t at = i * 64 + lane;
             *reinterpret_cast<u32x4 *>(tile + k_at<kRow>(at / kChunks, at % kChunks)) = kw[i];
         }
-        find_rows(next_key);
-        load(k_pages, kw);
+        find_rows(key0 + kTokenWaves * kTokenKeys);      // (past the end: loads that nobody uses)
+        load(a.c.k, kw);
         __builtin_amdgcn_sched_barrier(0);     // (loads of V moved up past here would not fit in registers)
         // scores of two times 16 keys: lane has keys 16 t + 4 grp + i of query col
         f32x4 s[2];
@@ -179,23 +180,35 @@ __global__ __launch_bounds__(kThreads, 3) void attend_token_kernel(TokenArgs a) 
             const uint32_t at = i * 64 + lane;
             *reinterpret_cast<u32x4 *>(tile + v_at<kRow, kInt8>(at / kChunks, at % kChunks)) = vw[i];
         }
-        load(v_pages, vw);
+        load(a.c.v, vw);
         f32x4 v_scale[2];
+        if (kInt8) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                s[t] *= ks[t] * a.log2_scale;
+                v_scale[t] = vs[t];
+            }
+            load_scales();
+        }
+        const float scale = kInt8 ? 1.0f : a.log2_scale;
+        if (key0 + kTokenKeys > n) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (key0 + 16 * t + 4 * grp + i >= n) {
+                        s[t][i] = -__builtin_inff();
+                        if (kInt8) v_scale[t][i] = 0;
+                    }
+        }
         float top = -__builtin_inff();
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const uint32_t key = key0 + 16 * t + 4 * grp;
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                s[t][i] = key + i < n ? s[t][i] * (kInt8 ? a.log2_scale * ks[t][i] : a.log2_scale) : -__builtin_inff();
-                if (kInt8) v_scale[t][i] = key + i < n ? vs[t][i] : 0.0f;
-                top = fmaxf(top, s[t][i]);
-            }
-        }
-        if (kInt8) load_scales(next_key);
+            for (int i = 0; i < 4; ++i) top = fmaxf(top, s[t][i]);
         f32x2 two = with_lane_16(top);
         two = with_lane_32(fmaxf(two.x, two.y));
-        top = fmaxf(two.x, two.y);
+        top = fmaxf(two.x, two.y) * scale;
         if (__any(top > m + kSlack)) {
             const float next = fmaxf(m, top);
             const float keep = exp2_fast(m - (next == -__builtin_inff() ? 0.0f : next));
@@ -214,7 +227,7 @@ __global__ __launch_bounds__(kThreads, 3) void attend_token_kernel(TokenArgs a) 
             float e[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                e[i] = exp2_fast(s[t][i] - base);
+                e[i] = exp2_fast(__builtin_fmaf(s[t][i], scale, -base));
                 l += e[i];
                 if (kInt8) e[i] *= v_scale[t][i];
             }
