@@ -10,7 +10,8 @@
 // Every key and value is read once and used by `group` queries, so HBM
 // traffic bounds it.  A workgroup takes up to `range` keys of one kv head
 // (work along a long sequence is split over workgroups, and a second kernel
-// joins the parts); its four waves take 32 keys a step in turn, each with its
+// joins the parts); its four waves (twelve, where they take a
+// sequence whole) take 32 keys a step in turn, each with its
 // own maximum, sum and accumulators, joined through LDS at the end.
 //
 // Matrix instructions, 16 x 16 x 32: S^T = K Q^T puts a query in each lane
@@ -26,8 +27,7 @@ namespace df11 {
 
 namespace {
 
-constexpr int kThreads = 64 * kTokenWaves;
-constexpr uint32_t kMostPages = kTokenRangeMax / 16;
+constexpr uint32_t kMostPages = (kTokenRangeMax > kTokenWholeMax ? kTokenRangeMax : kTokenWholeMax) / 16;
 
 // Where 16-byte chunk `chunk` of key row `row` lies in a wave's tile of 32
 // rows.  The exclusive or puts what is read together into different banks of
@@ -46,18 +46,19 @@ __device__ __forceinline__ uint32_t v_at(uint32_t row, uint32_t chunk) {
     return row * kRowBytes + ((chunk ^ x) << 4);
 }
 
-template <int D, bool kInt8>
-__global__ __launch_bounds__(kThreads, 3) void attend_token_kernel(TokenArgs a) {
+template <int D, bool kInt8, uint32_t kWaves>
+__global__ __launch_bounds__(64 * kWaves, 3) void attend_token_kernel(TokenArgs a) {
+    constexpr uint32_t kThreads = 64 * kWaves;
     constexpr int kRow = kInt8 ? D : 2 * D;            // bytes of a stored row
     constexpr int kChunks = kRow / 16;                 // 16-byte chunks of it
     constexpr int kLoads = kTokenKeys * kChunks / 64;  // chunks a lane loads of a step's K rows, and of its V rows
     constexpr int kDTiles = D / 16;
     constexpr int kOStride = D + 4;
     constexpr uint32_t kTileBytes = kTokenKeys * kRow;
-    constexpr uint32_t kJoinBytes = kTokenWaves * 16 * kOStride * 4;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[kTokenWaves * kTileBytes > kJoinBytes ? kTokenWaves * kTileBytes : kJoinBytes];
+    constexpr uint32_t kJoinBytes = kWaves * 16 * kOStride * 4;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kWaves * kTileBytes > kJoinBytes ? kWaves * kTileBytes : kJoinBytes];
     __shared__ uint32_t table[kMostPages];
-    __shared__ float ml[kTokenWaves][2][16];
+    __shared__ float ml[kWaves][2][16];
     __shared__ u32x4 q[D / 32][64];
 
     const uint32_t lane0 = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -84,7 +85,7 @@ __global__ __launch_bounds__(kThreads, 3) void attend_token_kernel(TokenArgs a) 
     const uint32_t head = kv_head * a.group + in_group;
     const bool real = in_group < a.group;
     // (in LDS, in the order of the operands' lanes, for the registers are full)
-    for (uint32_t i = wave; i < D / 32; i += kTokenWaves) {
+    for (uint32_t i = wave; i < D / 32; i += kWaves) {
         // words: step i holds d = 32 i + 8 grp ..; bytes: two steps share a
         // 16-byte chunk, so steps 2t and 2t + 1 hold d = 64 t + 16 grp + 0 and 8 ..
         const uint32_t d = kInt8 ? 64 * (i / 2) + 16 * grp + 8 * (i % 2) : 32 * i + 8 * grp;
@@ -139,7 +140,7 @@ __global__ __launch_bounds__(kThreads, 3) void attend_token_kernel(TokenArgs a) 
         load(a.c.v, vw);
         if (kInt8) load_scales();
     }
-    for (; key0 < n; key0 += kTokenWaves * kTokenKeys) {
+    for (; key0 < n; key0 += kWaves * kTokenKeys) {
         // (the tile's addresses are computed anew in each step: kept in
         // registers over the loop they would cost a wave of occupancy)
         uint32_t lane = lane0;
@@ -150,7 +151,7 @@ __global__ __launch_bounds__(kThreads, 3) void attend_token_kernel(TokenArgs a) 
             const uint32_t at = i * 64 + lane;
             *reinterpret_cast<u32x4 *>(tile + k_at<kRow>(at / kChunks, at % kChunks)) = kw[i];
         }
-        find_rows(key0 + kTokenWaves * kTokenKeys);      // (past the end: loads that nobody uses)
+        find_rows(key0 + kWaves * kTokenKeys);      // (past the end: loads that nobody uses)
         load(a.c.k, kw);
         __builtin_amdgcn_sched_barrier(0);     // (loads of V moved up past here would not fit in registers)
         // scores of two times 16 keys: lane has keys 16 t + 4 grp + i of query col
@@ -272,8 +273,8 @@ __global__ __launch_bounds__(kThreads, 3) void attend_token_kernel(TokenArgs a) 
     __syncthreads();                                   // (also: every wave is done with its tile)
     float *const parts = reinterpret_cast<float *>(lds);
     float most = -__builtin_inff();
-#pragma unroll
-    for (int w = 0; w < (int)kTokenWaves; ++w) most = fmaxf(most, ml[w][0][col]);
+#pragma unroll 4
+    for (int w = 0; w < (int)kWaves; ++w) most = fmaxf(most, ml[w][0][col]);
     const float base = most == -__builtin_inff() ? 0.0f : most;
     const float weight = exp2_fast(m - base);
 #pragma unroll
@@ -286,10 +287,10 @@ __global__ __launch_bounds__(kThreads, 3) void attend_token_kernel(TokenArgs a) 
         f32x4 sum = {0, 0, 0, 0};
         float most_c = -__builtin_inff(), l_c = 0;
 #pragma unroll
-        for (int w = 0; w < (int)kTokenWaves; ++w) most_c = fmaxf(most_c, ml[w][0][c]);
+        for (int w = 0; w < (int)kWaves; ++w) most_c = fmaxf(most_c, ml[w][0][c]);
         const float base_c = most_c == -__builtin_inff() ? 0.0f : most_c;
 #pragma unroll
-        for (int w = 0; w < (int)kTokenWaves; ++w) {
+        for (int w = 0; w < (int)kWaves; ++w) {
             sum += *reinterpret_cast<const f32x4 *>(parts + (w * 16 + c) * kOStride + d);
             l_c += ml[w][1][c] * exp2_fast(ml[w][0][c] - base_c);
         }
@@ -349,9 +350,15 @@ __global__ __launch_bounds__(256) void join_token_kernel(TokenArgs a) {
 
 hipError_t launch_attend_token(const TokenArgs &a, uint32_t head_dim, bool int8, hipStream_t stream) {
     const dim3 grid(a.n_seqs * a.c.kv_heads * a.q_tiles, a.splits);
-    const auto kernel = head_dim == 64 ? (int8 ? attend_token_kernel<64, true> : attend_token_kernel<64, false>)
-                                       : (int8 ? attend_token_kernel<128, true> : attend_token_kernel<128, false>);
-    hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, a);
+    if (a.whole) {
+        const auto kernel = head_dim == 64 ? (int8 ? attend_token_kernel<64, true, 12> : attend_token_kernel<64, false, 12>)
+                                           : (int8 ? attend_token_kernel<128, true, 12> : attend_token_kernel<128, false, 12>);
+        hipLaunchKernelGGL(kernel, grid, dim3(768), 0, stream, a);
+    } else {
+        const auto kernel = head_dim == 64 ? (int8 ? attend_token_kernel<64, true, 4> : attend_token_kernel<64, false, 4>)
+                                           : (int8 ? attend_token_kernel<128, true, 4> : attend_token_kernel<128, false, 4>);
+        hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, a);
+    }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.splits == 1) return e;
     hipLaunchKernelGGL(head_dim == 64 ? join_token_kernel<64> : join_token_kernel<128>, dim3(a.n_seqs * a.heads), dim3(256), 0,

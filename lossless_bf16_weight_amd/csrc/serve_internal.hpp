@@ -51,6 +51,7 @@ struct TokenArgs {
     float log2_scale;          // scale * log2(e): weights are 2^(log2_scale * <q, k> - max)
     uint32_t n_seqs, heads, group, q_tiles;   // group = heads / kv_heads, in q_tiles tiles of 16
     uint32_t range, splits;    // keys a workgroup takes, workgroups along a sequence
+    uint32_t whole;            // twelve waves a workgroup instead of four
     float *part;               // [seq][head][split][head_dim] unnormalised, then [..][2] maximum and sum
     float *part_ml;
 };
@@ -68,7 +69,7 @@ struct PromptArgs {
 constexpr uint32_t kPromptTile = 128;    // rows (queries of the heads of a kv head) a workgroup takes
 constexpr uint32_t kPromptKeys = 64;     // keys a step
 constexpr uint32_t kTokenKeys = 32;      // keys a wave's step
-constexpr uint32_t kTokenWaves = 4;
+constexpr uint32_t kTokenWholeMax = 1024; // and of one that twelve waves take whole
 constexpr uint32_t kTokenRangeMax = 1280;  // keys a workgroup takes of a long sequence
 
 hipError_t launch_kv_write(const WriteArgs &a, uint32_t head_dim, bool int8, hipStream_t stream);

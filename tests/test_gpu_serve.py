@@ -241,6 +241,8 @@ TOKENS = [
     ([300, 299], 128, 20, 1, 128),
     ([1000, 1], 1024, 16, 2, 64),
     ([5000, 4095, 4097, 0], 16, 8, 1, 128),
+    ([1023, 384, 0, 1024, 385, 31], 16, 8, 2, 128),            # taken whole by twelve waves
+    ([500, 900], 32, 20, 1, 64),
 ]
 
 

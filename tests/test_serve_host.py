@@ -132,9 +132,9 @@ def test_calls_with_nothing_to_do_succeed():
 
 
 def test_workspace_sizes():
-    assert df11.token_workspace(1, 8, 2, 128, 16, 16) == 0               # 256 positions: one part
-    parts = df11.token_workspace(1, 8, 2, 128, 16, 64) // (8 * 130 * 4)
-    assert parts > 1 and df11.token_workspace(1, 8, 2, 128, 16, 64) == parts * 8 * 130 * 4
+    assert df11.token_workspace(1, 8, 2, 128, 16, 64) == 0               # 1024 positions: taken whole
+    parts = df11.token_workspace(1, 8, 2, 128, 16, 65) // (8 * 130 * 4)
+    assert parts > 1 and df11.token_workspace(1, 8, 2, 128, 16, 65) == parts * 8 * 130 * 4
     assert df11.token_workspace(3, 8, 2, 64, 16, 4096) % (3 * 8 * 66 * 4) == 0
     assert df11.token_workspace(1, 8, 3, 128, 16, 64) == 0               # (refused by the call itself)
     assert df11.prompt_workspace(4096, 4096, 1, 32, 8, 128) == 0
@@ -160,8 +160,8 @@ def test_every_page_size_starts_ranges_with_a_page():
                 need = df11.token_workspace(seqs, 4, 2, 64, page, width)
                 parts = need // (seqs * 4 * 66 * 4) if need else 1
                 assert parts <= max(1, -(-width * page // 128)), (page, width, seqs)
-                # the longest part is a step of 128 positions, or a page, or at most 1280
-                assert parts >= width * page / max(1280, 2 * page, 256), (page, width, seqs)
+                # the longest part is at most 1280 positions, or a page or two
+                assert parts >= width * page / max(1280, 2 * page), (page, width, seqs)
 
 
 @pytest.mark.parametrize("plant", ["mask", "scale", "swap", "dropped key"])
