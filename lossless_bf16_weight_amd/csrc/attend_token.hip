@@ -46,7 +46,8 @@ __device__ __forceinline__ uint32_t v_at(uint32_t row, uint32_t chunk) {
     return row * kRowBytes + ((chunk ^ x) << 4);
 }
 
-template <int D, bool kInt8, uint32_t kWaves>
+// kOnce: no other workgroup reads the same rows (at most 16 heads share a kv head).
+template <int D, bool kInt8, uint32_t kWaves, bool kOnce>
 __global__ __launch_bounds__(64 * kWaves, 3) void attend_token_kernel(TokenArgs a) {
     constexpr uint32_t kThreads = 64 * kWaves;
     constexpr int kRow = kInt8 ? D : 2 * D;            // bytes of a stored row
@@ -63,10 +64,12 @@ __global__ __launch_bounds__(64 * kWaves, 3) void attend_token_kernel(TokenArgs 
 
     const uint32_t lane0 = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t lane = lane0, col = lane & 15u, grp = lane >> 4;
-    uint32_t at = blockIdx.x;
-    const uint32_t q_tile = at % a.q_tiles;
-    at /= a.q_tiles;
-    const uint32_t kv_head = at % a.c.kv_heads, seq = at / a.c.kv_heads;
+    // (a kv head's tiles of 16 queries go to one XCD, eight workgroups apart,
+    // so that the second finds the first one's rows in its L2)
+    const uint32_t block = blockIdx.x / (8 * a.q_tiles), in_block = blockIdx.x % (8 * a.q_tiles);
+    const uint32_t q_tile = in_block / 8, unit = 8 * block + in_block % 8;
+    if (unit >= a.n_seqs * a.c.kv_heads) return;
+    const uint32_t kv_head = unit % a.c.kv_heads, seq = unit / a.c.kv_heads;
     const uint32_t split = blockIdx.y;
 
     const uint32_t len = (uint32_t)min((int64_t)max(a.lens[seq], 0), (int64_t)a.t.width << a.c.shift);
@@ -123,7 +126,8 @@ __global__ __launch_bounds__(64 * kWaves, 3) void attend_token_kernel(TokenArgs 
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             const u32x4 *const half = reinterpret_cast<const u32x4 *>(pages + (uint64_t)half_row[2 * i / kLoads] * kRow);
-            w[i] = __builtin_nontemporal_load(half + i % (kLoads / 2) * 64 + lane);
+            const u32x4 *const from = half + i % (kLoads / 2) * 64 + lane;
+            w[i] = kOnce ? __builtin_nontemporal_load(from) : *from;
         }
     };
     const auto load_scales = [&] {
@@ -346,19 +350,25 @@ __global__ __launch_bounds__(256) void join_token_kernel(TokenArgs a) {
     }
 }
 
+template <uint32_t kWaves, bool kOnce>
+void launch_as(const TokenArgs &a, uint32_t head_dim, bool int8, dim3 grid, hipStream_t stream) {
+    const auto kernel = head_dim == 64 ? (int8 ? attend_token_kernel<64, true, kWaves, kOnce> : attend_token_kernel<64, false, kWaves, kOnce>)
+                                       : (int8 ? attend_token_kernel<128, true, kWaves, kOnce> : attend_token_kernel<128, false, kWaves, kOnce>);
+    hipLaunchKernelGGL(kernel, grid, dim3(64 * kWaves), 0, stream, a);
+}
+
+template <uint32_t kWaves>
+void launch(const TokenArgs &a, uint32_t head_dim, bool int8, dim3 grid, hipStream_t stream) {
+    if (a.q_tiles == 1) launch_as<kWaves, true>(a, head_dim, int8, grid, stream);
+    else launch_as<kWaves, false>(a, head_dim, int8, grid, stream);
+}
+
 }  // namespace
 
 hipError_t launch_attend_token(const TokenArgs &a, uint32_t head_dim, bool int8, hipStream_t stream) {
-    const dim3 grid(a.n_seqs * a.c.kv_heads * a.q_tiles, a.splits);
-    if (a.whole) {
-        const auto kernel = head_dim == 64 ? (int8 ? attend_token_kernel<64, true, 12> : attend_token_kernel<64, false, 12>)
-                                           : (int8 ? attend_token_kernel<128, true, 12> : attend_token_kernel<128, false, 12>);
-        hipLaunchKernelGGL(kernel, grid, dim3(768), 0, stream, a);
-    } else {
-        const auto kernel = head_dim == 64 ? (int8 ? attend_token_kernel<64, true, 4> : attend_token_kernel<64, false, 4>)
-                                           : (int8 ? attend_token_kernel<128, true, 4> : attend_token_kernel<128, false, 4>);
-        hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, a);
-    }
+    const dim3 grid(a.q_tiles == 1 ? a.n_seqs * a.c.kv_heads : (a.n_seqs * a.c.kv_heads + 7) / 8 * 8 * a.q_tiles, a.splits);
+    if (a.whole) launch<12>(a, head_dim, int8, grid, stream);
+    else launch<4>(a, head_dim, int8, grid, stream);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.splits == 1) return e;
     hipLaunchKernelGGL(head_dim == 64 ? join_token_kernel<64> : join_token_kernel<128>, dim3(a.n_seqs * a.heads), dim3(256), 0,
