@@ -28,6 +28,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr uint32_t kWaveRows = 32;
+constexpr int kHalves = kPromptKeys / 32;      // of a step: 32 keys are a product's rows
+constexpr int kAhead = 4;                      // reads of K ahead of the products
 
 // The K and V tiles in LDS: 16-byte chunk `chunk` of key row `row` lies at
 // place k_chunk (v_chunk) of its row, and the other way round.  K: 32 rows are
@@ -192,27 +194,27 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void attend_prompt_kerne
         constexpr bool kCareful = decltype(careful)::value;
         if (key0 >= wave_end) return;
 
-        f32x16 s[2];
+        f32x16 s[kHalves];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) s[t] = f32x16{};
+        for (int t = 0; t < kHalves; ++t) s[t] = f32x16{};
 #pragma unroll
         for (int i = 0; i < kDSteps; ++i)
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
+            for (int t = 0; t < kHalves; ++t) {
                 const u32x4 w = *reinterpret_cast<const u32x4 *>(kt + k_at<D>(32 * t + col, 2 * i + half));
                 s[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(w), as_bf16x8(q[i]), s[t], 0, 0, 0);
             }
         // (four reads of K ahead of the products)
-        __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
 #pragma unroll
-        for (int i = 0; i < 2 * kDSteps - 4; ++i) {
+        for (int i = 0; i < kHalves * kDSteps - kAhead; ++i) {
             __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
             __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
         }
-        __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, kAhead, 0);
         if (key0 + kPromptKeys > clear) {
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int t = 0; t < kHalves; ++t)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const uint32_t key = key0 + 32 * t + 8 * (i / 4) + 4 * half + i % 4;
@@ -221,7 +223,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void attend_prompt_kerne
         }
         float top = -__builtin_inff();
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < kHalves; ++t)
 #pragma unroll
             for (int i = 0; i < 16; ++i) top = fmaxf(top, s[t][i]);
         const f32x2 halves = with_lane_32(top);
@@ -236,7 +238,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void attend_prompt_kerne
         }
         const float base = m == -__builtin_inff() ? 0.0f : m;
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < kHalves; ++t) {
 #pragma unroll
             for (int st = 0; st < 2; ++st) {
                 u32x4 p;

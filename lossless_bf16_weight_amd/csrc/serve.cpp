@@ -159,15 +159,20 @@ df11_status check_token_sizes(const df11_attend_token_args &a) {
     return DF11_OK;
 }
 
-// How attend_prompt splits the keys: few tiles of query rows (a piece of a
-// prompt behind a long prefix) leave compute units idle otherwise.
+// How attend_prompt splits the keys: where the tiles of rows (a piece of a
+// prompt behind a long prefix) are fewer than compute units, into as many parts
+// as give each of these two workgroups, of 256 keys at least on average.  512
+// queries on 16384 keys take 146 us (205 us with one workgroup for each compute
+// unit, 278 us unsplit), 8 on 4096 16 us (parts of 128 keys 19 us, unsplit 66
+// us); as many tiles as compute units are better left whole (1024 queries on as
+// many keys: 24 us, in two parts 34 us).
 uint64_t prompt_tile_slots(const df11_attend_prompt_args &a) { return a.n_q * (a.n_heads / a.n_kv_heads) / kPromptTile + a.n_seqs; }
 
 uint32_t prompt_splits(const df11_attend_prompt_args &a, int dev) {
     if (a.n_q == 0 || a.n_seqs == 0) return 1;
     const uint64_t tiles = ceil_div(a.n_q * a.n_heads, kPromptTile), keys = a.n_k / a.n_seqs;
-    const uint64_t want = 2 * compute_units(dev) / std::max<uint64_t>(tiles, 1);
-    return (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>({want, keys / 512, 32}));
+    if (tiles >= compute_units(dev)) return 1;
+    return (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>({2 * compute_units(dev) / tiles, keys / 256, 32}));
 }
 
 uint64_t prompt_bytes(const df11_attend_prompt_args &a, uint32_t splits) {
