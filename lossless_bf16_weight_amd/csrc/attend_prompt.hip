@@ -75,10 +75,14 @@ __device__ __forceinline__ bool pick_tile(const PromptArgs &a, uint32_t slot, ui
         const int32_t qa = a.q_starts[at], qb = a.q_starts[at + 1], ka = a.k_starts[at], kb = a.k_starts[at + 1];
         const bool ok = lane < a.n_seqs && qa >= 0 && qb >= qa && (uint32_t)qb <= a.n_q && ka >= 0 && kb >= ka && (uint32_t)kb <= a.n_k;
         const uint32_t tiles = ok ? ((uint32_t)(qb - qa) * a.group + kPromptTile - 1) / kPromptTile : 0, keys = ok ? kb - ka : 0;
+        // (the order of two sequences whose keys differ by less than 64 does not
+        // matter, that of two lanes must be one or the other)
+        const uint32_t rank = keys & ~63u | (63u - lane);
         uint32_t before = 0;        // tiles of the sequences that come first
-        for (uint32_t j = 0; j < a.n_seqs; ++j) {
-            const uint32_t t = __builtin_amdgcn_readlane(tiles, j), k = __builtin_amdgcn_readlane(keys, j);
-            if (k > keys || (k == keys && j < lane)) before += t;
+        for (uint32_t j = 0; j < a.n_seqs; j += 8) {
+#pragma unroll
+            for (uint32_t x = 0; x < 8; ++x)
+                before += (uint32_t)__builtin_amdgcn_readlane(rank, j + x) > rank ? __builtin_amdgcn_readlane(tiles, j + x) : 0;
         }
         const uint64_t found = __ballot(slot >= before && slot - before < tiles);
         if (!found) return false;
@@ -325,8 +329,8 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void attend_prompt_kerne
     }
     const f32x2 l_halves = with_lane_32(l);
     l = l_halves.x + l_halves.y;
-    if (!real) return;
     if (kSplit) {
+        if (!real) return;
         const uint64_t at = ((uint64_t)blockIdx.y * a.n_q + q0 + query) * a.heads + head;
 #pragma unroll
         for (int i = 0; i < kDTiles; ++i)
@@ -339,12 +343,22 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void attend_prompt_kerne
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     uint16_t *const op = a.out.data + (int64_t)(q0 + query) * a.out.row + head * a.out.head;
+    // The lane has four of each eight neighbours, the lane 32 away the others:
+    // with two such eights they exchange halves and write one each.
 #pragma unroll
     for (int i = 0; i < kDTiles; ++i)
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
-            *reinterpret_cast<u32x2 *>(op + 32 * i + 8 * g + 4 * half) =
-                u32x2{pack_bf16(o[i][4 * g] * inv, o[i][4 * g + 1] * inv), pack_bf16(o[i][4 * g + 2] * inv, o[i][4 * g + 3] * inv)};
+        for (int g = 0; g < 4; g += 2) {
+            uint32_t w[2][2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const auto r = __builtin_amdgcn_permlane32_swap(pack_bf16(o[i][4 * g + 2 * x] * inv, o[i][4 * g + 2 * x + 1] * inv),
+                                                                pack_bf16(o[i][4 * g + 4 + 2 * x] * inv, o[i][4 * g + 5 + 2 * x] * inv), false, false);
+                w[0][x] = r[0];
+                w[1][x] = r[1];
+            }
+            if (real) *reinterpret_cast<u32x4 *>(op + 32 * i + 8 * (g + half)) = u32x4{w[0][0], w[0][1], w[1][0], w[1][1]};
+        }
 }
 
 // Joins the parts of a tile's rows: out = sum_a w_a o_a / sum_a w_a l_a with
