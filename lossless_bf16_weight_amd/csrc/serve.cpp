@@ -161,18 +161,21 @@ df11_status check_token_sizes(const df11_attend_token_args &a) {
 
 // How attend_prompt splits the keys: where the tiles of rows (a piece of a
 // prompt behind a long prefix) are fewer than compute units, into as many parts
-// as give each of these two workgroups, of 256 keys at least on average.  512
+// as give each of these two workgroups, of 256 keys at least on average: 512
 // queries on 16384 keys take 146 us (205 us with one workgroup for each compute
-// unit, 278 us unsplit), 8 on 4096 16 us (parts of 128 keys 19 us, unsplit 66
-// us); as many tiles as compute units are better left whole (1024 queries on as
-// many keys: 24 us, in two parts 34 us).
+// unit, 278 us unsplit), 32 on 1024 14 us (parts of 512 18 us, unsplit 22 us).
+// From a quarter as many tiles as compute units on, the join's traffic wants
+// parts of 1024 keys (512 queries on 1024: 22 us, in parts of 256 28 us), and
+// as many tiles as compute units are better left whole (1024 on 1024: 24 us, in
+// two parts 34 us).
 uint64_t prompt_tile_slots(const df11_attend_prompt_args &a) { return a.n_q * (a.n_heads / a.n_kv_heads) / kPromptTile + a.n_seqs; }
 
 uint32_t prompt_splits(const df11_attend_prompt_args &a, int dev) {
     if (a.n_q == 0 || a.n_seqs == 0) return 1;
     const uint64_t tiles = ceil_div(a.n_q * a.n_heads, kPromptTile), keys = a.n_k / a.n_seqs;
     if (tiles >= compute_units(dev)) return 1;
-    return (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>({2 * compute_units(dev) / tiles, keys / 256, 32}));
+    const uint64_t least = 4 * tiles < compute_units(dev) ? 256 : 1024;
+    return (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>({2 * compute_units(dev) / tiles, keys / least, 32}));
 }
 
 uint64_t prompt_bytes(const df11_attend_prompt_args &a, uint32_t splits) {
