@@ -26,7 +26,7 @@ namespace df11 {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr uint32_t kWaves = 4, kThreads = 64 * kWaves;
 constexpr uint32_t kWaveRows = 32;
 constexpr int kHalves = kPromptKeys / 32;      // of a step: 32 keys are a product's rows
 constexpr int kAhead = 4;                      // reads of K ahead of the products
@@ -101,6 +101,24 @@ __device__ __forceinline__ bool pick_tile(const PromptArgs &a, uint32_t slot, ui
     return *tile <= n_rows / kPromptTile && *tile * kPromptTile < n_rows;
 }
 
+// Writes a product's 32 x 32 results as BF16, the lane's column to 32 words
+// from `to`.  The lane has four of each eight neighbours, the lane 32 away the
+// others: with two such eights they exchange halves and write one each.
+__device__ __forceinline__ void store_tile(const f32x16 &o, uint16_t *to, uint32_t half, bool real) {
+#pragma unroll
+    for (int g = 0; g < 4; g += 2) {
+        uint32_t w[2][2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const auto r = __builtin_amdgcn_permlane32_swap(pack_bf16(o[4 * g + 2 * x], o[4 * g + 2 * x + 1]),
+                                                            pack_bf16(o[4 * g + 4 + 2 * x], o[4 * g + 5 + 2 * x]), false, false);
+            w[0][x] = r[0];
+            w[1][x] = r[1];
+        }
+        if (real) *reinterpret_cast<u32x4 *>(to + 8 * (g + half)) = u32x4{w[0][0], w[0][1], w[1][0], w[1][1]};
+    }
+}
+
 template <int D, bool kSplit>
 __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void attend_prompt_kernel(PromptArgs a) {
     constexpr int kChunks = D / 8;                           // 16-byte chunks of a row
@@ -111,7 +129,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void attend_prompt_kerne
     __shared__ __attribute__((aligned(16))) uint8_t vt0[kPromptKeys * D * 2], vt1[kPromptKeys * D * 2];
 
     const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const uint32_t col = lane & 31u, half = lane >> 5;
+    const uint32_t lane_of_wave = lane, col = lane & 31u, half = lane >> 5;
 
     // (workgroups are dealt to the eight XCDs in turn: kv heads vary fastest,
     // so that the tiles of one meet in one L2)
@@ -197,6 +215,11 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void attend_prompt_kerne
     const auto step = [&](auto careful, uint32_t key0, const uint8_t *kt, const uint8_t *vt) {
         constexpr bool kCareful = decltype(careful)::value;
         if (key0 >= wave_end) return;
+        // (the careful pass computes its LDS addresses in each step: there are
+        // no registers to keep them in)
+        uint32_t own = lane_of_wave;
+        if (kCareful) asm volatile("" : "+v"(own));
+        const uint32_t lane = own, col = own & 31u, half = own >> 5;
 
         f32x16 s[kHalves];
 #pragma unroll
@@ -264,18 +287,18 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void attend_prompt_kerne
                     if (kCareful) {
                         // Values that are not finite leave the product (0 times
                         // one of them is not 0) and are counted apart, over the
-                        // keys that the row sees: ones where they are +inf or
-                        // NaN, and where they are -inf or NaN.
+                        // keys that the row sees (whose score is not that of a
+                        // masked one): ones where they are +inf or NaN, and
+                        // where they are -inf or NaN.
                         u32x4 seen, up, down;
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
                             seen[x] = up[x] = down[x] = 0;
 #pragma unroll
                             for (int y = 0; y < 2; ++y) {
-                                const uint32_t key = key0 + 32 * t + 16 * st + 8 * (x / 2) + 4 * half + 2 * (x % 2) + y;
                                 const uint32_t h = w[x] >> (16 * y) & 0xFFFFu, one = 0x3F80u << (16 * y);
                                 const bool odd = (h & 0x7F80u) == 0x7F80u, nan = odd && (h & 0x7Fu);
-                                if (key < lim) seen[x] |= one;
+                                if (s[t][8 * st + 2 * x + y] != -__builtin_inff()) seen[x] |= one;
                                 if (nan || h == 0x7F80u) up[x] |= one;
                                 if (nan || h == 0xFF80u) down[x] |= one;
                                 if (odd) w[x] &= 0xFFFF0000u >> (16 * y);
@@ -330,70 +353,58 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void attend_prompt_kerne
     const f32x2 l_halves = with_lane_32(l);
     l = l_halves.x + l_halves.y;
     if (kSplit) {
-        if (!real) return;
-        const uint64_t at = ((uint64_t)blockIdx.y * a.n_q + q0 + query) * a.heads + head;
+        // as the lanes hold them, for the lanes of the join
+        const uint64_t at = ((uint64_t)blockIdx.y * gridDim.x + blockIdx.x) * kWaves + wave;
+        f32x4 *const part = reinterpret_cast<f32x4 *>(a.part) + at * (kDTiles * 4 * 64) + lane;
 #pragma unroll
         for (int i = 0; i < kDTiles; ++i)
 #pragma unroll
-            for (int g = 0; g < 4; ++g)
-                *reinterpret_cast<f32x4 *>(a.part + at * D + 32 * i + 8 * g + 4 * half) =
-                    f32x4{o[i][4 * g], o[i][4 * g + 1], o[i][4 * g + 2], o[i][4 * g + 3]};
-        if (half == 0) *reinterpret_cast<f32x2 *>(a.part_ml + 2 * at) = f32x2{m, l};
+            for (int g = 0; g < 4; ++g) part[(4 * i + g) * 64] = f32x4{o[i][4 * g], o[i][4 * g + 1], o[i][4 * g + 2], o[i][4 * g + 3]};
+        if (half == 0) reinterpret_cast<f32x2 *>(a.part_ml)[at * kWaveRows + col] = f32x2{m, l};
         return;
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     uint16_t *const op = a.out.data + (int64_t)(q0 + query) * a.out.row + head * a.out.head;
-    // The lane has four of each eight neighbours, the lane 32 away the others:
-    // with two such eights they exchange halves and write one each.
 #pragma unroll
-    for (int i = 0; i < kDTiles; ++i)
-#pragma unroll
-        for (int g = 0; g < 4; g += 2) {
-            uint32_t w[2][2];
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const auto r = __builtin_amdgcn_permlane32_swap(pack_bf16(o[i][4 * g + 2 * x] * inv, o[i][4 * g + 2 * x + 1] * inv),
-                                                                pack_bf16(o[i][4 * g + 4 + 2 * x] * inv, o[i][4 * g + 5 + 2 * x] * inv), false, false);
-                w[0][x] = r[0];
-                w[1][x] = r[1];
-            }
-            if (real) *reinterpret_cast<u32x4 *>(op + 32 * i + 8 * (g + half)) = u32x4{w[0][0], w[0][1], w[1][0], w[1][1]};
-        }
+    for (int i = 0; i < kDTiles; ++i) store_tile(o[i] * inv, op + 32 * i, half, real);
 }
 
-// Joins the parts of a tile's rows: out = sum_a w_a o_a / sum_a w_a l_a with
-// w_a = 2^(m_a - max m).  D / 4 lanes a row.
-constexpr uint32_t kJoinRows = 8;
-
+// Joins the parts of 32 rows (those of wave blockIdx.y of workgroup blockIdx.x):
+// out = sum_a w_a o_a / sum_a w_a l_a with w_a = 2^(m_a - max m).  A wave takes
+// 32 columns.
 template <int D>
-__global__ __launch_bounds__(kJoinRows * D / 4) void join_prompt_kernel(PromptArgs a) {
-    constexpr uint32_t kLanes = D / 4;
-    const uint32_t kv_head = blockIdx.x % a.kv_heads;
+__global__ __launch_bounds__(64 * D / 32) void join_prompt_kernel(PromptArgs a) {
+    constexpr int kDTiles = D / 32;
+    const uint32_t lane = threadIdx.x & 63u, i = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t col = lane & 31u, half = lane >> 5;
     uint32_t tile;
-    const uint32_t seq = sequence_of_slot(a.q_starts, a.n_seqs, blockIdx.x / a.kv_heads, a.group, 7, &tile);
-    const int32_t q0 = a.q_starts[seq], q1 = a.q_starts[seq + 1], k0 = a.k_starts[seq], k1 = a.k_starts[seq + 1];
-    if (q0 < 0 || q1 < q0 || (uint32_t)q1 > a.n_q || k0 < 0 || k1 < k0 || (uint32_t)k1 > a.n_k) return;
-    const uint64_t row = (uint64_t)tile * kPromptTile + blockIdx.y * kJoinRows + threadIdx.x / kLanes;
-    if (row >= (uint64_t)(q1 - q0) * a.group) return;
-    const uint32_t in_seq = over_group(a, (uint32_t)row), head = kv_head * a.group + (uint32_t)row - in_seq * a.group;
-    const uint64_t unit = (uint64_t)(q0 + in_seq) * a.heads + head, n_units = (uint64_t)a.n_q * a.heads;
-    const uint32_t d = threadIdx.x % kLanes * 4;
-    const f32x2 *const ml = reinterpret_cast<const f32x2 *>(a.part_ml) + unit;
+    int32_t q0, q1, k0, k1;
+    if (!pick_tile(a, blockIdx.x / a.kv_heads, &tile, &q0, &q1, &k0, &k1)) return;
+    const uint32_t first = tile * kPromptTile + blockIdx.y * kWaveRows, row = first + col, n_rows = (uint32_t)(q1 - q0) * a.group;
+    if (first >= n_rows) return;
+    const uint64_t at = (uint64_t)blockIdx.x * kWaves + blockIdx.y, step = (uint64_t)gridDim.x * kWaves;
+    const f32x2 *const ml = reinterpret_cast<const f32x2 *>(a.part_ml) + at * kWaveRows + col;
+    const f32x4 *const part = reinterpret_cast<const f32x4 *>(a.part) + (at * kDTiles + i) * 256 + lane;
     float most = -__builtin_inff();
-    for (uint32_t i = 0; i < a.splits; ++i) most = fmaxf(most, ml[i * n_units].x);
+#pragma unroll 8
+    for (uint32_t s = 0; s < a.splits; ++s) most = fmaxf(most, ml[s * step * kWaveRows].x);
     const float base = most == -__builtin_inff() ? 0.0f : most;
-    f32x4 sum = {0, 0, 0, 0};
+    f32x16 o = {};
     float l = 0;
 #pragma unroll 4
-    for (uint32_t i = 0; i < a.splits; ++i) {
-        const f32x2 p = ml[i * n_units];
+    for (uint32_t s = 0; s < a.splits; ++s) {
+        const f32x2 p = ml[s * step * kWaveRows];
         const float w = exp2_fast(p.x - base);
         l += w * p.y;
-        sum += *reinterpret_cast<const f32x4 *>(a.part + (i * n_units + unit) * D + d) * w;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const f32x4 v = __builtin_nontemporal_load(part + s * step * (kDTiles * 256) + g * 64);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) o[4 * g + x] += w * v[x];
+        }
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    *reinterpret_cast<u32x2 *>(a.out.data + (int64_t)(q0 + in_seq) * a.out.row + head * a.out.head + d) =
-        u32x2{pack_bf16(sum.x * inv, sum.y * inv), pack_bf16(sum.z * inv, sum.w * inv)};
+    const uint32_t query = over_group(a, row), head = blockIdx.x % a.kv_heads * a.group + row - query * a.group;
+    store_tile(o * (l == 0.0f ? 0.0f : 1.0f / l), a.out.data + (int64_t)(q0 + query) * a.out.row + head * a.out.head + 32 * i, half, row < n_rows);
 }
 
 }  // namespace
@@ -406,7 +417,7 @@ hipError_t launch_attend_prompt(const PromptArgs &a, uint32_t head_dim, hipStrea
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.splits == 1) return e;
     hipLaunchKernelGGL(head_dim == 64 ? join_prompt_kernel<64> : join_prompt_kernel<128>,
-                       dim3(a.tile_slots * a.kv_heads, kPromptTile / kJoinRows), dim3(kJoinRows * head_dim / 4), 0, stream, a);
+                       dim3(a.tile_slots * a.kv_heads, kWaves), dim3(2 * head_dim), 0, stream, a);
     return hipGetLastError();
 }
 

@@ -172,14 +172,14 @@ uint64_t prompt_tile_slots(const df11_attend_prompt_args &a) { return a.n_q * (a
 
 uint32_t prompt_splits(const df11_attend_prompt_args &a, int dev) {
     if (a.n_q == 0 || a.n_seqs == 0) return 1;
-    const uint64_t tiles = ceil_div(a.n_q * a.n_heads, kPromptTile), keys = a.n_k / a.n_seqs;
+    const uint64_t tiles = std::max(ceil_div(a.n_q * a.n_heads, kPromptTile), (uint64_t)a.n_seqs * a.n_kv_heads), keys = a.n_k / a.n_seqs;
     if (tiles >= compute_units(dev)) return 1;
     const uint64_t least = 4 * tiles < compute_units(dev) ? 256 : 1024;
     return (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>({2 * compute_units(dev) / tiles, keys / least, 32}));
 }
 
 uint64_t prompt_bytes(const df11_attend_prompt_args &a, uint32_t splits) {
-    return splits == 1 ? 0 : (uint64_t)splits * a.n_q * a.n_heads * (a.head_dim + 2) * sizeof(float);
+    return splits == 1 ? 0 : splits * prompt_tile_slots(a) * a.n_kv_heads * kPromptTile * (a.head_dim + 2) * sizeof(float);
 }
 
 df11_status check_prompt_sizes(const df11_attend_prompt_args &a) {
@@ -324,6 +324,6 @@ extern "C" df11_status df11_attend_prompt(const df11_attend_prompt_args *a, int 
     p.tile_slots = (uint32_t)prompt_tile_slots(*a);
     p.splits = splits;
     p.part = (float *)a->workspace;
-    p.part_ml = p.part + (uint64_t)splits * a->n_q * a->n_heads * a->head_dim;
+    p.part_ml = p.part + splits * prompt_tile_slots(*a) * a->n_kv_heads * kPromptTile * a->head_dim;
     return launched(launch_attend_prompt(p, a->head_dim, stream), "attend_prompt");
 }

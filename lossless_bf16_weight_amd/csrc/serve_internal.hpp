@@ -63,7 +63,7 @@ struct PromptArgs {
     uint32_t n_seqs, n_q, n_k, heads, kv_heads, group, causal;
     uint32_t group_magic, group_shift;   // x / group = (x * group_magic >> 32) >> group_shift for group > 1, x < 2^31
     uint32_t tile_slots, splits;
-    float *part, *part_ml;     // [split][row][head][head_dim], then [..][2]
+    float *part, *part_ml;     // [split][workgroup][wave][register / 4][lane][4], then [split][workgroup][wave][row][2]
 };
 
 constexpr uint32_t kPromptTile = 128;    // rows (queries of the heads of a kv head) a workgroup takes

@@ -139,7 +139,7 @@ def test_workspace_sizes():
     assert df11.token_workspace(1, 8, 3, 128, 16, 64) == 0               # (refused by the call itself)
     assert df11.prompt_workspace(4096, 4096, 1, 32, 8, 128) == 0
     need = df11.prompt_workspace(4, 4096, 1, 8, 2, 64)
-    assert need and need % (4 * 8 * 66 * 4) == 0
+    assert need and need % (2 * 128 * 66 * 4) == 0         # (whole tiles of 128 rows of each kv head)
     # too little, none, and misaligned
     long_q = dict(GOOD["df11_attend_prompt"], n_q=4, n_k=8192)
     need = df11.prompt_workspace(4, 8192, 1, 4, 2, 128)
