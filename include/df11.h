@@ -408,8 +408,9 @@ typedef struct {
  * page_size x head_dim elements, BF16 words or (DF11_KV_INT8) signed bytes;
  * with bytes, k_scale and v_scale are n_pages x n_kv_heads x page_size floats
  * (else NULL), and element x stands for code * scale.  page_size: a power of
- * two from 16 to 1024; head_dim: 64 or 128; all 16-byte aligned.  Slot
- * page * page_size + i is position i of a page. */
+ * two from 16 to 1024; head_dim: 64 or 128; all 16-byte aligned; fewer than
+ * 2^32 rows (n_pages * n_kv_heads * page_size).  Slot page * page_size + i is
+ * position i of a page. */
 typedef struct {
     void *k, *v;
     float *k_scale, *v_scale;
@@ -418,7 +419,7 @@ typedef struct {
 
 /* Page tables: pages[s * row_stride + i], i < width, is the page that holds
  * positions i * page_size .. of sequence s (entries past its length are not
- * read). */
+ * read).  width * page_size: at most 2^28. */
 typedef struct {
     const int32_t *pages;
     int64_t row_stride;
@@ -454,10 +455,11 @@ df11_status df11_kv_read(const df11_kv_read_args *args, int hip_device, hipStrea
 
 /* Attention of one query row a sequence (row s of q, n_heads heads, a multiple
  * of the cache's) over the first lens[s] positions of its pages, into row s of
- * out.  scale > 0.  Long sequences are split over workgroups and joined, for
- * which the call needs df11_attend_token_workspace bytes (0 for small calls;
- * the function reads the sizes alone, no pointers) of 16-byte aligned device
- * memory, that no other call uses meanwhile.  out may be q. */
+ * out.  scale is above 0 and below 2^127.  Long sequences are split over
+ * workgroups and joined, for which the call needs df11_attend_token_workspace
+ * bytes (0 for small calls; the function reads the sizes alone, no pointers)
+ * of 16-byte aligned device memory that no other call uses meanwhile.  out may
+ * be q, and overlaps nothing else. */
 typedef struct {
     df11_kv_cache cache;
     df11_page_table table;
@@ -481,9 +483,9 @@ df11_status df11_attend_token(const df11_attend_token_args *args, int hip_device
  * DF11_ATTEND_CAUSAL the queries are the last of their sequence: query i sees
  * the keys j <= i + n_keys - n_queries (so a prompt's next piece attends to
  * what came before, and with more queries than keys the first see none);
- * otherwise all.  head_dim 64 or 128, scale > 0, row strides of k and v
- * below 2^24 - 2.  Workspace: as for
- * df11_attend_token (few rows over many keys are split).  out may be q. */
+ * otherwise all.  head_dim 64 or 128; row strides of k and v below 2^24;
+ * scale, workspace (few rows over many keys are split) and out as for
+ * df11_attend_token. */
 typedef struct {
     df11_rows q, k, v, out;
     const int32_t *q_starts, *k_starts;

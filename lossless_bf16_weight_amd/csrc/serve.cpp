@@ -198,7 +198,7 @@ df11_status check_workspace(const void *p, uint64_t have, uint64_t need) {
 }
 
 df11_status check_scale(float s) {
-    return std::isfinite(s) && s > 0 ? DF11_OK : report_error(DF11_E_ARG, "scale: a finite number above 0 is needed");
+    return s > 0 && std::isfinite(log2_scale(s)) ? DF11_OK : report_error(DF11_E_ARG, "scale: a finite number above 0 is needed (and below 2^127)");
 }
 
 }  // namespace

@@ -82,7 +82,7 @@ REFUSED = [
     ("slots", 0, E_ARG), ("slots", P + 4, E_ARG), ("n_tokens", 1 << 40, E_UNSUPPORTED), ("starts", 0, E_ARG), ("starts", P + 2, E_ARG),
     ("table.pages", 0, E_ARG), ("table.pages", P + 2, E_ARG), ("table.row_stride", -1, E_ARG), ("table.width", 0, E_ARG),
     ("table.width", 1 << 26, E_UNSUPPORTED), ("lens", 0, E_ARG), ("scale", 0.0, E_ARG), ("scale", -1.0, E_ARG),
-    ("scale", float("nan"), E_ARG), ("scale", float("inf"), E_ARG), ("n_heads", 3, E_ARG), ("n_heads", 0, E_ARG),
+    ("scale", 3e38, E_ARG), ("scale", float("nan"), E_ARG), ("scale", float("inf"), E_ARG), ("n_heads", 3, E_ARG), ("n_heads", 0, E_ARG),
     ("n_kv_heads", 0, E_ARG), ("head_dim", 80, E_UNSUPPORTED), ("flags", 2, E_ARG), ("n_q", 1 << 33, E_UNSUPPORTED),
     ("n_k", 1 << 33, E_UNSUPPORTED), ("q_starts", 0, E_ARG), ("k_starts", P + 1, E_ARG), ("n_seqs", (1 << 32) - 1, E_UNSUPPORTED),
 ]
