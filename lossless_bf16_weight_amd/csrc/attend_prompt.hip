@@ -62,43 +62,51 @@ __device__ __forceinline__ uint32_t over_group(const PromptArgs &a, uint32_t row
 }
 
 // The tile of rows that work item `slot` stands for, and its sequence; false
-// where there is none.  The heaviest come first, or a few of them would keep
-// the others' compute units waiting at the end: up to 64 sequences in the order
-// of their keys (11 of up to 2113 tokens: 188 us, in the order given 203 us),
-// and in each the last tile, which sees the most keys of a causal prompt.
+// where there is none.  The last tiles of a sequence, which see the most keys
+// of a causal prompt, come first, and so do the sequences with the most keys
+// where there are few: a heavy tile at the end would keep the others' compute
+// units waiting (11 sequences of up to 2113 tokens, shortest first: 68 us,
+// unranked 76 us).  With more sequences it levels out, and each workgroup pays
+// for the ranking of all of them (64 of 1024 tokens: 719 us, ranked 782 us; 64
+// of 256: 99 and 119 us).
+constexpr uint32_t kRanked = 16;
+
 __device__ __forceinline__ bool pick_tile(const PromptArgs &a, uint32_t slot, uint32_t *tile, int32_t *q0, int32_t *q1,
                                           int32_t *k0, int32_t *k1) {
-    uint32_t s;
-    if (a.n_seqs <= 64) {
-        // a lane a sequence: one trip to memory gives all starts
-        const uint32_t lane = threadIdx.x & 63u, at = min(lane, a.n_seqs - 1);
-        const int32_t qa = a.q_starts[at], qb = a.q_starts[at + 1], ka = a.k_starts[at], kb = a.k_starts[at + 1];
-        const bool ok = lane < a.n_seqs && qa >= 0 && qb >= qa && (uint32_t)qb <= a.n_q && ka >= 0 && kb >= ka && (uint32_t)kb <= a.n_k;
-        const uint32_t tiles = ok ? ((uint32_t)(qb - qa) * a.group + kPromptTile - 1) / kPromptTile : 0, keys = ok ? kb - ka : 0;
+    if (a.n_seqs > 64) {
+        const uint32_t s = sequence_of_slot(a.q_starts, a.n_seqs, a.tile_slots - 1 - slot, a.group, 7, tile);
+        *q0 = a.q_starts[s], *q1 = a.q_starts[s + 1], *k0 = a.k_starts[s], *k1 = a.k_starts[s + 1];
+        if (*q0 < 0 || *q1 < *q0 || (uint32_t)*q1 > a.n_q || *k0 < 0 || *k1 < *k0 || (uint32_t)*k1 > a.n_k) return false;
+        const uint32_t n_rows = (uint32_t)(*q1 - *q0) * a.group;
+        return *tile <= n_rows / kPromptTile && *tile * kPromptTile < n_rows;
+    }
+    // a lane a sequence: one trip to memory gives all starts
+    const uint32_t lane = threadIdx.x & 63u, at = min(lane, a.n_seqs - 1);
+    const int32_t qa = a.q_starts[at], qb = a.q_starts[at + 1], ka = a.k_starts[at], kb = a.k_starts[at + 1];
+    const bool ok = lane < a.n_seqs && qa >= 0 && qb >= qa && (uint32_t)qb <= a.n_q && ka >= 0 && kb >= ka && (uint32_t)kb <= a.n_k;
+    const uint32_t tiles = ok ? ((uint32_t)(qb - qa) * a.group + kPromptTile - 1) / kPromptTile : 0;
+    uint32_t before = 0;        // slots before the sequence's
+    if (a.n_seqs <= kRanked) {
         // (the order of two sequences whose keys differ by less than 64 does not
         // matter, that of two lanes must be one or the other)
-        const uint32_t rank = keys & ~63u | (63u - lane);
-        uint32_t before = 0;        // tiles of the sequences that come first
+        const uint32_t rank = (ok ? kb - ka : 0) & ~63u | (63u - lane);
         for (uint32_t j = 0; j < a.n_seqs; j += 8) {
 #pragma unroll
             for (uint32_t x = 0; x < 8; ++x)
                 before += (uint32_t)__builtin_amdgcn_readlane(rank, j + x) > rank ? __builtin_amdgcn_readlane(tiles, j + x) : 0;
         }
-        const uint64_t found = __ballot(slot >= before && slot - before < tiles);
-        if (!found) return false;
-        s = (uint32_t)__builtin_ctzll(found);
-        *tile = __builtin_amdgcn_readlane(tiles, s) - 1 - (slot - __builtin_amdgcn_readlane(before, s));
-        *q0 = __builtin_amdgcn_readlane(qa, s);
-        *q1 = __builtin_amdgcn_readlane(qb, s);
-        *k0 = __builtin_amdgcn_readlane(ka, s);
-        *k1 = __builtin_amdgcn_readlane(kb, s);
-        return true;
+    } else {
+        before = ((uint32_t)qa * a.group >> 7) + lane;      // (at least as many slots as tiles: see sequence_of_slot)
     }
-    s = sequence_of_slot(a.q_starts, a.n_seqs, a.tile_slots - 1 - slot, a.group, 7, tile);
-    *q0 = a.q_starts[s], *q1 = a.q_starts[s + 1], *k0 = a.k_starts[s], *k1 = a.k_starts[s + 1];
-    if (*q0 < 0 || *q1 < *q0 || (uint32_t)*q1 > a.n_q || *k0 < 0 || *k1 < *k0 || (uint32_t)*k1 > a.n_k) return false;
-    const uint32_t n_rows = (uint32_t)(*q1 - *q0) * a.group;
-    return *tile <= n_rows / kPromptTile && *tile * kPromptTile < n_rows;
+    const uint64_t found = __ballot(slot >= before && slot - before < tiles);
+    if (!found) return false;
+    const uint32_t s = (uint32_t)__builtin_ctzll(found);
+    *tile = __builtin_amdgcn_readlane(tiles, s) - 1 - (slot - __builtin_amdgcn_readlane(before, s));
+    *q0 = __builtin_amdgcn_readlane(qa, s);
+    *q1 = __builtin_amdgcn_readlane(qb, s);
+    *k0 = __builtin_amdgcn_readlane(ka, s);
+    *k1 = __builtin_amdgcn_readlane(kb, s);
+    return true;
 }
 
 // Writes a product's 32 x 32 results as BF16, the lane's column to 32 words

@@ -70,6 +70,23 @@ def test_prompt(case):
     U.within(out, *U.prompt64(q, k, v, q_lens, k_lens, causal, d ** -0.5), case)
 
 
+@pytest.mark.parametrize("n", [1, 15, 16, 17, 40, 63, 64, 65, 130])
+def test_prompt_counts_of_sequences(n):
+    """The ways to find a work item's sequence; a third of the sequences empty,
+    whole and ragged tiles, with keys in one part and in several."""
+    log(f"prompt of {n} sequences")
+    h, hk, d = 6, 2, 64
+    q_lens = [(0, 43, 1, 128, 0, 86, 17, 0, 129)[(5 * i + n) % 9] for i in range(n)]
+    for extra in (0, 1200):
+        k_lens = [m + extra * (i % 13 == 3) for i, m in enumerate(q_lens)]
+        q, k, v = _prompt_inputs(q_lens, k_lens, h, hk, d, n)
+        buf, out = _guarded(q.shape)
+        df11.attend_prompt(q, k, v, U.starts_of(q_lens).to(DEV), U.starts_of(k_lens).to(DEV), out)
+        torch.cuda.synchronize()
+        _guards_hold(buf)
+        U.within(out, *U.prompt64(q, k, v, q_lens, k_lens, True, d ** -0.5), (n, extra))
+
+
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("n,m", [(1, 4096), (40, 3000), (130, 2049)])
 def test_prompt_split_over_keys(n, m, d):
