@@ -109,6 +109,20 @@ __device__ __forceinline__ bool pick_tile(const PromptArgs &a, uint32_t slot, ui
     return true;
 }
 
+// Keys of a sequence that a query sees.
+__device__ __forceinline__ uint32_t keys_seen(const PromptArgs &a, uint32_t query, uint32_t n_q, uint32_t n_k) {
+    if (!a.causal) return n_k;
+    const int64_t l = (int64_t)query + 1 + n_k - n_q;
+    return l < 0 ? 0 : l > n_k ? n_k : (uint32_t)l;
+}
+
+// Keys of one part of a sequence's.  A part that begins past the keys which its
+// tile sees is neither written nor read, but for the first.
+__device__ __forceinline__ uint32_t keys_a_part(const PromptArgs &a, uint32_t n_k) {
+    // (the quotient, or one more; whole steps, above n_k / splits)
+    return max((__umulhi(n_k, a.split_magic) + kPromptKeys) / kPromptKeys * kPromptKeys, kPromptPartKeys);
+}
+
 // Writes a product's 32 x 32 results as BF16, the lane's column to 32 words
 // from `to`.  The lane has four of each eight neighbours, the lane 32 away the
 // others: with two such eights they exchange halves and write one each.
@@ -148,19 +162,15 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void attend_prompt_kerne
     const uint32_t n_q = q1 - q0, n_k = k1 - k0, n_rows = n_q * a.group;
     const uint32_t row0 = tile * kPromptTile;
 
-    // keys that a query sees
-    const auto limit = [&](uint32_t query) -> uint32_t {
-        if (!a.causal) return n_k;
-        const int64_t l = (int64_t)query + 1 + n_k - n_q;
-        return l < 0 ? 0 : l > n_k ? n_k : (uint32_t)l;
-    };
+    const auto limit = [&](uint32_t query) { return keys_seen(a, query, n_q, n_k); };
     const uint32_t most_keys = limit(over_group(a, min(row0 + kPromptTile, n_rows) - 1));
     uint32_t key_begin = 0, key_end = most_keys;
     if (kSplit) {
-        const uint32_t per = ((n_k + a.splits - 1) / a.splits + kPromptKeys - 1) / kPromptKeys * kPromptKeys;
+        const uint32_t per = keys_a_part(a, n_k);
         const uint64_t b = (uint64_t)blockIdx.y * per;
-        key_begin = b < key_end ? (uint32_t)b : key_end;
-        key_end = b + per < key_end ? (uint32_t)(b + per) : key_end;
+        if (b >= most_keys && b) return;
+        key_begin = (uint32_t)b;
+        key_end = b + per < most_keys ? (uint32_t)(b + per) : most_keys;
     }
     const uint32_t wave_first = row0 + wave * kWaveRows, row = wave_first + col;
     const bool real = row < n_rows;
@@ -378,37 +388,57 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void attend_prompt_kerne
 }
 
 // Joins the parts of 32 rows (those of wave blockIdx.y of workgroup blockIdx.x):
-// out = sum_a w_a o_a / sum_a w_a l_a with w_a = 2^(m_a - max m).  A wave takes
-// 32 columns.
+// out = sum_a w_a o_a / sum_a w_a l_a with w_a = 2^(m_a - max m), the maximum
+// taken as the parts come.  A wave takes 32 columns.  It is bound by the way
+// to memory: the first parts are asked for before the number of parts is known.
 template <int D>
 __global__ __launch_bounds__(64 * D / 32) void join_prompt_kernel(PromptArgs a) {
     constexpr int kDTiles = D / 32;
+    constexpr int kBatch = 2;       // parts in flight
     const uint32_t lane = threadIdx.x & 63u, i = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t col = lane & 31u, half = lane >> 5;
+    const uint64_t at = (uint64_t)blockIdx.x * kWaves + blockIdx.y, step = (uint64_t)gridDim.x * kWaves;
+    const f32x2 *const ml = reinterpret_cast<const f32x2 *>(a.part_ml) + at * kWaveRows + col;
+    const f32x4 *const part = reinterpret_cast<const f32x4 *>(a.part) + (at * kDTiles + i) * 256 + lane;
+    f32x2 p[kBatch];
+    f32x4 v[kBatch][4];
+    const auto load = [&](uint32_t s, uint32_t parts) {
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x) {
+            const uint32_t from = min(s + x, parts - 1);
+            p[x] = ml[from * step * kWaveRows];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) v[x][g] = __builtin_nontemporal_load(part + from * step * (kDTiles * 256) + g * 64);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    load(0, a.splits);
     uint32_t tile;
     int32_t q0, q1, k0, k1;
     if (!pick_tile(a, blockIdx.x / a.kv_heads, &tile, &q0, &q1, &k0, &k1)) return;
     const uint32_t first = tile * kPromptTile + blockIdx.y * kWaveRows, row = first + col, n_rows = (uint32_t)(q1 - q0) * a.group;
     if (first >= n_rows) return;
-    const uint64_t at = (uint64_t)blockIdx.x * kWaves + blockIdx.y, step = (uint64_t)gridDim.x * kWaves;
-    const f32x2 *const ml = reinterpret_cast<const f32x2 *>(a.part_ml) + at * kWaveRows + col;
-    const f32x4 *const part = reinterpret_cast<const f32x4 *>(a.part) + (at * kDTiles + i) * 256 + lane;
-    float most = -__builtin_inff();
-#pragma unroll 8
-    for (uint32_t s = 0; s < a.splits; ++s) most = fmaxf(most, ml[s * step * kWaveRows].x);
-    const float base = most == -__builtin_inff() ? 0.0f : most;
+    const uint32_t n_k = k1 - k0, most_keys = keys_seen(a, over_group(a, min((tile + 1) * kPromptTile, n_rows) - 1), q1 - q0, n_k);
+    const uint32_t per = keys_a_part(a, n_k), parts = max(1, __builtin_popcountll(__ballot(lane < a.splits && lane * per < most_keys)));
     f32x16 o = {};
-    float l = 0;
-#pragma unroll 4
-    for (uint32_t s = 0; s < a.splits; ++s) {
-        const f32x2 p = ml[s * step * kWaveRows];
-        const float w = exp2_fast(p.x - base);
-        l += w * p.y;
+    float l = 0, m = -__builtin_inff();
+    for (uint32_t s = 0; s < parts; s += kBatch) {
+        if (s) load(s, parts);
+        float next = m;
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const f32x4 v = __builtin_nontemporal_load(part + s * step * (kDTiles * 256) + g * 64);
+        for (int x = 0; x < kBatch; ++x)
+            if (s + x < parts) next = fmaxf(next, p[x].x);
+        const float base = next == -__builtin_inff() ? 0.0f : next, keep = exp2_fast(m - base);
+        m = next;
+        l *= keep;
+        o *= keep;
 #pragma unroll
-            for (int x = 0; x < 4; ++x) o[4 * g + x] += w * v[x];
+        for (int x = 0; x < kBatch; ++x) {
+            if (s + x >= parts) break;      // (a part past the last was not written)
+            const float w = exp2_fast(p[x].x - base);
+            l += w * p[x].y;
+#pragma unroll
+            for (int y = 0; y < 16; ++y) o[y] += w * v[x][y / 4][y % 4];
         }
     }
     const uint32_t query = over_group(a, row), head = blockIdx.x % a.kv_heads * a.group + row - query * a.group;

@@ -161,20 +161,21 @@ df11_status check_token_sizes(const df11_attend_token_args &a) {
 
 // How attend_prompt splits the keys: where the tiles of rows (a piece of a
 // prompt behind a long prefix) are fewer than compute units, into as many parts
-// as give each of these two workgroups, of 256 keys at least on average: 512
-// queries on 16384 keys take 146 us (205 us with one workgroup for each compute
-// unit, 278 us unsplit), 32 on 1024 14 us (parts of 512 18 us, unsplit 22 us).
-// From a quarter as many tiles as compute units on, the join's traffic wants
-// parts of 1024 keys (512 queries on 1024: 22 us, in parts of 256 28 us), and
-// as many tiles as compute units are better left whole (1024 on 1024: 24 us, in
-// two parts 34 us).
+// as give each of these two workgroups: 512 queries on 16384 keys take 148 us
+// (205 us with one workgroup for each compute unit, 278 us unsplit).  A part
+// has 256 keys at least on average where tiles are fewer than a quarter of the
+// compute units (32 queries on 1024 keys 14 us, in parts of 512 17 us, unsplit
+// 22 us), 512 where they are fewer than half (256 on 1024: 19 us, unsplit 22
+// us; eight tokens on 2000 keys each 23 us, unsplit 38 us), 1024 above, for the
+// join's traffic (512 on 1024: 23 us, in parts of 256 28 us).  As many tiles as
+// compute units are better left whole (1024 on 1024: 24 us, in two parts 34 us).
 uint64_t prompt_tile_slots(const df11_attend_prompt_args &a) { return a.n_q * (a.n_heads / a.n_kv_heads) / kPromptTile + a.n_seqs; }
 
 uint32_t prompt_splits(const df11_attend_prompt_args &a, int dev) {
     if (a.n_q == 0 || a.n_seqs == 0) return 1;
     const uint64_t tiles = std::max(ceil_div(a.n_q * a.n_heads, kPromptTile), (uint64_t)a.n_seqs * a.n_kv_heads), keys = a.n_k / a.n_seqs;
     if (tiles >= compute_units(dev)) return 1;
-    const uint64_t least = 4 * tiles < compute_units(dev) ? 256 : 1024;
+    const uint64_t least = 4 * tiles < compute_units(dev) ? kPromptPartKeys : 2 * tiles < compute_units(dev) ? 512 : 1024;
     return (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>({2 * compute_units(dev) / tiles, keys / least, 32}));
 }
 
@@ -323,6 +324,7 @@ extern "C" df11_status df11_attend_prompt(const df11_attend_prompt_args *a, int 
     p.causal = a->flags & DF11_ATTEND_CAUSAL;
     p.tile_slots = (uint32_t)prompt_tile_slots(*a);
     p.splits = splits;
+    p.split_magic = splits > 1 ? (uint32_t)((((uint64_t)1 << 32) + splits - 1) / splits) : 0;
     p.part = (float *)a->workspace;
     p.part_ml = p.part + splits * prompt_tile_slots(*a) * a->n_kv_heads * kPromptTile * a->head_dim;
     return launched(launch_attend_prompt(p, a->head_dim, stream), "attend_prompt");

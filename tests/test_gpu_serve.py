@@ -88,7 +88,7 @@ def test_prompt_counts_of_sequences(n):
 
 
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("n,m", [(1, 4096), (40, 3000), (130, 2049)])
+@pytest.mark.parametrize("n,m", [(1, 4096), (40, 3000), (130, 2049), (700, 1600), (900, 650)])
 def test_prompt_split_over_keys(n, m, d):
     """Few rows over many keys: the keys are split and the parts joined, the
     second sequence too short for all parts."""
