@@ -225,7 +225,11 @@ __global__ __launch_bounds__(64 * kWaves, 3) void attend_token_kernel(TokenArgs 
         const float base = m == -__builtin_inff() ? 0.0f : m;
         // weights as the sum of two BF16 operands, for the product has matrix
         // rate to spare: rounded once they would add as much error as the
-        // rounding of the result (0.0027 of the norm against 0.0017)
+        // rounding of the result (0.0027 of the norm against 0.0017).  The
+        // first is the BF16 number before the one that the weight begins with:
+        // what is left for the second is then above zero and within 2^-14 of
+        // the weight as a BF16, and a value that is infinite times both is
+        // that infinity (times 0 or less it would make the result NaN).
         u32x4 p, p_low;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -238,7 +242,8 @@ __global__ __launch_bounds__(64 * kWaves, 3) void attend_token_kernel(TokenArgs 
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const uint32_t w = pack_bf16(e[2 * i], e[2 * i + 1]);
+                const uint32_t cut = __float_as_uint(e[2 * i]) >> 16 | (__float_as_uint(e[2 * i + 1]) & 0xFFFF0000u);
+                const uint32_t w = __builtin_bit_cast(uint32_t, __builtin_elementwise_sub_sat(__builtin_bit_cast(u16x2, cut), u16x2{1, 1}));
                 p[2 * t + i] = w;
                 p_low[2 * t + i] = pack_bf16(e[2 * i] - __uint_as_float(w << 16), e[2 * i + 1] - __uint_as_float(w & 0xFFFF0000u));
             }

@@ -278,6 +278,26 @@ def test_token(case, int8):
         U.within(out, *U.token64(q, cache, pages, lens, d ** -0.5), (case, int8, poison))
 
 
+@pytest.mark.parametrize("lens", [[1, 2, 40, 300], [900, 31], [6000, 40]])
+def test_token_infinite_values_that_are_seen(lens):
+    """Values that are infinite at keys that count: the result is infinite
+    there, and NaN where both infinities meet; others stay."""
+    log(f"token with infinite values {lens}")
+    ps, h, hk, d = 16, 4, 2, 128
+    cache, pages = _cache(lens, ps, hk, d, False, 43)
+    at = [(j // ps, j % ps) for j in (0, 1, 17, 30)]
+    for s, n in enumerate(lens):
+        for column, ((page, pos), value) in enumerate(zip(at, (math.inf, -math.inf, math.inf, math.nan))):
+            if page * ps + pos < n:
+                cache.v[pages[s, page], 0, pos, column] = value
+        if n > 30:
+            cache.v[pages[s, 0], 1, 2, 64], cache.v[pages[s, 1], 1, 3, 64] = math.inf, -math.inf
+    q = _rand((len(lens), h, d), 47, 0.5)
+    out = torch.empty_like(q)
+    df11.attend_token(q, cache, pages, torch.tensor(lens, dtype=torch.int32, device=DEV), out)
+    U.within(out, *U.token64(q, cache, pages, lens, d ** -0.5), lens)
+
+
 @pytest.mark.parametrize("int8", [False, True])
 def test_token_split_and_workspace(int8):
     """A wide table splits the work; short sequences leave most parts empty.
