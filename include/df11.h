@@ -380,7 +380,7 @@ df11_status df11_nf12_decode_batch(const void *const *host_headers, const void *
  * arrays of indexes: a page number past the cache reads the last page, a
  * length past the table's pages counts as theirs, a slot outside the cache is
  * not written, and a sequence whose starts are not in order within the rows
- * is passed over.
+ * is passed over (others of the call, whose rows then overlap, may be too).
  *
  * Attention of query row i of a sequence, per query head h and its kv head
  * h / (n_heads / n_kv_heads):

@@ -10,9 +10,18 @@
 // Every key and value is read once and used by `group` queries, so HBM
 // traffic bounds it.  A workgroup takes up to `range` keys of one kv head
 // (work along a long sequence is split over workgroups, and a second kernel
-// joins the parts); its four waves (twelve, where they take a
-// sequence whole) take 32 keys a step in turn, each with its
-// own maximum, sum and accumulators, joined through LDS at the end.
+// joins the parts); its four waves (twelve, where they take a sequence whole)
+// take 32 keys a step in turn, each with its own maximum, sum and
+// accumulators, joined through LDS at the end.  Three workgroups of four waves
+// run on a compute unit at a time, and each wave holds the next step's 16 KB of
+// keys and values in registers: 192 KB of loads in flight there.  LDS only
+// turns a wave's own rows around (a wave waits for no other until the end).
+//
+// Measured with 32 heads over 8 kv heads of 128, join included: 64 sequences
+// of up to 4096 tokens 94 us (505 MB, 5.6 TB/s in the first kernel's 90 us),
+// two of up to 100,001 tokens 84 us (440 MB, 5.5 TB/s in 80), 48 of up to
+// 16,384 in 8 bits 138 us (734 MB, 5.3 TB/s).  A read of the same bytes with
+// nothing computed reaches 6.6 TB/s.
 //
 // Matrix instructions, 16 x 16 x 32: S^T = K Q^T puts a query in each lane
 // (column) and four keys in its registers, so that the row statistics are per

@@ -10,7 +10,12 @@
 // of NaN or infinity and codes 0, and reads back as NaN.
 //
 // Both kernels are bound by HBM traffic: a lane moves 16 bytes of BF16 a step
-// (a row of 128 is 16 lanes), several steps in flight.
+// (a row of 128 is 16 lanes), several steps in flight.  Measured with 8 kv
+// heads of 128: 20,288 tokens written as words 28 us (166 MB read and written,
+// 5.9 TB/s; a copy of 2 GiB reaches 4.9), 5,520 tokens written in 8 bits 9.8 us
+// and read back 8.8 us (34 MB; an empty kernel takes 2.5 us of it), 118,617
+// tokens read back from 8 bits 139 us (736 MB, 5.3 TB/s).  64 tokens are
+// written in 2.6 us.
 #include "serve_device.hpp"
 #include "serve_internal.hpp"
 
@@ -94,7 +99,10 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(WriteArgs a) {
 }
 
 // A workgroup reads back 16 tokens of all heads: it writes whole rows, and
-// reads 16 neighbouring rows of each head's part of a page.
+// reads 16 neighbouring rows of each head's part of a page (one head a
+// workgroup, which writes a row's part at a time: 193 us for the 139 above).
+// Stores past the caches are 5% faster there and 20% slower for a few thousand
+// tokens, which the next kernel then finds in the L2.
 template <int D, bool kInt8>
 __global__ __launch_bounds__(kThreads) void kv_read_kernel(ReadArgs a) {
     constexpr uint32_t kLanes = D / 8;
