@@ -25,7 +25,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWriteUnroll = 2, kReadUnroll = 4;
-constexpr uint32_t kReadShift = 4;    // 16 tokens a workgroup
+constexpr uint32_t kReadShift = 4;
+static_assert(kReadTile == 1u << kReadShift && kReadSlice == 64 * kReadUnroll);
 
 // Maximum over the kLanes neighbouring lanes that hold a row, in each of them.
 template <int kLanes>
@@ -98,60 +99,65 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(WriteArgs a) {
     }
 }
 
-// A workgroup reads back 16 tokens of all heads: it writes whole rows, and
-// reads 16 neighbouring rows of each head's part of a page (one head a
-// workgroup, which writes a row's part at a time: 193 us for the 139 above).
-// Stores past the caches are 5% faster there and 20% slower for a few thousand
-// tokens, which the next kernel then finds in the L2.
+// A tile is 16 tokens of all heads: whole rows to write, and 16 neighbouring
+// rows of each head's part of a page to read (a workgroup for one head, which
+// writes a part of each row, takes 1.4 times as long).  A wave takes kReadSlice
+// 16-byte chunks of it, four a lane, in the order of the rows that are written:
+// few tokens of many heads are many waves' work (35 sequences, 2000 tokens of 24
+// heads in all: 8 us, with a workgroup for a tile 15 us), and of one head the
+// lanes have enough to do (56,000 tokens: 11 us, 16 us).  Stores past the caches
+// are slower for a few thousand tokens, which the next kernel then finds in the
+// L2.
 template <int D, bool kInt8>
 __global__ __launch_bounds__(kThreads) void kv_read_kernel(ReadArgs a) {
     constexpr uint32_t kLanes = D / 8;
+    const uint32_t lane = threadIdx.x & 63u, item = blockIdx.x * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t slot = item / a.slices, first = item % a.slices * kReadSlice;
+    if (slot >= a.tile_slots) return;
     uint32_t tile;
-    const uint32_t s = sequence_of_slot(a.starts, a.n_seqs, blockIdx.x, 1, kReadShift, &tile);
+    const uint32_t s = sequence_of_slot(a.starts, a.n_seqs, slot, 1, kReadShift, &tile);
     const int32_t begin = a.starts[s], end = a.starts[s + 1];
     if (begin < 0 || end < begin || (uint32_t)end > a.n_tokens) return;
     const uint32_t n = min((uint32_t)(end - begin), a.t.width << a.c.shift);
     if (tile > n >> kReadShift) return;
-    const uint32_t pos0 = tile << kReadShift, rows = min(n - pos0, 1u << kReadShift) * a.c.kv_heads;
-    if (rows == 0) return;
+    const uint32_t pos0 = tile << kReadShift, units = min(n - pos0, 1u << kReadShift) * a.c.kv_heads * kLanes;
+    if (first >= units) return;
     const bool is_v = blockIdx.y != 0;
     const Rows &x = is_v ? a.v : a.k;
     const uint8_t *const store = is_v ? a.c.v : a.c.k;
     const float *const scales = is_v ? a.c.v_scale : a.c.k_scale;
-    const uint32_t part = threadIdx.x % kLanes;
+    const uint32_t part = lane % kLanes;
     // (16 positions from a multiple of 16 lie in one page)
     const uint32_t page = min((uint32_t)a.t.pages[s * a.t.stride + (pos0 >> a.c.shift)], a.c.n_pages - 1);
     const uint32_t in_page = pos0 & ((1u << a.c.shift) - 1);
-    for (uint32_t r0 = threadIdx.x / kLanes; r0 < rows; r0 += kReadUnroll * kThreads / kLanes) {
-        u32x4 w[kReadUnroll];
-        u32x2 c[kReadUnroll];
-        float scale[kReadUnroll];
-        uint32_t pos[kReadUnroll], head[kReadUnroll];
+    u32x4 w[kReadUnroll];
+    u32x2 c[kReadUnroll];
+    float scale[kReadUnroll];
+    uint32_t pos[kReadUnroll], head[kReadUnroll];
 #pragma unroll
-        for (int i = 0; i < kReadUnroll; ++i) {
-            const uint32_t r = min(r0 + i * (kThreads / kLanes), rows - 1);
-            pos[i] = r / a.c.kv_heads;
-            head[i] = r - pos[i] * a.c.kv_heads;
-            const uint64_t row = (((uint64_t)page * a.c.kv_heads + head[i]) << a.c.shift) + in_page + pos[i];
-            if (kInt8) {
-                c[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x2 *>(store + row * D + 8 * part));
-                scale[i] = scales[row];
-            } else {
-                w[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(store + 2 * (row * D + 8 * part)));
+    for (int i = 0; i < kReadUnroll; ++i) {
+        const uint32_t r = min(first + i * 64 + lane, units - 1) / kLanes;
+        pos[i] = r / a.c.kv_heads;
+        head[i] = r - pos[i] * a.c.kv_heads;
+        const uint64_t row = (((uint64_t)page * a.c.kv_heads + head[i]) << a.c.shift) + in_page + pos[i];
+        if (kInt8) {
+            c[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x2 *>(store + row * D + 8 * part));
+            scale[i] = scales[row];
+        } else {
+            w[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(store + 2 * (row * D + 8 * part)));
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kReadUnroll; ++i) {
+        if (first + i * 64 + lane >= units) continue;
+        if (kInt8) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t two = c[i][j / 2] >> (16 * (j % 2));
+                w[i][j] = pack_bf16((float)(int8_t)two * scale[i], (float)(int8_t)(two >> 8) * scale[i]);
             }
         }
-#pragma unroll
-        for (int i = 0; i < kReadUnroll; ++i) {
-            if (r0 + i * (kThreads / kLanes) >= rows) continue;
-            if (kInt8) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t two = c[i][j / 2] >> (16 * (j % 2));
-                    w[i][j] = pack_bf16((float)(int8_t)two * scale[i], (float)(int8_t)(two >> 8) * scale[i]);
-                }
-            }
-            *reinterpret_cast<u32x4 *>(x.data + (int64_t)(begin + pos0 + pos[i]) * x.row + head[i] * x.head + 8 * part) = w[i];
-        }
+        *reinterpret_cast<u32x4 *>(x.data + (int64_t)(begin + pos0 + pos[i]) * x.row + head[i] * x.head + 8 * part) = w[i];
     }
 }
 
@@ -167,7 +173,7 @@ hipError_t launch_kv_write(const WriteArgs &a, uint32_t head_dim, bool int8, hip
 }
 
 hipError_t launch_kv_read(const ReadArgs &a, uint32_t head_dim, bool int8, hipStream_t stream) {
-    const dim3 grid((a.n_tokens >> kReadShift) + a.n_seqs, 2);
+    const dim3 grid((a.tile_slots * a.slices + kThreads / 64 - 1) / (kThreads / 64), 2);
     const auto kernel = head_dim == 64 ? (int8 ? kv_read_kernel<64, true> : kv_read_kernel<64, false>)
                                        : (int8 ? kv_read_kernel<128, true> : kv_read_kernel<128, false>);
     hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, a);

@@ -232,7 +232,8 @@ extern "C" df11_status df11_kv_read(const df11_kv_read_args *a, int hip_device, 
     if (!a) return report_error(DF11_E_ARG, "kv_read: NULL arguments");
     TRY(check_cache(a->cache));
     const uint32_t d = a->cache.head_dim, heads = a->cache.n_kv_heads;
-    if (a->n_tokens > 0x7FFFFFFFu || a->n_tokens / 16 + a->n_seqs > kMostGroups)
+    const uint64_t tiles = a->n_tokens / kReadTile + a->n_seqs, slices = ceil_div((uint64_t)heads * kReadTile * d / 8, kReadSlice);
+    if (a->n_tokens > 0x7FFFFFFFu || slices > 0x10000u || tiles > 4 * kMostGroups / slices)     // (four waves a workgroup)
         return report_error(DF11_E_UNSUPPORTED, "kv_read: %llu tokens of %u sequences", (unsigned long long)a->n_tokens, a->n_seqs);
     TRY(check_rows("k", a->k, a->n_tokens, heads, d, true));
     TRY(check_rows("v", a->v, a->n_tokens, heads, d, true));
@@ -240,7 +241,7 @@ extern "C" df11_status df11_kv_read(const df11_kv_read_args *a, int hip_device, 
     TRY(check_table(a->table, a->cache));
     if (bad_index(a->starts, 4)) return report_error(DF11_E_ARG, "kv_read: starts NULL or misaligned");
     ON_DEVICE(hip_device);
-    const ReadArgs r{view_of(a->cache), tables_of(a->table), rows_of(a->k), rows_of(a->v), a->starts, a->n_seqs, (uint32_t)a->n_tokens};
+    const ReadArgs r{view_of(a->cache), tables_of(a->table), rows_of(a->k), rows_of(a->v), a->starts, a->n_seqs, (uint32_t)a->n_tokens, (uint32_t)tiles, (uint32_t)slices};
     return launched(launch_kv_read(r, d, a->cache.store == DF11_KV_INT8, stream), "kv_read");
 }
 

@@ -41,6 +41,7 @@ struct ReadArgs {
     Rows k, v;
     const int32_t *starts;
     uint32_t n_seqs, n_tokens;
+    uint32_t tile_slots, slices;         // tiles of kReadTile tokens, waves for each
 };
 
 struct TokenArgs {
@@ -67,6 +68,8 @@ struct PromptArgs {
     float *part, *part_ml;     // [split][workgroup][wave][register / 4][lane][4], then [split][workgroup][wave][row][2]
 };
 
+constexpr uint32_t kReadTile = 16;       // tokens of a tile that kv_read reads back
+constexpr uint32_t kReadSlice = 256;     // 16-byte chunks of its rows that a wave takes
 constexpr uint32_t kPromptTile = 128;    // rows (queries of the heads of a kv head) a workgroup takes
 constexpr uint32_t kPromptKeys = 64;     // keys a step
 constexpr uint32_t kPromptPartKeys = 256; // the least that a part of a sequence takes
