@@ -380,6 +380,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void attend_prompt_kerne
     const f32x2 l_halves = with_lane_32(l);
     l = l_halves.x + l_halves.y;
     if (kSplit) {
+        if (wave_first >= n_rows) return;
         // as the lanes hold them, for the lanes of the join
         const uint64_t at = ((uint64_t)blockIdx.y * gridDim.x + blockIdx.x) * kWaves + wave;
         f32x4 *const part = reinterpret_cast<f32x4 *>(a.part) + at * (kDTiles * 4 * 64) + lane;

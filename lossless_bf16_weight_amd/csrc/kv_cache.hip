@@ -13,8 +13,8 @@
 // (a row of 128 is 16 lanes), several steps in flight.  Measured with 8 kv
 // heads of 128: 20,288 tokens written as words 28 us (166 MB read and written,
 // 5.9 TB/s; a copy of 2 GiB reaches 4.9), 5,520 tokens written in 8 bits 9.8 us
-// and read back 8.8 us (34 MB; an empty kernel takes 2.5 us of it), 118,617
-// tokens read back from 8 bits 139 us (736 MB, 5.3 TB/s).  64 tokens are
+// and read back 8.5 us (34 MB; an empty kernel takes 2.5 us of it), 118,617
+// tokens read back from 8 bits 131 us (736 MB, 5.6 TB/s).  64 tokens are
 // written in 2.6 us.
 #include "serve_device.hpp"
 #include "serve_internal.hpp"
@@ -105,9 +105,9 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(WriteArgs a) {
 // 16-byte chunks of it, four a lane, in the order of the rows that are written:
 // few tokens of many heads are many waves' work (35 sequences, 2000 tokens of 24
 // heads in all: 8 us, with a workgroup for a tile 15 us), and of one head the
-// lanes have enough to do (56,000 tokens: 11 us, 16 us).  Stores past the caches
-// are slower for a few thousand tokens, which the next kernel then finds in the
-// L2.
+// lanes have enough to do (56,000 tokens: 11 us, 16 us).  Stores past the
+// caches are 5% sooner for 228,000 tokens, but the attention that reads these
+// rows next is later by more (four times 16,000 tokens, with it 184 and 197 us).
 template <int D, bool kInt8>
 __global__ __launch_bounds__(kThreads) void kv_read_kernel(ReadArgs a) {
     constexpr uint32_t kLanes = D / 8;

@@ -162,20 +162,22 @@ df11_status check_token_sizes(const df11_attend_token_args &a) {
 // How attend_prompt splits the keys: where the tiles of rows (a piece of a
 // prompt behind a long prefix) are fewer than compute units, into as many parts
 // as give each of these two workgroups: 512 queries on 16384 keys take 148 us
-// (205 us with one workgroup for each compute unit, 278 us unsplit).  A part
-// has 256 keys at least on average where tiles are fewer than a quarter of the
-// compute units (32 queries on 1024 keys 14 us, in parts of 512 17 us, unsplit
-// 22 us), 512 where they are fewer than half (256 on 1024: 19 us, unsplit 22
-// us; eight tokens on 2000 keys each 23 us, unsplit 38 us), 1024 above, for the
-// join's traffic (512 on 1024: 23 us, in parts of 256 28 us).  As many tiles as
-// compute units are better left whole (1024 on 1024: 24 us, in two parts 34 us).
+// (205 us with one workgroup for each compute unit, 278 us unsplit).  How many
+// keys a part has at least, on average, goes by the rows, whose parts the join
+// reads: 256 for less than a quarter of a tile a compute unit (32 queries on
+// 1024 keys 14 us, in parts of 512 17 us, unsplit 22 us; eight tokens on 2000
+// keys each 21 us, unsplit 38 us), 512 for less than half (256 on 1024: 19 us,
+// unsplit 22 us), 1024 above (512 on 1024: 23 us, in parts of 256 28 us).  As
+// many tiles as compute units are better left whole (1024 on 1024: 24 us, in
+// two parts 34 us).
 uint64_t prompt_tile_slots(const df11_attend_prompt_args &a) { return a.n_q * (a.n_heads / a.n_kv_heads) / kPromptTile + a.n_seqs; }
 
 uint32_t prompt_splits(const df11_attend_prompt_args &a, int dev) {
     if (a.n_q == 0 || a.n_seqs == 0) return 1;
     const uint64_t tiles = std::max(ceil_div(a.n_q * a.n_heads, kPromptTile), (uint64_t)a.n_seqs * a.n_kv_heads), keys = a.n_k / a.n_seqs;
     if (tiles >= compute_units(dev)) return 1;
-    const uint64_t least = 4 * tiles < compute_units(dev) ? kPromptPartKeys : 2 * tiles < compute_units(dev) ? 512 : 1024;
+    const uint64_t full = ceil_div(a.n_q * a.n_heads, kPromptTile);
+    const uint64_t least = 4 * full < compute_units(dev) ? kPromptPartKeys : 2 * full < compute_units(dev) ? 512 : 1024;
     return (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>({2 * compute_units(dev) / tiles, keys / least, 32}));
 }
 
