@@ -126,10 +126,10 @@ __device__ __forceinline__ uint32_t keys_seen(const PromptArgs &a, uint32_t quer
 }
 
 // Keys of one part of a sequence's.  A part that begins past the keys which its
-// tile sees is neither written nor read, but for the first.
+// tile sees is neither written nor read, and a tile of one part is not joined.
 __device__ __forceinline__ uint32_t keys_a_part(const PromptArgs &a, uint32_t n_k) {
     // (the quotient, or one more; whole steps, above n_k / splits)
-    return max((__umulhi(n_k, a.split_magic) + kPromptKeys) / kPromptKeys * kPromptKeys, kPromptPartKeys);
+    return max((__umulhi(n_k, a.split_magic) + kPromptKeys) / kPromptKeys * kPromptKeys, a.part_keys);
 }
 
 // Writes a product's 32 x 32 results as BF16, the lane's column to 32 words
@@ -174,12 +174,14 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void attend_prompt_kerne
     const auto limit = [&](uint32_t query) { return keys_seen(a, query, n_q, n_k); };
     const uint32_t most_keys = limit(over_group(a, min(row0 + kPromptTile, n_rows) - 1));
     uint32_t key_begin = 0, key_end = most_keys;
+    bool whole = true;
     if (kSplit) {
         const uint32_t per = keys_a_part(a, n_k);
         const uint64_t b = (uint64_t)blockIdx.y * per;
         if (b >= most_keys && b) return;
         key_begin = (uint32_t)b;
         key_end = b + per < most_keys ? (uint32_t)(b + per) : most_keys;
+        whole = most_keys <= per;
     }
     const uint32_t wave_first = row0 + wave * kWaveRows, row = wave_first + col;
     const bool real = row < n_rows;
@@ -379,7 +381,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void attend_prompt_kerne
     }
     const f32x2 l_halves = with_lane_32(l);
     l = l_halves.x + l_halves.y;
-    if (kSplit) {
+    if (kSplit && !whole) {
         if (wave_first >= n_rows) return;
         // as the lanes hold them, for the lanes of the join
         const uint64_t at = ((uint64_t)blockIdx.y * gridDim.x + blockIdx.x) * kWaves + wave;
@@ -429,7 +431,9 @@ __global__ __launch_bounds__(64 * D / 32) void join_prompt_kernel(PromptArgs a) 
     const uint32_t first = tile * kPromptTile + blockIdx.y * kWaveRows, row = first + col, n_rows = (uint32_t)(q1 - q0) * a.group;
     if (first >= n_rows) return;
     const uint32_t n_k = k1 - k0, most_keys = keys_seen(a, over_group(a, min((tile + 1) * kPromptTile, n_rows) - 1), q1 - q0, n_k);
-    const uint32_t per = keys_a_part(a, n_k), parts = max(1, __builtin_popcountll(__ballot(lane < a.splits && lane * per < most_keys)));
+    const uint32_t per = keys_a_part(a, n_k);
+    if (most_keys <= per) return;
+    const uint32_t parts = __builtin_popcountll(__ballot(lane < a.splits && lane * per < most_keys));
     f32x16 o = {};
     float l = 0, m = -__builtin_inff();
     for (uint32_t s = 0; s < parts; s += kBatch) {

@@ -159,26 +159,33 @@ df11_status check_token_sizes(const df11_attend_token_args &a) {
     return DF11_OK;
 }
 
+uint64_t prompt_tile_slots(const df11_attend_prompt_args &a) { return a.n_q * (a.n_heads / a.n_kv_heads) / kPromptTile + a.n_seqs; }
+
 // How attend_prompt splits the keys: where the tiles of rows (a piece of a
 // prompt behind a long prefix) are fewer than compute units, into as many parts
 // as give each of these two workgroups: 512 queries on 16384 keys take 148 us
 // (205 us with one workgroup for each compute unit, 278 us unsplit).  How many
-// keys a part has at least, on average, goes by the rows, whose parts the join
-// reads: 256 for less than a quarter of a tile a compute unit (32 queries on
-// 1024 keys 14 us, in parts of 512 17 us, unsplit 22 us; eight tokens on 2000
-// keys each 21 us, unsplit 38 us), 512 for less than half (256 on 1024: 19 us,
-// unsplit 22 us), 1024 above (512 on 1024: 23 us, in parts of 256 28 us).  As
-// many tiles as compute units are better left whole (1024 on 1024: 24 us, in
-// two parts 34 us).
-uint64_t prompt_tile_slots(const df11_attend_prompt_args &a) { return a.n_q * (a.n_heads / a.n_kv_heads) / kPromptTile + a.n_seqs; }
+// keys a part has at least goes by the rows, whose parts the join reads: 256
+// for less than a quarter of a tile a compute unit (32 queries on 1024 keys 14
+// us, in parts of 512 17 us, unsplit 22 us; eight tokens on 2000 keys each 21
+// us, unsplit 38 us), 512 for less than half (256 on 1024: 19 us, unsplit 22
+// us), 1024 above (512 on 1024: 23 us, in parts of 256 28 us).  As many tiles
+// as compute units are better left whole (2048 on 2048: 48 us, with the tiles
+// that see more than 1024 keys in two parts 60 us).  The number of parts goes
+// by the average of the sequences, whose lengths the host does not know, and
+// the least by each: a tile that sees no more keys than one part has is not
+// joined.
+struct PromptSplit {
+    uint32_t splits, part_keys;
+};
 
-uint32_t prompt_splits(const df11_attend_prompt_args &a, int dev) {
-    if (a.n_q == 0 || a.n_seqs == 0) return 1;
-    const uint64_t tiles = std::max(ceil_div(a.n_q * a.n_heads, kPromptTile), (uint64_t)a.n_seqs * a.n_kv_heads), keys = a.n_k / a.n_seqs;
-    if (tiles >= compute_units(dev)) return 1;
-    const uint64_t full = ceil_div(a.n_q * a.n_heads, kPromptTile);
-    const uint64_t least = 4 * full < compute_units(dev) ? kPromptPartKeys : 2 * full < compute_units(dev) ? 512 : 1024;
-    return (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>({2 * compute_units(dev) / tiles, keys / least, 32}));
+PromptSplit prompt_split(const df11_attend_prompt_args &a, int dev) {
+    if (a.n_q == 0 || a.n_seqs == 0) return {1, 0};
+    const uint64_t full = ceil_div(a.n_q * a.n_heads, kPromptTile), cus = compute_units(dev);
+    const uint64_t tiles = std::max(full, (uint64_t)a.n_seqs * a.n_kv_heads), keys = a.n_k / a.n_seqs;
+    if (tiles >= cus) return {1, 0};
+    const uint64_t least = 4 * full < cus ? 256 : 2 * full < cus ? 512 : 1024;
+    return {(uint32_t)std::max<uint64_t>(1, std::min<uint64_t>({2 * cus / tiles, keys / least, 32})), (uint32_t)least};
 }
 
 uint64_t prompt_bytes(const df11_attend_prompt_args &a, uint32_t splits) {
@@ -287,7 +294,7 @@ extern "C" df11_status df11_attend_token(const df11_attend_token_args *a, int hi
 
 extern "C" uint64_t df11_attend_prompt_workspace(const df11_attend_prompt_args *a, int hip_device) {
     if (!a || check_prompt_sizes(*a)) return 0;
-    return prompt_bytes(*a, prompt_splits(*a, hip_device));
+    return prompt_bytes(*a, prompt_split(*a, hip_device).splits);
 }
 
 extern "C" df11_status df11_attend_prompt(const df11_attend_prompt_args *a, int hip_device, hipStream_t stream) {
@@ -303,7 +310,8 @@ extern "C" df11_status df11_attend_prompt(const df11_attend_prompt_args *a, int 
         return report_error(DF11_E_UNSUPPORTED, "k, v: rows more than %lld elements apart", (long long)kMostKeyStride);
     if (a->n_q == 0 || a->n_seqs == 0) return DF11_OK;
     if (bad_index(a->q_starts, 4) || bad_index(a->k_starts, 4)) return report_error(DF11_E_ARG, "attend_prompt: starts NULL or misaligned");
-    const uint32_t splits = prompt_splits(*a, hip_device);
+    const PromptSplit split = prompt_split(*a, hip_device);
+    const uint32_t splits = split.splits;
     TRY(check_workspace(a->workspace, a->workspace_bytes, prompt_bytes(*a, splits)));
     ON_DEVICE(hip_device);
     PromptArgs p{};
@@ -328,6 +336,7 @@ extern "C" df11_status df11_attend_prompt(const df11_attend_prompt_args *a, int 
     p.tile_slots = (uint32_t)prompt_tile_slots(*a);
     p.splits = splits;
     p.split_magic = splits > 1 ? (uint32_t)((((uint64_t)1 << 32) + splits - 1) / splits) : 0;
+    p.part_keys = split.part_keys;
     p.part = (float *)a->workspace;
     p.part_ml = p.part + splits * prompt_tile_slots(*a) * a->n_kv_heads * kPromptTile * a->head_dim;
     return launched(launch_attend_prompt(p, a->head_dim, stream), "attend_prompt");

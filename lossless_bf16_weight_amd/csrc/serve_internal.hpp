@@ -64,7 +64,7 @@ struct PromptArgs {
     uint32_t n_seqs, n_q, n_k, heads, kv_heads, group, causal;
     uint32_t group_magic, group_shift;   // x / group = (x * group_magic >> 32) >> group_shift for group > 1, x < 2^31
     uint32_t tile_slots, splits;
-    uint32_t split_magic;                // ceil(2^32 / splits)
+    uint32_t split_magic, part_keys;     // ceil(2^32 / splits), the least keys of a part
     float *part, *part_ml;     // [split][workgroup][wave][register / 4][lane][4], then [split][workgroup][wave][row][2]
 };
 
@@ -72,7 +72,6 @@ constexpr uint32_t kReadTile = 16;       // tokens of a tile that kv_read reads 
 constexpr uint32_t kReadSlice = 256;     // 16-byte chunks of its rows that a wave takes
 constexpr uint32_t kPromptTile = 128;    // rows (queries of the heads of a kv head) a workgroup takes
 constexpr uint32_t kPromptKeys = 64;     // keys a step
-constexpr uint32_t kPromptPartKeys = 256; // the least that a part of a sequence takes
 constexpr uint32_t kTokenKeys = 32;      // keys a wave's step
 constexpr uint32_t kTokenWholeMax = 1024; // and of one that twelve waves take whole
 constexpr uint32_t kTokenRangeMax = 1280;  // keys a workgroup takes of a long sequence
