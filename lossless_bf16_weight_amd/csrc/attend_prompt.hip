@@ -18,8 +18,8 @@
 // reads.
 //
 // The matrix rate and, beside it, the exponentials bound it.  Measured with 32
-// heads over 8 kv heads of 128, causal: a prompt of 16,384 tokens 1.9 to 2.0 ms
-// (2.2 TFLOP: 1.1 to 1.16 PFLOP/s; a product of 16,384-square matrices reaches
+// heads over 8 kv heads of 128, causal: a prompt of 16,384 tokens 1.9 to 2.1 ms
+// (2.2 TFLOP: 1.05 to 1.16 PFLOP/s; a product of 16,384-square matrices reaches
 // 1.37), its matrix units busy 60% of the cycles at the 1.76 GHz that the power
 // limit leaves; 64 prompts of 1024 tokens 0.72 ms, 11 of up to 2,113 170 us
 // (0.83 PFLOP/s of the visible pairs), 64 tokens 7.4 us.  With twice the rows a
