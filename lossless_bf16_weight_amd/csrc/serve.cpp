@@ -242,7 +242,7 @@ extern "C" df11_status df11_kv_read(const df11_kv_read_args *a, int hip_device, 
     TRY(check_cache(a->cache));
     const uint32_t d = a->cache.head_dim, heads = a->cache.n_kv_heads;
     const uint64_t tiles = a->n_tokens / kReadTile + a->n_seqs, slices = ceil_div((uint64_t)heads * kReadTile * d / 8, kReadSlice);
-    if (a->n_tokens > 0x7FFFFFFFu || slices > 0x10000u || tiles > 4 * kMostGroups / slices)     // (four waves a workgroup)
+    if (a->n_tokens > 0x7FFFFFFFu || tiles > 4 * kMostGroups / slices)     // (four waves a workgroup; at most 65535 heads)
         return report_error(DF11_E_UNSUPPORTED, "kv_read: %llu tokens of %u sequences", (unsigned long long)a->n_tokens, a->n_seqs);
     TRY(check_rows("k", a->k, a->n_tokens, heads, d, true));
     TRY(check_rows("v", a->v, a->n_tokens, heads, d, true));

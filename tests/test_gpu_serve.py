@@ -376,7 +376,7 @@ def test_token_nan_in_a_sequence_stays_there(int8):
 
 @pytest.mark.parametrize("int8", [False, True])
 @pytest.mark.parametrize("lens,ps,hk,d", [([1], 16, 1, 64), ([5, 0, 16, 17, 100], 16, 3, 128), ([63, 64, 65, 129, 1], 32, 2, 64),
-                                          ([300, 200], 256, 8, 128)])
+                                          ([300, 200], 256, 8, 128), ([70, 0, 5, 17], 16, 40, 128), ([33, 1], 128, 24, 64)])
 def test_write_then_read(lens, ps, hk, d, int8):
     """Codes and scales equal those of the same operations in 32 bits, are
     within half a step of the definition in 64, touch no other slot, and read

@@ -115,6 +115,11 @@ def test_key_rows_too_far_apart_are_refused():
         assert _call("df11_attend_prompt", dict(GOOD["df11_attend_prompt"], **{f"{x}.row_stride": 1 << 24})) == E_UNSUPPORTED
 
 
+def test_reads_of_more_waves_than_a_launch_holds_are_refused():
+    for heads, n, seqs in ((65535, 1 << 15, 2), (2, 1 << 30, 2), (8, 5, (1 << 24) - 1)):
+        assert _call("df11_kv_read", dict(GOOD["df11_kv_read"], **{"cache.n_kv_heads": heads, "n_tokens": n, "n_seqs": seqs})) == E_UNSUPPORTED
+
+
 def test_output_rows_that_overlap_are_refused():
     # (inputs may overlap; a single row or head has no stride)
     for name, what, other in (("df11_kv_read", "v", "n_tokens"), ("df11_attend_token", "out", "n_seqs"), ("df11_attend_prompt", "out", "n_q")):
