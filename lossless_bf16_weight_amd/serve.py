@@ -53,16 +53,21 @@ class DecoderStack:
 
     def _grow(self, new: Sequence[int]):
         """Makes room for new[s] tokens of each sequence; their positions and
-        slots, and the new lengths."""
+        slots, and the new lengths.  Where they do not all fit, nothing changes."""
+        if len(new) != len(self.lens) or min(new, default=0) < 0:
+            raise ValueError(f"{list(new)}: a count for each of {len(self.lens)} sequences is needed")
+        have = [-(-n // self.page_size) for n in self.lens]
+        need = [-(-(a + n) // self.page_size) for a, n in zip(self.lens, new)]
+        for s, n in enumerate(need):
+            if n > self.pages.shape[1]:
+                raise RuntimeError(f"sequence {s}: {self.lens[s] + new[s]} tokens are more than its page table holds")
+        if sum(need) - sum(have) > len(self.free):
+            raise RuntimeError(f"{sum(need) - sum(have)} pages are needed, {len(self.free)} are left")
         positions, slots = [], []
         for s, n in enumerate(new):
-            need = -(-(self.lens[s] + n) // self.page_size)
-            have = -(-self.lens[s] // self.page_size)
-            if need > self.pages.shape[1] or need - have > len(self.free):
-                raise RuntimeError(f"sequence {s}: no page is left for {self.lens[s] + n} tokens")
-            if need > have:
-                taken, self.free = self.free[:need - have], self.free[need - have:]
-                self.pages[s, have:need] = torch.tensor(taken, dtype=torch.int32, device=self.device)
+            if need[s] > have[s]:
+                taken, self.free = self.free[:need[s] - have[s]], self.free[need[s] - have[s]:]
+                self.pages[s, have[s]:need[s]] = torch.tensor(taken, dtype=torch.int32, device=self.device)
             at = torch.arange(self.lens[s], self.lens[s] + n, device=self.device)
             positions.append(at)
             slots.append(self.pages[s, at // self.page_size].long() * self.page_size + at % self.page_size)
@@ -75,8 +80,14 @@ class DecoderStack:
             out.append(out[-1] + n)
         return torch.tensor(out, dtype=torch.int32, device=self.device)
 
-    def _run(self, x: torch.Tensor, positions, slots, attend):
-        """One pass of the stack; attend(layer, q, k, v) gives the attention."""
+    def _run(self, x: torch.Tensor, new: Sequence[int], attend):
+        """One pass of the stack over the next new[s] tokens of each sequence
+        (rows of x); attend(layer, q, k, v) gives the attention.  A pass that
+        fails leaves the lengths and pages as they were: what it had written
+        lies past them."""
+        if x.shape[0] != sum(new):
+            raise ValueError(f"x: {x.shape[0]} rows for {sum(new)} tokens")
+        held = list(self.lens), self.free
         state = [x]
 
         def layer(l: int, ws: List[torch.Tensor]):
@@ -90,38 +101,42 @@ class DecoderStack:
             h = norm(x)
             state[0] = x + F.linear(F.silu(F.linear(h, gate)) * F.linear(h, up), down)
 
-        self.loop.run(layer)
+        try:
+            positions, slots = self._grow(new)
+            self.loop.run(layer)
+        except BaseException:
+            self.lens, self.free = held
+            raise
         return state[0]
 
     def prompt(self, x: torch.Tensor, new: Sequence[int]) -> torch.Tensor:
         """The next new[s] tokens of each sequence, rows of x packed in order
         (bfloat16): their hidden states after the last layer.  Sequences that
         have tokens in the cache attend to those too."""
-        before = list(self.lens)
-        positions, slots = self._grow(new)
-        q_starts, k_starts, total = self._starts(new), self._starts(self.lens), sum(self.lens)
+        after = [a + n for a, n in zip(self.lens, new)]
+        cached = any(self.lens)
+        q_starts, k_starts = self._starts(new), self._starts(after)
 
         def attend(l, q, k, v):
-            if any(before):     # what came before is in the cache
-                k, v = (torch.empty(total, self.kv_heads, self.d, dtype=q.dtype, device=q.device) for _ in range(2))
+            if cached:     # what came before is in the cache
+                k, v = (torch.empty(sum(after), self.kv_heads, self.d, dtype=q.dtype, device=q.device) for _ in range(2))
                 kv_read(self.caches[l], self.pages, k_starts, k, v)
             out = torch.empty_like(q)
             attend_prompt(q, k, v, q_starts, k_starts, out)
             return out
 
-        return self._run(x, positions, slots, attend)
+        return self._run(x, new, attend)
 
     def token(self, x: torch.Tensor) -> torch.Tensor:
         """One more token of every sequence (row s of x)."""
-        positions, slots = self._grow([1] * len(self.lens))
-        lens = torch.tensor(self.lens, dtype=torch.int32, device=self.device)
+        lens = torch.tensor([n + 1 for n in self.lens], dtype=torch.int32, device=self.device)
 
         def attend(l, q, k, v):
             out = torch.empty_like(q)
             attend_token(q, self.caches[l], self.pages, lens, out)
             return out
 
-        return self._run(x, positions, slots, attend)
+        return self._run(x, [1] * len(self.lens), attend)
 
 
 def compressed_layers(layers: Sequence[Sequence], device: str = "cuda") -> LayerLoop:
