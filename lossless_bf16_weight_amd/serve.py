@@ -94,10 +94,10 @@ class DecoderStack:
             wq, wk, wv, wo, gate, up, down = ws
             x = state[0]
             h = norm(x)
-            q, k, v = (F.linear(h, w).view(x.shape[0], -1, self.d) for w in (wq, wk, wv))
+            q, k, v = (F.linear(h, w).unflatten(1, (n, self.d)) for w, n in ((wq, self.heads), (wk, self.kv_heads), (wv, self.kv_heads)))
             q, k = rotary(q, positions), rotary(k, positions)
             kv_write(self.caches[l], k, v, slots)
-            x = x + F.linear(attend(l, q, k, v).view(x.shape[0], -1), wo)
+            x = x + F.linear(attend(l, q, k, v).flatten(1), wo)
             h = norm(x)
             state[0] = x + F.linear(F.silu(F.linear(h, gate)) * F.linear(h, up), down)
 

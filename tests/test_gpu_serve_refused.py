@@ -41,3 +41,16 @@ def test_refused_passes_leave_no_trace(int8):
         torch.cuda.synchronize()
         assert torch.equal(got.view(torch.int16), want.view(torch.int16)), new
         assert one.lens == other.lens and one.free == other.free
+
+
+def test_a_prompt_of_no_tokens():
+    """Rows that no sequence adds: an empty result, and nothing changes."""
+    log("decoder stack, a prompt of no tokens")
+    words = [[W.normal_bf16(s, seed=i, std=0.06) for i, s in enumerate(SHAPES)]]
+    loop = serve.compressed_layers(words)
+    one, other = (serve.DecoderStack(loop, HEADS, KV, D, 2, n_pages=4, page_size=16, max_len=32) for _ in range(2))
+    x = torch.randn(9, HIDDEN, device="cuda", generator=torch.Generator(device="cuda").manual_seed(7)).to(torch.bfloat16)
+    for new in ([3, 2], [0, 4]):
+        assert one.prompt(x[:0], [0, 0]).shape == (0, HIDDEN)
+        got, want = (s.prompt(x[:sum(new)], new) for s in (one, other))
+        assert torch.equal(got.view(torch.int16), want.view(torch.int16)) and one.lens == other.lens and one.free == other.free
