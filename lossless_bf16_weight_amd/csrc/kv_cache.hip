@@ -26,6 +26,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWriteUnroll = 2, kReadUnroll = 4;
 constexpr uint32_t kReadShift = 4;
+static_assert(kWriteChunks == kThreads * kWriteUnroll);
 static_assert(kReadTile == 1u << kReadShift && kReadSlice == 64 * kReadUnroll);
 
 // Maximum over the kLanes neighbouring lanes that hold a row, in each of them.
@@ -55,7 +56,7 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(WriteArgs a) {
     uint8_t *const store = is_v ? a.c.v : a.c.k;
     float *const scales = is_v ? a.c.v_scale : a.c.k_scale;
     const uint64_t n_units = (uint64_t)a.n_tokens * a.c.kv_heads * kLanes;
-    const uint64_t first = (uint64_t)blockIdx.x * (kThreads * kWriteUnroll) + threadIdx.x;
+    const uint64_t first = (uint64_t)blockIdx.x * kWriteChunks + threadIdx.x;
     u32x4 w[kWriteUnroll];
     int64_t slot[kWriteUnroll];
     uint32_t head[kWriteUnroll];
@@ -165,7 +166,7 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(ReadArgs a) {
 
 hipError_t launch_kv_write(const WriteArgs &a, uint32_t head_dim, bool int8, hipStream_t stream) {
     const uint64_t units = (uint64_t)a.n_tokens * a.c.kv_heads * (head_dim / 8);
-    const dim3 grid((uint32_t)((units + kThreads * kWriteUnroll - 1) / (kThreads * kWriteUnroll)), 2);
+    const dim3 grid((uint32_t)((units + kWriteChunks - 1) / kWriteChunks), 2);
     const auto kernel = head_dim == 64 ? (int8 ? kv_write_kernel<64, true> : kv_write_kernel<64, false>)
                                        : (int8 ? kv_write_kernel<128, true> : kv_write_kernel<128, false>);
     hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, a);

@@ -10,7 +10,7 @@ using namespace df11;
 
 namespace {
 
-constexpr uint64_t kMostGroups = uint64_t(1) << 24;   // workgroups along x: threads stay below 2^32
+constexpr uint64_t kMostGroups = (uint64_t(1) << 24) - 1;   // workgroups of 256 along x: threads stay below 2^32
 constexpr int64_t kMostStride = int64_t(1) << 32;
 // a step's key rows lie within 2^31 bytes of the first (attend_prompt.hip's descriptors)
 constexpr int64_t kMostKeyStride = ((int64_t(1) << 31) - 256) / (2 * kPromptKeys);
@@ -227,7 +227,7 @@ extern "C" df11_status df11_kv_write(const df11_kv_write_args *a, int hip_device
     if (!a) return report_error(DF11_E_ARG, "kv_write: NULL arguments");
     TRY(check_cache(a->cache));
     const uint32_t d = a->cache.head_dim, heads = a->cache.n_kv_heads;
-    if (a->n_tokens > (uint64_t(1) << 30) / heads) return report_error(DF11_E_UNSUPPORTED, "kv_write: %llu tokens", (unsigned long long)a->n_tokens);
+    if (a->n_tokens > kMostGroups * kWriteChunks / ((uint64_t)heads * (d / 8))) return report_error(DF11_E_UNSUPPORTED, "kv_write: %llu tokens", (unsigned long long)a->n_tokens);
     TRY(check_rows("k", a->k, a->n_tokens, heads, d, false));
     TRY(check_rows("v", a->v, a->n_tokens, heads, d, false));
     if (a->n_tokens == 0) return DF11_OK;

@@ -68,6 +68,7 @@ struct PromptArgs {
     float *part, *part_ml;     // [split][workgroup][wave][register / 4][lane][4], then [split][workgroup][wave][row][2]
 };
 
+constexpr uint32_t kWriteChunks = 512;   // 16-byte chunks of rows that a workgroup of kv_write takes
 constexpr uint32_t kReadTile = 16;       // tokens of a tile that kv_read reads back
 constexpr uint32_t kReadSlice = 256;     // 16-byte chunks of its rows that a wave takes
 constexpr uint32_t kPromptTile = 128;    // rows (queries of the heads of a kv head) a workgroup takes
