@@ -196,7 +196,10 @@ df11_status check_prompt_sizes(const df11_attend_prompt_args &a) {
     if (a.head_dim != 64 && a.head_dim != 128) return report_error(DF11_E_UNSUPPORTED, "head_dim %u, 64 and 128 are built", a.head_dim);
     if (a.n_kv_heads == 0 || a.n_heads == 0 || a.n_heads % a.n_kv_heads) return report_error(DF11_E_ARG, "%u heads over %u kv heads", a.n_heads, a.n_kv_heads);
     if (a.n_q > 0x7FFFFFFFu || a.n_k > 0x7FFFFFFFu) return report_error(DF11_E_UNSUPPORTED, "2^31 rows or more");
-    if (a.n_q * (a.n_heads / a.n_kv_heads) > 0x7FFFFFFFu || prompt_tile_slots(a) * a.n_kv_heads > kMostGroups) return report_error(DF11_E_UNSUPPORTED, "%llu rows of %u heads", (unsigned long long)a.n_q, a.n_heads);
+    // (each factor alone first: the product of two of 2^32 does not fit 64 bits)
+    if (a.n_q * (a.n_heads / a.n_kv_heads) > 0x7FFFFFFFu || a.n_kv_heads > kMostGroups || a.n_seqs > kMostGroups ||
+        prompt_tile_slots(a) * a.n_kv_heads > kMostGroups)
+        return report_error(DF11_E_UNSUPPORTED, "%llu rows of %u heads in %u sequences", (unsigned long long)a.n_q, a.n_heads, a.n_seqs);
     return DF11_OK;
 }
 

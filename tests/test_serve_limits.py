@@ -3,6 +3,8 @@ call: a grid's x dimension times its workgroup's threads stays below 2^32, its
 y and z dimensions within 65,535.  (Every call here is refused.)"""
 import pytest
 
+import lossless_bf16_weight_amd as df11
+
 from test_serve_host import E_UNSUPPORTED, GOOD, _call
 
 
@@ -32,3 +34,11 @@ def test_2_to_the_24_workgroups_of_256_threads_are_refused():
                                             "out.row_stride": 2048})
     # prompts: rows of a head and its sequences, in tiles of 128
     assert _refused("df11_attend_prompt", n_q=128 * ((1 << 24) - 2), n_seqs=2, n_heads=1, n_kv_heads=1, **{"out.row_stride": 128})
+
+
+def test_prompt_sizes_whose_product_passes_64_bits():
+    """2^32 + 65,536 tile slots of 2^32 - 65,535 kv heads are 2^64 + 65,536 workgroups."""
+    kv, n_q = (1 << 32) - 65535, 128 * 65537
+    strides = {"out.row_stride": 128, "out.head_stride": 128 * n_q}
+    assert _refused("df11_attend_prompt", n_q=n_q, n_seqs=(1 << 32) - 1, n_heads=kv, n_kv_heads=kv, **strides)
+    assert df11.prompt_workspace(n_q, 5, (1 << 32) - 1, kv, kv, 128) == 0
