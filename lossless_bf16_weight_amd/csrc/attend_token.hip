@@ -79,7 +79,7 @@ __global__ __launch_bounds__(64 * kWaves, 3) void attend_token_kernel(TokenArgs 
     const uint32_t q_tile = in_block / 8, unit = 8 * block + in_block % 8;
     if (unit >= a.n_seqs * a.c.kv_heads) return;
     const uint32_t kv_head = unit % a.c.kv_heads, seq = unit / a.c.kv_heads;
-    const uint32_t split = blockIdx.y;
+    const uint32_t split = blockIdx.z * gridDim.y + blockIdx.y;     // (past the last: begins past every length)
 
     const uint32_t len = (uint32_t)min((int64_t)max(a.lens[seq], 0), (int64_t)a.t.width << a.c.shift);
     const uint32_t begin = split * a.range;
@@ -380,7 +380,10 @@ void launch(const TokenArgs &a, uint32_t head_dim, bool int8, dim3 grid, hipStre
 }  // namespace
 
 hipError_t launch_attend_token(const TokenArgs &a, uint32_t head_dim, bool int8, hipStream_t stream) {
-    const dim3 grid(a.q_tiles == 1 ? a.n_seqs * a.c.kv_heads : (a.n_seqs * a.c.kv_heads + 7) / 8 * 8 * a.q_tiles, a.splits);
+    // (a table of 2^28 positions has 262,144 parts of 1024, a grid's y and z dimensions hold 65,535)
+    const uint32_t parts = a.splits < 65535 ? a.splits : 65535;
+    const dim3 grid(a.q_tiles == 1 ? a.n_seqs * a.c.kv_heads : (a.n_seqs * a.c.kv_heads + 7) / 8 * 8 * a.q_tiles, parts,
+                    (a.splits + parts - 1) / parts);
     if (a.whole) launch<12>(a, head_dim, int8, grid, stream);
     else launch<4>(a, head_dim, int8, grid, stream);
     hipError_t e = hipGetLastError();
