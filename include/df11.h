@@ -390,8 +390,11 @@ df11_status df11_nf12_decode_batch(const void *const *host_headers, const void *
  * rest of a page, another sequence's rows) does not reach it, be it infinite
  * or NaN.  Products are of BF16 operands (attend_prompt rounds the weights p_j
  * to BF16; attend_token takes them as the sum of two); scores, maxima, sums
- * and accumulators are in 32 bits, and the result is rounded once.  Results do
- * not depend on other work on the GPU: sums are taken in a fixed order. */
+ * and accumulators are in 32 bits, and the result is rounded once.  Where the
+ * scores are finite in 32 bits, finite values give finite results, whatever
+ * their size and the number of keys (but attend_prompt's rounded weights may
+ * take a result within 2^-8 of the largest BF16 number to infinity).  Results
+ * do not depend on other work on the GPU: sums are taken in a fixed order. */
 
 /* Rows of heads in BF16: element (row, head, d) at data[row * row_stride +
  * head * head_stride + d].  Strides in elements, multiples of 8, at least 0;

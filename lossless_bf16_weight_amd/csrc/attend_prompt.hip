@@ -2,9 +2,10 @@
 //
 // Query i of a sequence with n_q queries and n_k keys sees the keys below
 // lim_i = i + 1 + n_k - n_q (causal) or n_k.  s_j = <q_i, k_j>, p_j =
-// 2^(c s_j - m), c = scale log2(e), m the running maximum of c s_j, out = sum
-// p_j v_j / sum p_j; a row that sees no key is 0.  One pass over the keys:
-// when a step raises m, the sums are scaled by 2^(old - new).
+// 2^(c s_j - m), c = scale log2(e), m the running maximum of c s_j (and a
+// constant: see kSlack), out = sum p_j v_j / sum p_j; a row that sees no key is
+// 0.  One pass over the keys: when a step raises m, the sums are scaled by
+// 2^(old - new).
 //
 // The queries of the heads that share a kv head are the rows of one matrix:
 // row r is query r / group of head r % group.  A workgroup takes 128 rows of a
@@ -201,6 +202,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void attend_prompt_kerne
 
     f32x16 o[kDTiles];
     float m, l;
+    const float log2_n = log2_up(n_k);
     const auto start = [&] {
 #pragma unroll
         for (int i = 0; i < kDTiles; ++i) o[i] = f32x16{};
@@ -284,8 +286,8 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void attend_prompt_kerne
             for (int i = 0; i < 16; ++i) top = fmaxf(top, s[t][i]);
         const f32x2 halves = with_lane_32(top);
         top = fmaxf(halves.x, halves.y) * a.log2_scale;
-        if (__any(top > m + kSlack)) {
-            const float next = fmaxf(m, top);
+        if (__any(top > m - log2_n)) {
+            const float next = fmaxf(m, top + (kSlack + log2_n));
             const float keep = exp2_fast(m - (next == -__builtin_inff() ? 0.0f : next));
             m = next;
             l *= keep;

@@ -2,9 +2,9 @@
 // gfx950.
 //
 // For query head h of kv head h / group: s_j = <q, k_j>, p_j = 2^(c s_j - m)
-// with c = scale log2(e) and m the running maximum of c s_j, out = sum p_j
-// v_j / sum p_j.  One pass over the keys: when a step raises m, the sums are
-// scaled by 2^(old - new).  Keys in 8 bits keep their codes as exact BF16
+// with c = scale log2(e) and m the running maximum of c s_j (and a constant:
+// see kSlack), out = sum p_j v_j / sum p_j.  One pass over the keys: when a
+// step raises m, the sums are scaled by 2^(old - new).  Keys in 8 bits keep their codes as exact BF16
 // operands: a key's scale multiplies its score, a value's scale its weight.
 //
 // Every key and value is read once and used by `group` queries, so HBM
@@ -111,6 +111,7 @@ __global__ __launch_bounds__(64 * kWaves, 3) void attend_token_kernel(TokenArgs 
 #pragma unroll
     for (int i = 0; i < kDTiles; ++i) o[i] = f32x4{0, 0, 0, 0};
     float m = -__builtin_inff(), l = 0;
+    const float log2_n = log2_up(len);      // (of the sequence: its parts are joined)
     uint8_t *const tile = lds + wave * kTileBytes;
 
     // A step's 32 rows of K and V, held in registers from one step before:
@@ -223,8 +224,8 @@ __global__ __launch_bounds__(64 * kWaves, 3) void attend_token_kernel(TokenArgs 
         f32x2 two = with_lane_16(top);
         two = with_lane_32(fmaxf(two.x, two.y));
         top = fmaxf(two.x, two.y) * scale;
-        if (__any(top > m + kSlack)) {
-            const float next = fmaxf(m, top);
+        if (__any(top > m - log2_n)) {
+            const float next = fmaxf(m, top + (kSlack + log2_n));
             const float keep = exp2_fast(m - (next == -__builtin_inff() ? 0.0f : next));
             m = next;
             l *= keep;

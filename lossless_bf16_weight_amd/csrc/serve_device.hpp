@@ -40,11 +40,20 @@ __device__ __forceinline__ f32x2 with_lane_16(float x) {
     return f32x2{__uint_as_float(r[0]), __uint_as_float(r[1])};
 }
 
-// Softmax sums are kept against a base that is raised only when a row's
-// maximum passes it by more than this: weights stay below 2^8, which neither
-// 32 bits nor the rounding of the weights minds, and most steps then need not
-// scale the sums.
+// Softmax sums are kept against a base, m below, that is raised only when a
+// row's maximum passes what it was by more than kSlack: most steps then need
+// not scale the sums.  The base lies kSlack + log2(n) above that maximum for
+// n keys, so that a weight is at most 1 / n and a sum of weights at most 1:
+// sums of weighted values stay within the values, and no finite value
+// overflows them.  (A power of two costs the weights no bits; those below
+// 2^-126 n 2^8 of the largest are lost, which no sum in 32 bits sees.)
 constexpr float kSlack = 8.0f;
+
+// log2(n) rounded up (0 for none), in a scalar register.
+__device__ __forceinline__ float log2_up(uint32_t n) {
+    const float x = (float)(n > 1 ? 32 - __builtin_clz(n - 1) : 0);
+    return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x)));
+}
 
 // The four signed bytes of w as BF16 words (exact: |code| <= 128 has eight
 // significant bits, so the float's upper half is the whole value).
