@@ -140,6 +140,11 @@ __global__ __launch_bounds__(64 * kWaves, 3) void attend_token_kernel(TokenArgs 
             w[i] = kOnce ? __builtin_nontemporal_load(from) : *from;
         }
     };
+    // LDS keeps a wave's accesses in order; this keeps the compiler's.
+    const auto handed_over = [] {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+        __builtin_amdgcn_wave_barrier();
+    };
     const auto load_scales = [&] {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -160,11 +165,13 @@ __global__ __launch_bounds__(64 * kWaves, 3) void attend_token_kernel(TokenArgs 
         uint32_t lane = lane0;
         asm volatile("" : "+v"(lane));
         const uint32_t col = lane & 15u, grp = lane >> 4;
+        handed_over();
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             const uint32_t at = i * 64 + lane;
             *reinterpret_cast<u32x4 *>(tile + k_at<kRow>(at / kChunks, at % kChunks)) = kw[i];
         }
+        handed_over();
         find_rows(key0 + kWaves * kTokenKeys);      // (past the end: loads that nobody uses)
         load(a.c.k, kw);
         __builtin_amdgcn_sched_barrier(0);     // (loads of V moved up past here would not fit in registers)
@@ -190,11 +197,13 @@ __global__ __launch_bounds__(64 * kWaves, 3) void attend_token_kernel(TokenArgs 
             for (int i = 0; i < kLoads; ++i)
                 if (key0 + (i * 64 + lane) / kChunks >= n) vw[i] = u32x4{0, 0, 0, 0};
         }
+        handed_over();
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             const uint32_t at = i * 64 + lane;
             *reinterpret_cast<u32x4 *>(tile + v_at<kRow, kInt8>(at / kChunks, at % kChunks)) = vw[i];
         }
+        handed_over();
         load(a.c.v, vw);
         f32x4 v_scale[2];
         if (kInt8) {
