@@ -461,8 +461,9 @@ df11_status df11_kv_read(const df11_kv_read_args *args, int hip_device, hipStrea
  * out.  scale is above 0 and below 2^127.  Long sequences are split over
  * workgroups and joined, for which the call needs df11_attend_token_workspace
  * bytes (0 for small calls; the function reads the sizes alone, no pointers)
- * of 16-byte aligned device memory that no other call uses meanwhile.  out may
- * be q, and overlaps nothing else. */
+ * of 16-byte aligned device memory that no other call uses meanwhile.  The
+ * split goes by the table's width: a table wider than the lengths costs
+ * workspace and time.  out may be q, and overlaps nothing else. */
 typedef struct {
     df11_kv_cache cache;
     df11_page_table table;

@@ -22,8 +22,10 @@
 // heads over 8 kv heads of 128, causal: a prompt of 16,384 tokens 1.9 to 2.1 ms
 // (2.2 TFLOP: 1.05 to 1.16 PFLOP/s; a product of 16,384-square matrices reaches
 // 1.37), its matrix units busy 60% of the cycles at the 1.76 GHz that the power
-// limit leaves; 64 prompts of 1024 tokens 0.72 ms, 11 of up to 2,113 170 us
-// (0.83 PFLOP/s of the visible pairs), 64 tokens 7.4 us.  With twice the rows a
+// limit leaves; 64 prompts of 1024 tokens 0.70 ms, 11 of up to 2,113 172 us
+// (0.82 PFLOP/s of the visible pairs), 64 tokens 7.4 us.  With heads of 64
+// 16,384 tokens take 1.10 ms (1.0 PFLOP/s: as many exponentials for half the
+// products); 8192 not causal 0.97 ms (1.13 PFLOP/s).  With twice the rows a
 // workgroup (eight waves) 16,384 tokens are 2.5% faster and shorter prompts
 // slower; steps of 32 keys, with a third wave for each SIMD or four stages in
 // LDS, are no faster.
@@ -75,10 +77,12 @@ __device__ __forceinline__ uint32_t over_group(const PromptArgs &a, uint32_t row
 // where there is none.  The last tiles of a sequence, which see the most keys
 // of a causal prompt, come first, and so do the sequences with the most keys
 // where there are few: a heavy tile at the end would keep the others' compute
-// units waiting (11 sequences of up to 2113 tokens, shortest first: 68 us,
-// unranked 76 us).  With more sequences it levels out, and each workgroup pays
-// for the ranking of all of them (64 of 1024 tokens: 719 us, ranked 782 us; 64
-// of 256: 99 and 119 us).
+// units waiting (11 sequences of 1 to 2113 tokens, shortest first: with 12
+// heads over 4 71 us, unranked 80 us; with 32 over 8 177 and 180 us).  Each
+// workgroup pays for the ranking: sequences that are equal, or come longest
+// first, are better off without (16 of 256 tokens: 28.8 us, unranked 26.0; the
+// 11 longest first 72 and 70 us), and with more sequences it levels out (64 of
+// 1024 tokens: 703 us, ranked 749 us; 64 of 256: 96 and 114 us).
 constexpr uint32_t kRanked = 16;
 
 __device__ __forceinline__ bool pick_tile(const PromptArgs &a, uint32_t slot, uint32_t *tile, int32_t *q0, int32_t *q1,

@@ -12,16 +12,19 @@
 // (work along a long sequence is split over workgroups, and a second kernel
 // joins the parts); its four waves (twelve, where they take a sequence whole)
 // take 32 keys a step in turn, each with its own maximum, sum and
-// accumulators, joined through LDS at the end.  Three workgroups of four waves
-// run on a compute unit at a time, and each wave holds the next step's 16 KB of
-// keys and values in registers: 192 KB of loads in flight there.  LDS only
-// turns a wave's own rows around (a wave waits for no other until the end).
+// accumulators, joined through LDS at the end.  Each wave holds the next step's
+// keys and values in registers, 16 KB of them for words of head_dim 128, and
+// three workgroups of four waves run on a compute unit at a time: 192 KB of
+// loads in flight there (half in 8 bits; head_dim 64 has half for each wave and
+// registers for five waves a SIMD).  LDS only turns a wave's own rows around (a
+// wave waits for no other until the end).
 //
 // Measured with 32 heads over 8 kv heads of 128, join included: 64 sequences
 // of up to 4096 tokens 94 us (505 MB, 5.6 TB/s in the first kernel's 90 us),
 // two of up to 100,001 tokens 84 us (440 MB, 5.5 TB/s in 80), 48 of up to
-// 16,384 in 8 bits 138 us (734 MB, 5.3 TB/s).  A read of the same bytes with
-// nothing computed reaches 6.6 TB/s.
+// 16,384 in 8 bits 139 us (734 MB, 5.3 TB/s).  A read of the same bytes with
+// nothing computed reaches 6.6 TB/s.  With heads of 64 the same take 53, 48 and
+// 82 us for half the bytes (4.6 to 4.7 TB/s).
 //
 // Matrix instructions, 16 x 16 x 32: S^T = K Q^T puts a query in each lane
 // (column) and four keys in its registers, so that the row statistics are per

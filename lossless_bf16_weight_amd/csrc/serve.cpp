@@ -115,15 +115,21 @@ float log2_scale(float scale) { return (float)((double)scale * 1.442695040888963
 // one sequence of 1024 keys takes 7.7 us in parts of 128 keys and 10 us in
 // parts of 384; 256 keys take 6.1 us in one part and 7.5 us in two.  Where the
 // units fill the compute units, the three workgroups for each that run at a
-// time are enough (16 sequences of 1024 keys: 14.9 us; with four 17.3 us), in
-// parts of at most 1280 keys: lengths are unequal, and no more parts than
-// compute units leave some of these idle (sequences of 100001 and 7640 keys:
-// 78 us, in parts of 2048 91 us; shorter parts of 512 84 us).
+// time are enough (16 sequences of 1024 keys: 14.9 us; with four 17.3 us; with
+// head_dim 64 five would run, and three are taken all the same), in parts of at
+// most 1280 keys: lengths are unequal, and no more parts than compute units
+// leave some of these idle (sequences of 100001 and 7640 keys: 78 us, in parts
+// of 2048 91 us; shorter parts of 512 84 us).
 // Sequences of up to 1024 keys that would be split are taken whole instead by
 // workgroups of twelve waves: one launch and no workspace, which a caller that
 // launches call by call has 3.8 us sooner, and for 16 and more sequences the
 // faster way (32 of 784 keys: 18.5 us, split 20.8 us; one of 784 keys: 9.8 us,
-// split 7.4 us; of 1152 keys 11.8 us and 7.7 us).
+// split 7.4 us; of 1152 keys 11.8 us and 7.7 us).  In a captured graph, where
+// the second launch costs the host nothing, one sequence would be faster split.
+// The table's width stands for the lengths, which the host does not know: 64
+// sequences of up to 4096 keys take 94 us with a table of that width and 107 us
+// with one of 131,072 positions, whose workgroups past the lengths read a length
+// and leave.
 struct TokenSplit {
     uint32_t q_tiles, range, splits, whole;
 };
@@ -163,7 +169,9 @@ uint64_t prompt_tile_slots(const df11_attend_prompt_args &a) { return a.n_q * (a
 
 // How attend_prompt splits the keys: where the tiles of rows (a piece of a
 // prompt behind a long prefix) are fewer than compute units, into as many parts
-// as give each of these two workgroups: 512 queries on 16384 keys take 148 us
+// as give each of these two workgroups, or a few more (the rows are counted as
+// if no tile but the last were part empty, each sequence's last one may be: 130
+// and 35 queries of 32 heads over 8 count 42 for 56 tiles): 512 queries on 16384 keys take 148 us
 // (205 us with one workgroup for each compute unit, 278 us unsplit).  How many
 // keys a part has at least goes by the rows, whose parts the join reads: 256
 // for less than a quarter of a tile a compute unit (32 queries on 1024 keys 14
