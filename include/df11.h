@@ -443,6 +443,61 @@ typedef struct {
 } df11_kv_write_args;
 df11_status df11_kv_write(const df11_kv_write_args *args, int hip_device, hipStream_t stream);
 
+/* The position rotation.  Pair i of a head, i < pairs, is its elements i and
+ * i + pairs, or with DF11_ROTATE_NEIGHBOURS 2i and 2i + 1; (x, y) becomes
+ * factor * (x c - y s, y c + x s) with the cosine and sine of
+ *   2 pi * positions[t * position_stride + axis] * turns[i] / 2^64
+ * for token t, axis = axes[i] (0 where axes is NULL; one past n_axes - 1
+ * counts as that).  turns[i] is pair i's frequency as a fraction of a turn a
+ * position, times 2^64; the phase is exact for any position.  The head's other
+ * elements stay as they are.  pairs: a multiple of 8 up to head_dim / 2, 0 for
+ * no rotation (then nothing else is read); n_axes: 1 to 4; turns and axes
+ * 16-byte aligned; factor finite. */
+#define DF11_ROTATE_NEIGHBOURS 1u
+typedef struct {
+    const uint64_t *turns;
+    const uint8_t *axes;
+    const int32_t *positions;
+    int64_t position_stride;
+    uint32_t pairs, n_axes, flags;
+    float factor;
+} df11_rotation;
+
+/* Queries and keys of n_tokens tokens (rows of n_heads and n_kv_heads heads;
+ * either may be 0, its rows are then not looked at), each head normed where
+ * its weight (head_dim BF16 words) is not NULL, x * weight / sqrt(mean(x^2) +
+ * eps), and rotated, into q_out and k_out.  All in 32 bits, rounded once.
+ * eps: finite, at least 2^-100.  q_out may be q and k_out may be k (the same
+ * pointer and strides); they overlap nothing else.  Finite values of any size
+ * are normed as the formula says. */
+typedef struct {
+    df11_rotation rotation;
+    df11_rows q, k, q_out, k_out;
+    const void *q_weight, *k_weight;
+    uint64_t n_tokens;
+    uint32_t n_heads, n_kv_heads, head_dim;
+    float eps;
+} df11_rotate_heads_args;
+df11_status df11_rotate_heads(const df11_rotate_heads_args *args, int hip_device, hipStream_t stream);
+
+/* df11_rotate_heads and df11_kv_write in one: keys normed and rotated on their
+ * way into slot slots[t] of the cache, with the values as they are, and (n_heads
+ * above 0) queries normed and rotated into q_out; keys also as rows of k_out
+ * unless its data is NULL.  Slots as for df11_kv_write; a token that is left out
+ * of the cache still has its rows of q_out and k_out.  Keys in 8 bits are
+ * quantised from the 32-bit values, not from rounded ones. */
+typedef struct {
+    df11_kv_cache cache;
+    df11_rotation rotation;
+    df11_rows q, k, v, q_out, k_out;
+    const int64_t *slots;
+    const void *q_weight, *k_weight;
+    uint64_t n_tokens;
+    uint32_t n_heads;
+    float eps;
+} df11_kv_append_args;
+df11_status df11_kv_append(const df11_kv_append_args *args, int hip_device, hipStream_t stream);
+
 /* Read back the first starts[s + 1] - starts[s] tokens of each sequence s <
  * n_seqs as packed rows: position i of sequence s to row starts[s] + i of k
  * and v (n_tokens rows).  8-bit codes times their scale are rounded to BF16. */

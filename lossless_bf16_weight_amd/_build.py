@@ -27,6 +27,7 @@ SOURCES = [
     ("encode_gpu.hip", DEVICE),
     ("serve.cpp", ["-x", "c++", "-D__HIP_PLATFORM_AMD__", "-I/opt/rocm/include"]),
     ("kv_cache.hip", DEVICE),
+    ("heads.hip", DEVICE),
     ("attend_token.hip", DEVICE),
     ("attend_prompt.hip", DEVICE),
 ]

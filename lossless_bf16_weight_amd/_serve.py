@@ -10,6 +10,7 @@ Calls enqueue on `stream` (the current one by default) and return.
 """
 from __future__ import annotations
 
+import math
 import struct
 from functools import lru_cache
 from typing import NamedTuple, Optional
@@ -20,6 +21,7 @@ from ._lib import OK, _raise, lib
 
 BF16, INT8, F32, I32, I64 = torch.bfloat16, torch.int8, torch.float32, torch.int32, torch.int64
 KV_BF16, KV_INT8 = 0, 1
+ROTATE_NEIGHBOURS = 1
 ATTEND_CAUSAL = 1
 
 # The argument structs of include/df11.h, field by field.
@@ -27,6 +29,9 @@ _CACHE = "QQQQIIIIII"
 _TABLE = "QqII"
 _ROWS = "Qqq"
 _WRITE = struct.Struct("<" + _CACHE + 2 * _ROWS + "QQ")
+_ROTATION = "QQQqIIIf"
+_HEADS = struct.Struct("<" + _ROTATION + 4 * _ROWS + "QQQIIIf")
+_APPEND = struct.Struct("<" + _CACHE + _ROTATION + 5 * _ROWS + "QQQQIf")
 _READ = struct.Struct("<" + _CACHE + _TABLE + 2 * _ROWS + "QQII")
 _TOKEN = struct.Struct("<" + _CACHE + _TABLE + 2 * _ROWS + "QQQIIfI")
 _PROMPT = struct.Struct("<" + 4 * _ROWS + "QQQQQQIIIIIf")
@@ -143,6 +148,117 @@ def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tens
     n, _, kr = _rows(k, "k", dev, d, heads=heads)
     _, _, vr = _rows(v, "v", dev, d, n, heads)
     _launch(lib().df11_kv_write, _WRITE.pack(*c, *kr, *vr, _index(slots, "slots", dev, I64, n), n), dev, stream)
+
+
+class Rotation(NamedTuple):
+    """The position rotation of a head's first 2 * len(turns) elements (made by
+    rotation()): frequencies as fractions of a turn a position, times 2^64."""
+    turns: torch.Tensor                    # int64 [pairs]
+    axes: Optional[torch.Tensor] = None    # uint8 [pairs]
+    n_axes: int = 1
+    interleaved: bool = False
+    factor: float = 1.0
+
+
+def rotation(rotary_dim: int, base: float = 10000.0, freqs=None, axes=None, interleaved: bool = False, factor: float = 1.0,
+             device="cuda") -> Rotation:
+    """A rotation of the first rotary_dim elements of a head (a multiple of 16,
+    0 for none): pair i turns by position * freqs[i] radians, freqs[i] being
+    base ** (-2 i / rotary_dim) unless given.  Pairs are elements i and i +
+    rotary_dim / 2, or (interleaved) neighbours.  axes: for positions with
+    several axes (time, height, width ...; up to 4), the axis of each pair.
+    factor multiplies the rotated elements."""
+    pairs = rotary_dim // 2
+    if rotary_dim % 16 or rotary_dim < 0:
+        raise ValueError(f"rotary_dim {rotary_dim}: a multiple of 16 is needed")
+    f = [base ** (-i / pairs) for i in range(pairs)] if freqs is None else [float(x) for x in freqs]
+    if len(f) != pairs or not all(map(math.isfinite, f)) or not math.isfinite(factor):
+        raise ValueError(f"freqs, factor: {pairs} finite frequencies and a finite factor are needed")
+    turns = [round(math.fmod(x / (2 * math.pi), 1.0) * 2.0 ** 64) % 2 ** 64 for x in f]
+    n_axes = 1
+    if axes is not None:
+        axes = [int(x) for x in axes]
+        if len(axes) != pairs or not all(0 <= x < 4 for x in axes):
+            raise ValueError(f"axes: {pairs} numbers from 0 to 3 are needed")
+        n_axes = max(axes, default=0) + 1
+    return Rotation(torch.tensor([x - 2 ** 64 if x >= 2 ** 63 else x for x in turns], dtype=I64, device=device),
+                    torch.tensor(axes, dtype=torch.uint8, device=device) if n_axes > 1 else None, n_axes, bool(interleaved), float(factor))
+
+
+def _rotation_fields(r: Optional[Rotation], positions, dev: int, n: int):
+    if r is None or r.turns.shape[0] == 0:
+        return 0, 0, 0, 0, 0, 0, 0, 0.0
+    turns, axes, n_axes, interleaved, factor = r
+    pairs = turns.shape[0]
+    if turns.dtype is not I64 or turns.dim() != 1 or turns.get_device() != dev or not turns.is_contiguous():
+        raise ValueError(f"rotation: contiguous int64 turns [pairs] on cuda:{dev} are needed")
+    at = 0
+    if axes is not None:
+        if axes.dtype is not torch.uint8 or axes.shape != turns.shape or axes.get_device() != dev or not axes.is_contiguous():
+            raise ValueError(f"rotation: contiguous uint8 axes [{pairs}] on cuda:{dev} are needed")
+        at = axes.data_ptr()
+    p = positions
+    if not isinstance(p, torch.Tensor) or p.dtype is not I32 or p.get_device() != dev or p.dim() not in (1, 2) or p.shape[0] != n:
+        raise ValueError(f"positions: an int32 tensor [{n}] or [{n}, axes] on cuda:{dev} is needed")
+    if p.dim() == 2:
+        if not n_axes <= p.shape[1] <= 4 or (p.shape[1] > 1 and p.stride(1) != 1):
+            raise ValueError(f"positions: shape {tuple(p.shape)}, strides {p.stride()}; {n_axes} to 4 axes, contiguous in a row, are needed")
+        n_axes = p.shape[1]
+    elif n_axes > 1:
+        raise ValueError(f"positions: [{n}, {n_axes}] is needed")
+    return turns.data_ptr(), at, p.data_ptr(), p.stride(0) if n > 1 else 0, pairs, n_axes, ROTATE_NEIGHBOURS if interleaved else 0, factor
+
+
+def _weight(w, what: str, dev: int, d: int):
+    if w is None:
+        return 0
+    if not isinstance(w, torch.Tensor) or w.dtype is not BF16 or w.shape != (d,) or w.get_device() != dev or not w.is_contiguous():
+        raise ValueError(f"{what}: a contiguous bfloat16 tensor [{d}] on cuda:{dev} is needed")
+    return w.data_ptr()
+
+
+_NO_ROWS = 0, 0, (0, 0, 0)
+
+
+def rotate_heads(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions: Optional[torch.Tensor], rotation: Optional[Rotation],
+                 q_out: Optional[torch.Tensor], k_out: Optional[torch.Tensor], q_weight: Optional[torch.Tensor] = None,
+                 k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, stream=None):
+    """Queries and keys ([tokens, heads, head_dim] bfloat16; either may be None)
+    with each head normed, x * weight / sqrt(mean(x^2) + eps), where its weight
+    ([head_dim] bfloat16) is given, and rotated by the token's position, into
+    q_out and k_out (which may be q and k).  positions: int32 [tokens], or
+    [tokens, axes].  rotation None: the norms alone."""
+    x = k if q is None else q
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dim() != 3:
+        raise ValueError("q, k: CUDA tensors [tokens, heads, head_dim] are needed")
+    dev, (n, _, d) = x.get_device(), x.shape
+    _, h, qr = _NO_ROWS if q is None else _rows(q, "q", dev, d, n)
+    _, hk, kr = _NO_ROWS if k is None else _rows(k, "k", dev, d, n)
+    _, _, qo = _NO_ROWS if q is None else _rows(q_out, "q_out", dev, d, n, h)
+    _, _, ko = _NO_ROWS if k is None else _rows(k_out, "k_out", dev, d, n, hk)
+    _launch(lib().df11_rotate_heads, _HEADS.pack(*_rotation_fields(rotation, positions, dev, n), *qr, *kr, *qo, *ko,
+                                                 _weight(q_weight, "q_weight", dev, d), _weight(k_weight, "k_weight", dev, d), n, h, hk, d, eps),
+            dev, stream)
+
+
+def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, positions: Optional[torch.Tensor], slots: torch.Tensor,
+              rotation: Optional[Rotation], k_weight: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
+              q_out: Optional[torch.Tensor] = None, q_weight: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+              eps: float = 1e-6, stream=None):
+    """rotate_heads and kv_write in one launch: token t's keys normed and
+    rotated into slot slots[t] (int64) of the cache, with its values as they
+    are; queries, where given, into q_out; keys also as rows of k_out, where
+    that is given.  Keys in 8 bits are quantised without rounding them to
+    bfloat16 first.  A slot outside the cache leaves its token out of it."""
+    dev, heads, d, c = _cache_fields(cache)
+    n, _, kr = _rows(k, "k", dev, d, heads=heads)
+    _, _, vr = _rows(v, "v", dev, d, n, heads)
+    _, h, qr = _NO_ROWS if q is None else _rows(q, "q", dev, d, n)
+    _, _, qo = _NO_ROWS if q is None else _rows(q_out, "q_out", dev, d, n, h)
+    _, _, ko = _NO_ROWS if k_out is None else _rows(k_out, "k_out", dev, d, n, heads)
+    _launch(lib().df11_kv_append, _APPEND.pack(*c, *_rotation_fields(rotation, positions, dev, n), *qr, *kr, *vr, *qo, *ko,
+                                               _index(slots, "slots", dev, I64, n), _weight(q_weight, "q_weight", dev, d),
+                                               _weight(k_weight, "k_weight", dev, d), n, h, eps), dev, stream)
 
 
 def kv_read(cache: KVCache, pages: torch.Tensor, starts: torch.Tensor, k_out: torch.Tensor, v_out: torch.Tensor, stream=None):

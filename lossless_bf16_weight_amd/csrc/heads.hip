@@ -1,0 +1,224 @@
+// Query, key and value heads of new tokens for gfx950: RMS norms of each
+// query and key head, the position rotation, and the keys' and values' way
+// into the paged cache (as BF16 words or in 8 bits), in one pass.
+//
+// norm: y = x * w / sqrt(mean(x^2) + eps).  Rotation: pair i (a, b) of a head
+// becomes (a c - b s, b c + a s), c and s of position * frequency_i.  A
+// frequency is kept as F, turns a position times 2^64: position * F modulo
+// 2^64 is the phase without any rounding, two 32-bit multiplications give its
+// upper half, and the sine takes that as a fraction of a turn from -1/2 to
+// 1/2.  Far positions are then as exact as near ones.  8 bits: as in
+// kv_cache.hip, but of the 32-bit values, so that an element is rounded once.
+//
+// HBM traffic bounds it.  A lane holds 16 elements of a row, its pairs
+// complete: with pairs of the two halves chunks of 8 that are half the rotated
+// part apart, with neighbours two chunks side by side, pairs 8 l .. 8 l + 7 of
+// lane l either way.  A wave takes the rows of one token eight (heads of 64:
+// sixteen) at a time, whose sines it computes once.
+#include <type_traits>
+
+#include "serve_device.hpp"
+#include "serve_internal.hpp"
+
+namespace df11 {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kBatch = 3;      // rows of a lane in flight
+
+__device__ __forceinline__ float low(uint32_t w) { return __builtin_bit_cast(float, w << 16); }
+__device__ __forceinline__ float high(uint32_t w) { return __builtin_bit_cast(float, w & 0xFFFF0000u); }
+
+template <int kLanes>
+__device__ __forceinline__ uint32_t row_max(uint32_t x) {
+    x = max(x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0xB1, 0xF, 0xF, true));    // lanes xor 1
+    x = max(x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x4E, 0xF, 0xF, true));    // lanes xor 2
+    if (kLanes == 8) x = max(x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x141, 0xF, 0xF, true));   // mirrored in 8
+    return x;
+}
+
+template <int kLanes>
+__device__ __forceinline__ float row_sum(float x) {
+    const auto from = [&](auto ctrl) { return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), decltype(ctrl)::value, 0xF, 0xF, true)); };
+    x += from(std::integral_constant<int, 0xB1>{});
+    x += from(std::integral_constant<int, 0x4E>{});
+    if (kLanes == 8) x += from(std::integral_constant<int, 0x141>{});
+    return x;
+}
+
+template <int D, int kStore, bool kNeighbours>
+__global__ __launch_bounds__(kThreads) void heads_kernel(HeadsArgs a) {
+    constexpr uint32_t kLanes = D / 16, kRows = 64 / kLanes;
+    const uint32_t lane = threadIdx.x & 63u, l = lane % kLanes, in_step = lane / kLanes;
+    const uint32_t item = blockIdx.x * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t token = item / a.parts, part = item % a.parts;
+    if (token >= a.n_tokens) return;
+    const uint32_t n_rows = a.heads + (kStore == kHeadsOnly ? 1 : 2) * a.kv_heads;
+    const uint32_t first = part * a.run * kRows, end = min(first + a.run * kRows, n_rows);
+
+    const bool turned = l < a.pairs / 8;
+    const uint32_t at0 = !kNeighbours && turned ? 8 * l : 16 * l, at1 = !kNeighbours && turned ? 8 * l + a.pairs : 16 * l + 8;
+
+    float c[8], s[8];
+    u32x4 wq[2], wk[2];
+    int64_t slot = -1;
+    if (kStore != kHeadsOnly) {
+        slot = a.slots[token];
+        if (slot < 0 || slot >= a.c.n_slots) slot = -1;
+    }
+    const auto angles = [&] {
+        const int32_t *const at = a.positions + token * a.position_stride;
+        int32_t p[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) p[x] = a.pairs && x < (int)a.n_axes ? at[x] : 0;
+        u32x2 axes = {0, 0};
+        if (a.axes && turned) axes = *reinterpret_cast<const u32x2 *>(a.axes + 8 * l);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            c[i] = 1, s[i] = 0;
+            if (!turned) continue;
+            const u32x2 f = *reinterpret_cast<const u32x2 *>(a.turns + 8 * l + i);
+            const uint32_t axis = axes[i / 4] >> (8 * (i % 4)) & 255;
+            int32_t pos = p[0];
+#pragma unroll
+            for (int x = 1; x < 4; ++x) pos = axis >= (uint32_t)x && x < (int)a.n_axes ? p[x] : pos;
+            const uint32_t phase = (uint32_t)pos * f.y + __umulhi((uint32_t)pos, f.x) - (pos < 0 ? f.x : 0);
+            const float t = (float)(int32_t)phase * 0x1p-32f;
+            c[i] = __builtin_amdgcn_cosf(t) * a.factor;
+            s[i] = __builtin_amdgcn_sinf(t) * a.factor;
+        }
+    };
+
+    // row r of the token: its rows of queries, then keys, then values
+    const auto source = [&](uint32_t r) -> const uint16_t * {
+        const bool is_q = r < a.heads, is_k = r < a.heads + a.kv_heads;
+        const uint16_t *const data = is_q ? a.q.data : is_k ? a.k.data : a.v.data;
+        const int64_t row = is_q ? a.q.row : is_k ? a.k.row : a.v.row, head = is_q ? a.q.head : is_k ? a.k.head : a.v.head;
+        return data + token * row + (r - (is_q ? 0 : is_k ? a.heads : a.heads + a.kv_heads)) * head;
+    };
+
+    bool begun = false;
+    for (uint32_t r0 = first; r0 < end; r0 += kBatch * kRows) {
+        u32x4 w[kBatch][2];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const uint32_t r = r0 + i * kRows + in_step;
+            if (r < end) {
+                const uint16_t *const from = source(r);
+                w[i][0] = *reinterpret_cast<const u32x4 *>(from + at0);
+                w[i][1] = *reinterpret_cast<const u32x4 *>(from + at1);
+            }
+        }
+        if (!begun) {
+            begun = true;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                wq[x] = wk[x] = u32x4{0, 0, 0, 0};
+                if (a.q_weight) wq[x] = *reinterpret_cast<const u32x4 *>(a.q_weight + (x ? at1 : at0));
+                if (a.k_weight) wk[x] = *reinterpret_cast<const u32x4 *>(a.k_weight + (x ? at1 : at0));
+            }
+            angles();
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const uint32_t r = r0 + i * kRows + in_step;
+            if (r >= end) continue;        // (a row's lanes go together)
+            const bool is_q = r < a.heads, is_v = r >= a.heads + a.kv_heads, is_k = !is_q && !is_v;
+            const uint32_t head = r - (is_q ? 0 : is_k ? a.heads : a.heads + a.kv_heads);
+            float y[16];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                y[2 * x] = low(w[i][x / 4][x % 4]);
+                y[2 * x + 1] = high(w[i][x / 4][x % 4]);
+            }
+            if (is_q ? a.q_weight != nullptr : is_k && a.k_weight) {
+                float sum = 0;
+#pragma unroll
+                for (int x = 0; x < 16; ++x) sum = __builtin_fmaf(y[x], y[x], sum);
+                sum = row_sum<kLanes>(sum);
+                float eps = a.eps;
+                if (!(sum < __builtin_inff())) {
+                    // squares that pass 32 bits (or an infinity): of values 2^-100 as
+                    // large, and eps 2^-200 of itself
+                    sum = 0, eps = 0;
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) {
+                        y[x] *= 0x1p-100f;
+                        sum = __builtin_fmaf(y[x], y[x], sum);
+                    }
+                    sum = row_sum<kLanes>(sum);
+                }
+                const float by = __builtin_amdgcn_rsqf(__builtin_fmaf(sum, 1.0f / D, eps));
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    const uint32_t two = is_q ? wq[x / 4][x % 4] : wk[x / 4][x % 4];
+                    y[2 * x] *= by * low(two);
+                    y[2 * x + 1] *= by * high(two);
+                }
+            }
+            if (turned && !is_v) {
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    float &p = kNeighbours ? y[2 * x] : y[x], &q = kNeighbours ? y[2 * x + 1] : y[x + 8];
+                    const float p0 = p, q0 = q;
+                    p = __builtin_fmaf(p0, c[x], -(q0 * s[x]));
+                    q = __builtin_fmaf(q0, c[x], p0 * s[x]);
+                }
+            }
+            u32x4 out[2];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) out[x / 4][x % 4] = is_v ? w[i][x / 4][x % 4] : pack_bf16(y[2 * x], y[2 * x + 1]);
+            const Rows &to = is_q ? a.q_out : a.k_out;
+            if (is_q || (is_k && a.k_out.data)) {
+                uint16_t *const row = to.data + token * to.row + head * to.head;
+                *reinterpret_cast<u32x4 *>(row + at0) = out[0];
+                *reinterpret_cast<u32x4 *>(row + at1) = out[1];
+            }
+            if (kStore == kHeadsOnly || is_q || slot < 0) continue;
+            const uint64_t row = ((((uint64_t)slot >> a.c.shift) * a.c.kv_heads + head) << a.c.shift) + (slot & ((1 << a.c.shift) - 1));
+            uint8_t *const store = is_v ? a.c.v : a.c.k;
+            if (kStore == kHeadsInt8) {
+                uint32_t m = 0x0D800000u;      // 2^-100
+#pragma unroll
+                for (int x = 0; x < 16; ++x) m = max(m, __float_as_uint(y[x]) & 0x7FFFFFFFu);
+                const float top = __uint_as_float(row_max<kLanes>(m)), inv = 127.0f / top;
+                uint32_t codes[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    codes[x] = 0;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) codes[x] |= (uint32_t)((int)__builtin_rintf(y[4 * x + j] * inv) & 255) << (8 * j);
+                }
+                *reinterpret_cast<u32x2 *>(store + row * D + at0) = u32x2{codes[0], codes[1]};
+                *reinterpret_cast<u32x2 *>(store + row * D + at1) = u32x2{codes[2], codes[3]};
+                if (l == 0) (is_v ? a.c.v_scale : a.c.k_scale)[row] = top / 127.0f;
+            } else {
+                *reinterpret_cast<u32x4 *>(store + 2 * (row * D + at0)) = out[0];
+                *reinterpret_cast<u32x4 *>(store + 2 * (row * D + at1)) = out[1];
+            }
+        }
+    }
+}
+
+template <int D, int kStore>
+auto kernel_of(bool neighbours) {
+    return neighbours ? heads_kernel<D, kStore, true> : heads_kernel<D, kStore, false>;
+}
+
+template <int D>
+auto kernel_of(int store, bool neighbours) {
+    return store == kHeadsOnly ? kernel_of<D, kHeadsOnly>(neighbours)
+                               : store == kHeadsInt8 ? kernel_of<D, kHeadsInt8>(neighbours) : kernel_of<D, kHeadsBf16>(neighbours);
+}
+
+}  // namespace
+
+hipError_t launch_heads(const HeadsArgs &a, uint32_t head_dim, int store, bool neighbours, hipStream_t stream) {
+    const uint64_t waves = (uint64_t)a.n_tokens * a.parts;
+    const auto kernel = head_dim == 64 ? kernel_of<64>(store, neighbours) : kernel_of<128>(store, neighbours);
+    hipLaunchKernelGGL(kernel, dim3((uint32_t)((waves + kThreads / 64 - 1) / (kThreads / 64))), dim3(kThreads), 0, stream, a);
+    return hipGetLastError();
+}
+
+}  // namespace df11

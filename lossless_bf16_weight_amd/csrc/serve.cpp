@@ -109,6 +109,50 @@ df11_status launched(hipError_t e, const char *what) {
 
 float log2_scale(float scale) { return (float)((double)scale * 1.4426950408889634074); }
 
+df11_status check_rotation(const df11_rotation &r, uint32_t head_dim) {
+    if (r.flags & ~DF11_ROTATE_NEIGHBOURS) return report_error(DF11_E_ARG, "rotation: flags %u", r.flags);
+    if (r.pairs % 8 || r.pairs > head_dim / 2) return report_error(DF11_E_ARG, "rotation: %u pairs, a multiple of 8 up to %u is needed", r.pairs, head_dim / 2);
+    if (r.pairs == 0) return DF11_OK;
+    if (!r.turns || misaligned(r.turns)) return report_error(DF11_E_ARG, "rotation: turns NULL or not 16-byte aligned");
+    if (misaligned(r.axes)) return report_error(DF11_E_ARG, "rotation: axes not 16-byte aligned");
+    if (r.n_axes < 1 || r.n_axes > 4) return report_error(DF11_E_ARG, "rotation: %u axes, 1 to 4 are needed", r.n_axes);
+    if (!r.positions || ((uintptr_t)r.positions & 3)) return report_error(DF11_E_ARG, "rotation: positions NULL or misaligned");
+    if (r.position_stride < 0 || r.position_stride >= kMostStride) return report_error(DF11_E_ARG, "rotation: position_stride must be from 0 to below 2^32");
+    if (!std::isfinite(r.factor)) return report_error(DF11_E_ARG, "rotation: a finite factor is needed");
+    return DF11_OK;
+}
+
+df11_status check_norms(const void *q_weight, const void *k_weight, float eps) {
+    if (misaligned(q_weight) || misaligned(k_weight)) return report_error(DF11_E_ARG, "weights: not 16-byte aligned");
+    if ((q_weight || k_weight) && !(eps >= 0x1p-100f && std::isfinite(eps))) return report_error(DF11_E_ARG, "eps: a finite number from 2^-100 is needed");
+    return DF11_OK;
+}
+
+// What rotate_heads and kv_append share: the rotation, the norms, and the
+// waves.  A wave takes the rows of one token, 64 lanes of 16 elements a step;
+// where tokens are few, a part of them.
+df11_status heads_args(HeadsArgs *h, const df11_rotation &r, const void *q_weight, const void *k_weight, float eps, uint64_t n_tokens,
+                       uint32_t rows, uint32_t head_dim, int dev) {
+    const uint64_t steps = ceil_div((uint64_t)rows * head_dim, 64 * 16);
+    const uint64_t want = ceil_div(32 * (uint64_t)compute_units(dev), n_tokens);
+    h->run = (uint32_t)ceil_div(steps, std::min(want, steps));
+    h->parts = (uint32_t)ceil_div(steps, h->run);
+    if (n_tokens > 0x7FFFFFFFu || n_tokens * h->parts > 4 * kMostGroups)
+        return report_error(DF11_E_UNSUPPORTED, "%llu tokens of %u heads", (unsigned long long)n_tokens, rows);
+    h->turns = r.turns;
+    h->axes = r.axes;
+    h->positions = r.positions;
+    h->position_stride = r.position_stride;
+    h->pairs = r.pairs;
+    h->n_axes = r.n_axes;
+    h->factor = r.factor;
+    h->q_weight = (const uint16_t *)q_weight;
+    h->k_weight = (const uint16_t *)k_weight;
+    h->eps = eps;
+    h->n_tokens = (uint32_t)n_tokens;
+    return DF11_OK;
+}
+
 // How attend_token splits: keys a workgroup takes and workgroups along a
 // sequence, from the longest length that the table holds.  A step of the four
 // waves is 128 keys and takes 1.3 us when little else runs, the join 2.7 us:
@@ -246,6 +290,64 @@ extern "C" df11_status df11_kv_write(const df11_kv_write_args *a, int hip_device
     ON_DEVICE(hip_device);
     const WriteArgs w{view_of(a->cache), rows_of(a->k), rows_of(a->v), a->slots, (uint32_t)a->n_tokens};
     return launched(launch_kv_write(w, d, a->cache.store == DF11_KV_INT8, stream), "kv_write");
+}
+
+extern "C" df11_status df11_rotate_heads(const df11_rotate_heads_args *a, int hip_device, hipStream_t stream) {
+    if (!a) return report_error(DF11_E_ARG, "rotate_heads: NULL arguments");
+    if (a->head_dim != 64 && a->head_dim != 128) return report_error(DF11_E_UNSUPPORTED, "head_dim %u, 64 and 128 are built", a->head_dim);
+    if (a->n_heads > 65535 || a->n_kv_heads > 65535) return report_error(DF11_E_ARG, "%u heads, %u kv heads", a->n_heads, a->n_kv_heads);
+    TRY(check_norms(a->q_weight, a->k_weight, a->eps));
+    if (a->n_heads) {
+        TRY(check_rows("q", a->q, a->n_tokens, a->n_heads, a->head_dim, false));
+        TRY(check_rows("q_out", a->q_out, a->n_tokens, a->n_heads, a->head_dim, true));
+    }
+    if (a->n_kv_heads) {
+        TRY(check_rows("k", a->k, a->n_tokens, a->n_kv_heads, a->head_dim, false));
+        TRY(check_rows("k_out", a->k_out, a->n_tokens, a->n_kv_heads, a->head_dim, true));
+    }
+    if (a->n_tokens == 0 || a->n_heads + a->n_kv_heads == 0) return DF11_OK;
+    TRY(check_rotation(a->rotation, a->head_dim));
+    HeadsArgs h{};
+    TRY(heads_args(&h, a->rotation, a->q_weight, a->k_weight, a->eps, a->n_tokens, a->n_heads + a->n_kv_heads, a->head_dim, hip_device));
+    h.q = rows_of(a->q);
+    h.k = rows_of(a->k);
+    h.q_out = rows_of(a->q_out);
+    h.k_out = rows_of(a->k_out);
+    h.heads = a->n_heads;
+    h.kv_heads = a->n_kv_heads;
+    ON_DEVICE(hip_device);
+    return launched(launch_heads(h, a->head_dim, kHeadsOnly, a->rotation.flags & DF11_ROTATE_NEIGHBOURS, stream), "rotate_heads");
+}
+
+extern "C" df11_status df11_kv_append(const df11_kv_append_args *a, int hip_device, hipStream_t stream) {
+    if (!a) return report_error(DF11_E_ARG, "kv_append: NULL arguments");
+    TRY(check_cache(a->cache));
+    const uint32_t d = a->cache.head_dim, heads = a->cache.n_kv_heads;
+    if (a->n_heads > 65535) return report_error(DF11_E_ARG, "%u heads", a->n_heads);
+    TRY(check_norms(a->q_weight, a->k_weight, a->eps));
+    TRY(check_rows("k", a->k, a->n_tokens, heads, d, false));
+    TRY(check_rows("v", a->v, a->n_tokens, heads, d, false));
+    if (a->n_heads) {
+        TRY(check_rows("q", a->q, a->n_tokens, a->n_heads, d, false));
+        TRY(check_rows("q_out", a->q_out, a->n_tokens, a->n_heads, d, true));
+    }
+    if (a->k_out.data) TRY(check_rows("k_out", a->k_out, a->n_tokens, heads, d, true));
+    if (a->n_tokens == 0) return DF11_OK;
+    if (bad_index(a->slots, 8)) return report_error(DF11_E_ARG, "kv_append: slots NULL or misaligned");
+    TRY(check_rotation(a->rotation, d));
+    HeadsArgs h{};
+    TRY(heads_args(&h, a->rotation, a->q_weight, a->k_weight, a->eps, a->n_tokens, a->n_heads + 2 * heads, d, hip_device));
+    h.c = view_of(a->cache);
+    h.q = rows_of(a->q);
+    h.k = rows_of(a->k);
+    h.v = rows_of(a->v);
+    h.q_out = rows_of(a->q_out);
+    h.k_out = rows_of(a->k_out);
+    h.slots = a->slots;
+    h.heads = a->n_heads;
+    h.kv_heads = heads;
+    ON_DEVICE(hip_device);
+    return launched(launch_heads(h, d, a->cache.store == DF11_KV_INT8 ? kHeadsInt8 : kHeadsBf16, a->rotation.flags & DF11_ROTATE_NEIGHBOURS, stream), "kv_append");
 }
 
 extern "C" df11_status df11_kv_read(const df11_kv_read_args *a, int hip_device, hipStream_t stream) {

@@ -1,5 +1,6 @@
 // What the host code of the serving operators (serve.cpp) and their kernels
-// (attend_prompt.hip, attend_token.hip, kv_cache.hip) share.
+// (attend_chunk.hip, attend_prompt.hip, attend_token.hip, heads.hip,
+// kv_cache.hip) share.
 #pragma once
 #include "df11_internal.hpp"
 
@@ -44,6 +45,24 @@ struct ReadArgs {
     uint32_t tile_slots, slices;         // tiles of kReadTile tokens, waves for each
 };
 
+// Where heads go: rows only, or keys and values also into a cache.
+enum { kHeadsOnly = 0, kHeadsBf16 = 1, kHeadsInt8 = 2 };
+
+struct HeadsArgs {
+    CacheView c;
+    Rows q, k, v, q_out, k_out;          // k_out.data may be null beside a cache
+    const int64_t *slots;
+    const uint64_t *turns;               // [pairs]: turns a position, times 2^64
+    const uint8_t *axes;                 // [pairs], or null: the first
+    const int32_t *positions;
+    int64_t position_stride;
+    const uint16_t *q_weight, *k_weight; // BF16 [head_dim], or null: no norm
+    uint32_t n_tokens, heads, kv_heads;
+    uint32_t pairs, n_axes;
+    uint32_t parts, run;                 // waves a token, steps of each
+    float factor, eps;
+};
+
 struct TokenArgs {
     CacheView c;
     Tables t;
@@ -79,6 +98,7 @@ constexpr uint32_t kTokenRangeMax = 1280;  // keys a workgroup takes of a long s
 
 hipError_t launch_kv_write(const WriteArgs &a, uint32_t head_dim, bool int8, hipStream_t stream);
 hipError_t launch_kv_read(const ReadArgs &a, uint32_t head_dim, bool int8, hipStream_t stream);
+hipError_t launch_heads(const HeadsArgs &a, uint32_t head_dim, int store, bool neighbours, hipStream_t stream);
 hipError_t launch_attend_token(const TokenArgs &a, uint32_t head_dim, bool int8, hipStream_t stream);
 hipError_t launch_attend_prompt(const PromptArgs &a, uint32_t head_dim, hipStream_t stream);
 
