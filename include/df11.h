@@ -557,6 +557,31 @@ typedef struct {
 uint64_t df11_attend_prompt_workspace(const df11_attend_prompt_args *args, int hip_device);
 df11_status df11_attend_prompt(const df11_attend_prompt_args *args, int hip_device, hipStream_t stream);
 
+/* Attention of a chunk of new tokens of each sequence over its pages: the
+ * queries of sequence s are rows q_starts[s] .. q_starts[s + 1] - 1 of q (n_q
+ * rows; those behind the last sequence are left alone), its keys and values the
+ * first lens[s] positions of its pages, the new tokens' own among them (written
+ * before).  With DF11_ATTEND_CAUSAL query i of n stands at position p = lens[s] -
+ * n + i and sees the keys j <= p; with a window above 0, of these only j > p -
+ * window and j < sinks (a window needs the flag; sinks without one do nothing).
+ * Otherwise all.  A sequence may have one query or all its tokens, or none.
+ * scale, workspace and out as for df11_attend_token; weights are rounded as in
+ * df11_attend_prompt.  The division of the work follows lens, on the device: a
+ * table wider than the lengths costs workspace, no time. */
+typedef struct {
+    df11_kv_cache cache;
+    df11_page_table table;
+    df11_rows q, out;
+    const int32_t *q_starts, *lens;
+    void *workspace;
+    uint64_t workspace_bytes;
+    uint64_t n_q;
+    uint32_t n_seqs, n_heads, flags, window, sinks;
+    float scale;
+} df11_attend_chunk_args;
+uint64_t df11_attend_chunk_workspace(const df11_attend_chunk_args *args, int hip_device);
+df11_status df11_attend_chunk(const df11_attend_chunk_args *args, int hip_device, hipStream_t stream);
+
 /* ------------------------------------------------------------------- misc */
 
 /* Text of the last non-OK status on this thread (never NULL). */

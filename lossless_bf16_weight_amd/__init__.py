@@ -11,8 +11,8 @@ from ._lib import (ABI_VERSION, FLAG_SHA256, DF11Error, Plan, bw_control, check,
                    sha256, validate, validate_status, verify, verify_decoded, verify_status)
 
 # (imported when first used: they need torch, which the rest loads only for calls on the GPU)
-_SERVING = ("KVCache", "Rotation", "attend_prompt", "attend_token", "kv_append", "kv_cache", "kv_read", "kv_write", "prompt_workspace",
-            "rotate_heads", "rotation", "token_workspace")
+_SERVING = ("KVCache", "Rotation", "attend_chunk", "attend_prompt", "attend_token", "chunk_workspace", "kv_append", "kv_cache", "kv_read",
+            "kv_write", "prompt_workspace", "rotate_heads", "rotation", "token_workspace")
 
 
 def __getattr__(name):

@@ -30,6 +30,7 @@ SOURCES = [
     ("heads.hip", DEVICE),
     ("attend_token.hip", DEVICE),
     ("attend_prompt.hip", DEVICE),
+    ("attend_chunk.hip", DEVICE),
 ]
 
 

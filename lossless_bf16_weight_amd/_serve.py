@@ -36,6 +36,8 @@ _READ = struct.Struct("<" + _CACHE + _TABLE + 2 * _ROWS + "QQII")
 _TOKEN = struct.Struct("<" + _CACHE + _TABLE + 2 * _ROWS + "QQQIIfI")
 _PROMPT = struct.Struct("<" + 4 * _ROWS + "QQQQQQIIIIIf")
 
+_CHUNK = struct.Struct("<" + _CACHE + _TABLE + 2 * _ROWS + "QQQQQIIIIIf")
+
 
 class KVCache(NamedTuple):
     """A paged key-value cache: k and v are [n_pages, n_kv_heads, page_size,
@@ -127,6 +129,12 @@ def _workspace(need: int, given, dev: int, stream):
     elif given.get_device() != dev or not given.is_contiguous():
         raise ValueError(f"workspace: a contiguous tensor on cuda:{dev} is needed")
     return given.data_ptr(), given.numel() * given.element_size(), given
+
+
+def _window(window: int, sinks: int):
+    if window < 0 or sinks < 0:
+        raise ValueError(f"window {window}, sinks {sinks}: numbers from 0 are needed")
+    return min(window, 2 ** 31), min(sinks, 2 ** 31)
 
 
 def _launch(fn, args: bytes, dev: int, stream):
@@ -329,3 +337,36 @@ def attend_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_starts: t
     p, size, keep = _workspace(prompt_workspace(n, m, seqs, h, hk, d, dev), workspace, dev, stream)
     _launch(lib().df11_attend_prompt, _PROMPT.pack(*qr, *kr, *vr, *orow, a, b, p, size, n, m, seqs, h, hk, d,
                                                    ATTEND_CAUSAL if causal else 0, d ** -0.5 if scale is None else scale), dev, stream)
+
+
+@lru_cache(maxsize=4096)
+def chunk_workspace(n_q: int, n_seqs: int, n_heads: int, n_kv_heads: int, head_dim: int, page_size: int, entries: int, window: int = 0,
+                    sinks: int = 0, device: int = 0) -> int:
+    """Bytes of workspace that attend_chunk needs for these sizes (`entries`:
+    the page table's width)."""
+    args = _CHUNK.pack(0, 0, 0, 0, 1, page_size, n_kv_heads, head_dim, 0, 0, 0, 0, entries, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, n_q,
+                       n_seqs, n_heads, ATTEND_CAUSAL, window, sinks, 1.0)
+    return lib().df11_attend_chunk_workspace(args, device)
+
+
+def attend_chunk(q: torch.Tensor, cache: KVCache, pages: torch.Tensor, q_starts: torch.Tensor, lens: torch.Tensor, out: torch.Tensor,
+                 causal: bool = True, window: int = 0, sinks: int = 0, scale=None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """Attention of a chunk of new tokens of each sequence: queries q_starts[s]
+    .. q_starts[s + 1] - 1 (rows of q, [rows, n_heads, head_dim] bfloat16) over
+    the first lens[s] (int32) positions of its pages (int32 [sequences,
+    entries]), the new tokens' among them, into the same rows of out.  causal:
+    query i of n stands at position p = lens[s] - n + i and sees the keys j <=
+    p, with a window above 0 of these only j > p - window and the first `sinks`.
+    A row that sees no key is zero; rows behind the last sequence are left
+    alone.  starts: int32 [sequences + 1].  scale, workspace: as for
+    attend_token."""
+    dev, hk, d, c = _cache_fields(cache)
+    n, h, qr = _rows(q, "q", dev, d)
+    _, _, orow = _rows(out, "out", dev, d, n, h)
+    seqs = lens.shape[0]
+    t = _table(pages, dev, seqs)
+    a, b = _index(q_starts, "q_starts", dev, I32, seqs + 1), _index(lens, "lens", dev, I32, seqs)
+    window, sinks = _window(window, sinks)
+    p, size, keep = _workspace(chunk_workspace(n, seqs, h, hk, d, c[5], t[2], window, sinks, dev), workspace, dev, stream)
+    _launch(lib().df11_attend_chunk, _CHUNK.pack(*c, *t, *qr, *orow, a, b, p, size, n, seqs, h, ATTEND_CAUSAL if causal else 0, window, sinks,
+                                                 d ** -0.5 if scale is None else scale), dev, stream)

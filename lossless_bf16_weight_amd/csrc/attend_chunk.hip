@@ -1,0 +1,576 @@
+// Attention of a chunk of new tokens of each sequence over the paged cache, for
+// gfx950: a prompt's piece, a single token, a whole prompt.
+//
+// Query i of a sequence's n_q stands at position p = n_k - n_q + i of its n_k
+// cached ones and sees the keys j <= p (causal), of these with a window of w
+// the last w and the first `sinks`; or all keys.  s_j = <q_i, k_j>, p_j =
+// 2^(c s_j - m), c = scale log2(e), m the running maximum of c s_j (and a
+// constant: see kSlack), out = sum p_j v_j / sum p_j; a row that sees no key is
+// 0.  Keys in 8 bits become exact BF16 operands; a key's scale multiplies its
+// scores, a value's scale its weights, in 32 bits.
+//
+// Rows, tiles, products and the steps of 64 keys through LDS are those of
+// attend_prompt.hip; rows come from pages, 16 at a time from one page, whose
+// numbers lie in the lanes of a register (64 entries of the table).  Words go
+// from memory into LDS without passing through registers; codes pass through
+// them, converted once by the workgroup.  The steps of a tile are those of the
+// sinks and those of the window.
+//
+// How long the sequences are the host does not know.  Each workgroup finds
+// from q_starts and lens how the work of the whole call is divided: the steps
+// of all tiles over `places` workgroups give a quota, and a sequence's tiles
+// are split into as many parts as their steps hold quotas.  A second kernel
+// joins the parts.
+#include <type_traits>
+
+#include "attend_tiles.hpp"
+
+namespace df11 {
+
+// x * y, but 0 where either is 0, whatever the other.
+__device__ float mul_or_zero(float x, float y) __asm("llvm.amdgcn.fmul.legacy");
+
+namespace {
+
+constexpr uint32_t kWaves = 4, kThreads = 64 * kWaves;
+constexpr uint32_t kWaveRows = 32;
+constexpr int kHalves = kPromptKeys / 32;      // of a step: 32 keys are a product's rows
+constexpr int kAhead = 4;                      // reads of K ahead of the products
+
+// What a workgroup does: a part of a tile of a sequence.
+struct Piece {
+    uint32_t seq, n_q, n_k;
+    int32_t q0;
+    uint32_t tile, part, parts, per;      // of `parts`, each of `per` steps
+    uint32_t place;                       // where the parts of the tile lie in the workspace
+};
+
+__device__ __forceinline__ uint32_t of_lane(uint32_t x, uint32_t lane) { return __builtin_amdgcn_readlane(x, lane); }
+
+// Finds work item `item` (kJoin: the tile of that number among those that are
+// split).  False where there is none.
+template <bool kSplit, bool kJoin>
+__device__ __forceinline__ bool find_piece(const ChunkArgs &a, uint32_t item, Piece *p) {
+    const uint32_t lane = threadIdx.x & 63u;
+    uint32_t q0 = 0, n_q = 0, n_k = 0, tiles = 0, steps = 0;
+    const auto look = [&](uint32_t s0) {
+        const uint32_t s = min(s0 + lane, a.n_seqs - 1);
+        const int32_t from = a.q_starts[s], to = a.q_starts[s + 1];
+        const bool ok = s0 + lane < a.n_seqs && from >= 0 && to >= from && (uint32_t)to <= a.n_q;
+        q0 = from;
+        n_q = ok ? to - from : 0;
+        n_k = (uint32_t)min((int64_t)max(a.lens[s], 0), (int64_t)a.t.width << a.c.shift);
+        tiles = (n_q * a.group + kPromptTile - 1) / kPromptTile;
+        steps = min((n_k + kPromptKeys - 1) / kPromptKeys, a.most_steps);
+    };
+    uint32_t quota = 0;
+    if (kSplit) {
+        float total = 0;
+        for (uint32_t s0 = 0; s0 < a.n_seqs; s0 += 64) {
+            look(s0);
+            total += (float)tiles * (float)steps;
+        }
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) total += __shfl_xor(total, d);
+        // (above the quotient, whatever the sum's rounding: the parts of all
+        // split tiles are then no more than the places)
+        quota = (uint32_t)fminf(total * a.by_places * (1.0f + 0x1p-18f), 4.0e9f) + 1;
+    } else if (a.n_seqs > 64) {
+        uint32_t tile;
+        const uint32_t s = sequence_of_slot(a.q_starts, a.n_seqs, item, a.group, 7, &tile);
+        const int32_t from = a.q_starts[s], to = a.q_starts[s + 1];
+        if (from < 0 || to < from || (uint32_t)to > a.n_q) return false;
+        const uint32_t n_rows = (uint32_t)(to - from) * a.group;
+        if (tile > n_rows / kPromptTile || tile * kPromptTile >= n_rows) return false;
+        p->seq = s, p->q0 = from, p->n_q = to - from;
+        p->n_k = (uint32_t)min((int64_t)max(a.lens[s], 0), (int64_t)a.t.width << a.c.shift);
+        p->tile = tile, p->part = 0, p->parts = 1, p->per = ~0u, p->place = 0;
+        return true;
+    }
+    uint32_t items_before = 0, places_before = 0;
+    for (uint32_t s0 = 0; s0 < a.n_seqs; s0 += 64) {
+        if (!kSplit || a.n_seqs > 64 || s0 == 0) look(s0);
+        const uint32_t parts = kSplit ? max(1u, min(steps / quota, steps >> a.least_shift)) : 1;
+        const uint32_t places = parts > 1 ? tiles * parts : 0, items = kJoin ? (parts > 1 ? tiles : 0) : tiles * parts;
+        uint32_t items_to = items, places_to = places;     // sums up to this lane
+        for (uint32_t d = 1; d < min(a.n_seqs, 64u); d *= 2) {
+            const uint32_t x = __shfl_up(items_to, d), y = kSplit ? __shfl_up(places_to, d) : 0;
+            if (lane >= d) items_to += x, places_to += y;
+        }
+        const uint32_t before = items_before + items_to - items;
+        const uint64_t found = __ballot(item >= before && item - before < items);
+        if (found) {
+            const uint32_t x = (uint32_t)__builtin_ctzll(found);
+            p->seq = s0 + x;
+            p->q0 = of_lane(q0, x);
+            p->n_q = of_lane(n_q, x);
+            p->n_k = of_lane(n_k, x);
+            p->parts = of_lane(parts, x);
+            p->per = kSplit ? (of_lane(steps, x) + p->parts - 1) / p->parts : ~0u;
+            const uint32_t in = item - of_lane(before, x), by = kJoin ? 1 : p->parts, at = in / by;
+            p->part = in - at * by;
+            // (the last tiles of a sequence, which see the most keys, come first)
+            p->tile = of_lane(tiles, x) - 1 - at;
+            p->place = places_before + of_lane(places_to - places, x) + at * p->parts;
+            return true;
+        }
+        items_before += of_lane(items_to, 63);
+        places_before += of_lane(places_to, 63);
+    }
+    return false;
+}
+
+// The keys that a query sees: those below `end`, of these those from `begin` on
+// and the sinks.
+struct Seen {
+    uint32_t begin, end;
+};
+
+__device__ __forceinline__ Seen seen_by(const ChunkArgs &a, uint32_t query, uint32_t n_q, uint32_t n_k) {
+    if (!a.causal) return Seen{0, n_k};
+    const int64_t l = (int64_t)query + 1 + n_k - n_q;
+    const uint32_t end = l < 0 ? 0 : l > n_k ? n_k : (uint32_t)l;
+    return Seen{a.window && end > a.window ? end - a.window : 0, end};
+}
+
+// The steps of a tile: those of the sinks, then those of the window.
+struct Steps {
+    uint32_t sinks, skipped, n;
+    __device__ __forceinline__ uint32_t key(uint32_t step) const { return (step < sinks ? step : step + skipped) * kPromptKeys; }
+};
+
+__device__ __forceinline__ Steps steps_of(const ChunkArgs &a, const Piece &p) {
+    const uint32_t row0 = p.tile * kPromptTile, n_rows = p.n_q * a.group;
+    const Seen first = seen_by(a, over_group(a, row0), p.n_q, p.n_k);
+    const uint32_t end = seen_by(a, over_group(a, min(row0 + kPromptTile, n_rows) - 1), p.n_q, p.n_k).end;
+    Steps s;
+    s.sinks = min((a.sinks + kPromptKeys - 1) / kPromptKeys, first.begin / kPromptKeys);
+    s.skipped = first.begin / kPromptKeys - s.sinks;
+    s.n = (end + kPromptKeys - 1) / kPromptKeys - s.skipped;
+    return s;
+}
+
+template <int D, bool kInt8, bool kSplit>
+__global__ __launch_bounds__(kThreads, 2) void attend_chunk_kernel(ChunkArgs a) {
+    constexpr int kChunks = D / 8;                           // 16-byte chunks of a row of words
+    constexpr int kLoads = kPromptKeys * kChunks / kThreads; // chunks of words a thread stages
+    constexpr int kCodeLoads = kLoads / 2;                   // chunks of codes
+    constexpr int kDTiles = D / 32;
+    constexpr int kDSteps = D / 16;
+    __shared__ __attribute__((aligned(16))) uint8_t kt0[kPromptKeys * D * 2], kt1[kPromptKeys * D * 2];
+    __shared__ __attribute__((aligned(16))) uint8_t vt0[kPromptKeys * D * 2], vt1[kPromptKeys * D * 2];
+    __shared__ __attribute__((aligned(16))) float sc0[kInt8 ? 2 * kPromptKeys : 4], sc1[kInt8 ? 2 * kPromptKeys : 4];
+
+    const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t lane_of_wave = lane, col = lane & 31u, half = lane >> 5;
+
+    // (workgroups are dealt to the eight XCDs in turn: kv heads vary fastest,
+    // so that the tiles of one meet in one L2)
+    const uint32_t kv_head = blockIdx.x % a.c.kv_heads;
+    Piece p;
+    if (!find_piece<kSplit, false>(a, blockIdx.x / a.c.kv_heads, &p)) return;
+    const uint32_t n_q = p.n_q, n_k = p.n_k, n_rows = n_q * a.group;
+    const uint32_t row0 = p.tile * kPromptTile;
+    const Steps steps = steps_of(a, p);
+    uint32_t step_begin = 0, step_end = steps.n;
+    bool whole = true;
+    if (kSplit) {
+        step_begin = p.part * p.per;
+        if (step_begin >= steps.n && p.part) return;
+        step_end = min(step_begin + p.per, steps.n);
+        whole = steps.n <= p.per;
+    }
+
+    const uint32_t wave_first = row0 + wave * kWaveRows, row = wave_first + col;
+    const bool real = row < n_rows;
+    const uint32_t query = over_group(a, row), head = kv_head * a.group + row - query * a.group;
+    // (rows past the last compute on zero queries, and are not stored)
+    const Seen seen = real ? seen_by(a, query, n_q, n_k) : Seen{0, n_k};
+    // The wave's rows see no key from wave_end on and none below wave_begin but
+    // sinks; they all see those from clear_begin (and the sinks) to clear_end.
+    const Seen wave_low = seen_by(a, over_group(a, wave_first), n_q, n_k);
+    const Seen wave_high = seen_by(a, over_group(a, min(wave_first + kWaveRows, n_rows) - 1), n_q, n_k);
+    const uint32_t wave_begin = wave_low.begin, wave_end = wave_first < n_rows ? wave_high.end : 0;
+    const uint32_t clear_begin = wave_high.begin, clear_end = wave_low.end;
+
+    u32x4 q[kDSteps];
+#pragma unroll
+    for (int i = 0; i < kDSteps; ++i) {
+        q[i] = u32x4{0, 0, 0, 0};
+        if (real) q[i] = *reinterpret_cast<const u32x4 *>(a.q.data + (int64_t)(p.q0 + query) * a.q.row + head * a.q.head + 16 * i + 8 * half);
+    }
+
+    f32x16 o[kDTiles];
+    float m, l;
+    const float log2_n = log2_up(n_k);
+    const auto start = [&] {
+#pragma unroll
+        for (int i = 0; i < kDTiles; ++i) o[i] = f32x16{};
+        m = -__builtin_inff();
+        l = 0;
+    };
+
+    // 64 entries of the sequence's table, a lane each, asked for a step before
+    // they are used.
+    uint32_t entries_from = 0, entries = 0;
+    const auto read_entries = [&](uint32_t key0) {
+        entries_from = key0 >> a.c.shift;
+        const uint32_t at = min(entries_from + lane, (n_k - 1) >> a.c.shift);
+        entries = min((uint32_t)a.t.pages[p.seq * a.t.stride + at], a.c.n_pages - 1);
+    };
+    const auto need_entries = [&](uint32_t key0) {
+        if (key0 >> a.c.shift < entries_from || (key0 + kPromptKeys - 1) >> a.c.shift > entries_from + 63) read_entries(key0);
+    };
+    // The cache's row of 16 keys' first (the host keeps their number below 2^32).
+    const auto row_of = [&](uint32_t key) {
+        return ((of_lane(entries, (key >> a.c.shift) - entries_from) * a.c.kv_heads + kv_head) << a.c.shift) + (key & ((1u << a.c.shift) - 1));
+    };
+
+    // Words: a step's K and V rows go from memory into LDS without passing
+    // through registers, one step ahead: the chunk that lane `at` of the tile
+    // holds is the one that belongs there.  Rows past the sequence's end are
+    // out of the descriptor's range and arrive as zeros.
+    constexpr uint32_t kRowsALoad = kThreads / kChunks;
+    const uint32_t tile_row = threadIdx.x / kChunks, chunk = threadIdx.x % kChunks;
+    const uint32_t k_offset = (tile_row & 15) * (2 * D) + 16 * k_chunk<D>(tile_row, chunk);
+    const uint32_t v_offset = (tile_row & 15) * (2 * D) + 16 * v_chunk<D>(tile_row, chunk);
+    const auto load = [&](uint32_t key0, uint8_t *kt, uint8_t *vt) {
+        const uint32_t left = n_k - key0;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const uint64_t at = (uint64_t)row_of(key0 + i * kRowsALoad + (D == 64 ? 16 * (wave >> 1) : 0)) * (2 * D);
+            const __amdgpu_buffer_rsrc_t kr = __builtin_amdgcn_make_buffer_rsrc((void *)(a.c.k + at), 0, kOutOfRange, 0x00020000);
+            const __amdgpu_buffer_rsrc_t vr = __builtin_amdgcn_make_buffer_rsrc((void *)(a.c.v + at), 0, kOutOfRange, 0x00020000);
+            const bool in = tile_row + i * kRowsALoad < left;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(kr, (DF11_LDS void *)(kt + (i * kThreads + wave * 64) * 16), 16, in ? k_offset : kOutOfRange, 0, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(vr, (DF11_LDS void *)(vt + (i * kThreads + wave * 64) * 16), 16, in ? v_offset : kOutOfRange, 0, 0, 0);
+        }
+    };
+    const auto arrived = [&] {
+        __builtin_amdgcn_s_waitcnt(0x0F70);        // vmcnt(0): this wave's rows
+        __syncthreads();                           // and the others'; and all are done with the step before
+    };
+
+    // 8 bits: codes go through registers, one step ahead, and become words on
+    // their way into LDS; scales beside them, K's of 64 rows and then V's.
+    constexpr uint32_t kCodeChunks = D / 16, kCodeRows = kThreads / kCodeChunks;
+    const uint32_t code_row = threadIdx.x / kCodeChunks, code_chunk = threadIdx.x % kCodeChunks;
+    u32x4 kw[kCodeLoads], vw[kCodeLoads];
+    float scale_w = 0;
+    const auto load_codes = [&](uint32_t key0) {
+        const uint32_t left = n_k - key0;
+#pragma unroll
+        for (int i = 0; i < kCodeLoads; ++i) {
+            // (a wave's rows: 8 or 16 neighbours)
+            const uint32_t first = key0 + i * kCodeRows + wave * (64 / kCodeChunks);
+            const uint64_t at = ((uint64_t)row_of(first & ~15u) + (first & 15)) * D;
+            const uint32_t from = (lane / kCodeChunks) * D + 16 * code_chunk;
+            kw[i] = vw[i] = u32x4{0, 0, 0, 0};
+            if (code_row + i * kCodeRows < left) {
+                kw[i] = *reinterpret_cast<const u32x4 *>(a.c.k + at + from);
+                vw[i] = *reinterpret_cast<const u32x4 *>(a.c.v + at + from);
+            }
+        }
+        scale_w = 0;
+        if (wave < 2) {
+            // (16 lanes share a page's row)
+            uint32_t r = row_of(key0);
+#pragma unroll
+            for (int g = 1; g < 4; ++g) {
+                const uint32_t other = row_of(key0 + 16 * g);
+                if ((int)(lane >> 4) == g) r = other;
+            }
+            if (lane < left) scale_w = (wave ? a.c.v_scale : a.c.k_scale)[(uint64_t)r + (lane & 15)];
+        }
+    };
+    const auto store_codes = [&](uint8_t *kt, uint8_t *vt, float *sc) {
+#pragma unroll
+        for (int i = 0; i < kCodeLoads; ++i) {
+            const uint32_t r = code_row + i * kCodeRows;
+            *reinterpret_cast<u32x4 *>(kt + k_at<D>(r, 2 * code_chunk)) = bf16_of_bytes8(u32x2{kw[i].x, kw[i].y});
+            *reinterpret_cast<u32x4 *>(kt + k_at<D>(r, 2 * code_chunk + 1)) = bf16_of_bytes8(u32x2{kw[i].z, kw[i].w});
+            *reinterpret_cast<u32x4 *>(vt + v_at<D>(r, 2 * code_chunk)) = bf16_of_bytes8(u32x2{vw[i].x, vw[i].y});
+            *reinterpret_cast<u32x4 *>(vt + v_at<D>(r, 2 * code_chunk + 1)) = bf16_of_bytes8(u32x2{vw[i].z, vw[i].w});
+        }
+        if (wave < 2) sc[threadIdx.x] = scale_w;
+    };
+
+    // One step's keys.  kCareful: values that are infinite or NaN at keys which
+    // only some rows see do not reach the others.
+    const auto step = [&](auto careful, uint32_t key0, const uint8_t *kt, const uint8_t *vt, const float *sc) {
+        constexpr bool kCareful = decltype(careful)::value;
+        if (key0 >= wave_end || (key0 + kPromptKeys <= wave_begin && key0 >= a.sinks)) return;
+        // (the careful pass computes its LDS addresses in each step: there are
+        // no registers to keep them in)
+        uint32_t own = lane_of_wave;
+        if (kCareful) asm volatile("" : "+v"(own));
+        const uint32_t lane = own, col = own & 31u, half = own >> 5;
+
+        f32x16 s[kHalves];
+#pragma unroll
+        for (int t = 0; t < kHalves; ++t) s[t] = f32x16{};
+#pragma unroll
+        for (int i = 0; i < kDSteps; ++i)
+#pragma unroll
+            for (int t = 0; t < kHalves; ++t) {
+                const u32x4 w = *reinterpret_cast<const u32x4 *>(kt + k_at<D>(32 * t + col, 2 * i + half));
+                s[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(w), as_bf16x8(q[i]), s[t], 0, 0, 0);
+            }
+        // (four reads of K ahead of the products)
+        __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+#pragma unroll
+        for (int i = 0; i < kHalves * kDSteps - kAhead; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, kAhead, 0);
+        if (kInt8) {
+#pragma unroll
+            for (int t = 0; t < kHalves; ++t)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const f32x4 w = *reinterpret_cast<const f32x4 *>(sc + 32 * t + 8 * g + 4 * half);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s[t][4 * g + i] *= w[i];
+                }
+        }
+        if (key0 + kPromptKeys > clear_end || (key0 < clear_begin && key0 + kPromptKeys > a.sinks)) {
+#pragma unroll
+            for (int t = 0; t < kHalves; ++t)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const uint32_t key = key0 + 32 * t + 8 * (i / 4) + 4 * half + i % 4;
+                    if (key >= seen.end || (key < seen.begin && key >= a.sinks)) s[t][i] = -__builtin_inff();
+                }
+        }
+        float top = -__builtin_inff();
+#pragma unroll
+        for (int t = 0; t < kHalves; ++t)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = fmaxf(top, s[t][i]);
+        const f32x2 halves = with_lane_32(top);
+        top = fmaxf(halves.x, halves.y) * a.log2_scale;
+        if (__any(top > m - log2_n)) {
+            const float next = fmaxf(m, top + (kSlack + log2_n));
+            const float keep = exp2_fast(m - (next == -__builtin_inff() ? 0.0f : next));
+            m = next;
+            l *= keep;
+#pragma unroll
+            for (int i = 0; i < kDTiles; ++i) o[i] *= keep;
+        }
+        const float base = m == -__builtin_inff() ? 0.0f : m;
+#pragma unroll
+        for (int t = 0; t < kHalves; ++t) {
+#pragma unroll
+            for (int st = 0; st < 2; ++st) {
+                u32x4 p;
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    float e[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        e[i] = exp2_fast(__builtin_fmaf(s[t][8 * st + 4 * g + i], a.log2_scale, -base));
+                        l += e[i];
+                    }
+                    if (kInt8) {
+                        // (a weight of 0, a masked key's too, stays 0 whatever the scale)
+                        const f32x4 w = *reinterpret_cast<const f32x4 *>(sc + kPromptKeys + 32 * t + 16 * st + 8 * g + 4 * half);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) e[i] = mul_or_zero(e[i], w[i]);
+                    }
+                    p[2 * g] = pack_bf16(e[0], e[1]);
+                    p[2 * g + 1] = pack_bf16(e[2], e[3]);
+                }
+#pragma unroll
+                for (int i = 0; i < kDTiles; ++i) {
+                    const uint32_t j = lane & 15u, r = 32 * t + 16 * st + 4 * half + (j >> 2);
+                    const uint32_t chunk = 4 * i + 2 * ((lane >> 4) & 1u) + ((j & 3) >> 1);
+                    const s16x4 b0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((DF11_LDS s16x4 *)(vt + v_at<D>(r, chunk) + 8 * (j & 1)));
+                    const s16x4 b1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((DF11_LDS s16x4 *)(vt + v_at<D>(r + 8, chunk) + 8 * (j & 1)));
+                    const u32x2 w0 = __builtin_bit_cast(u32x2, b0), w1 = __builtin_bit_cast(u32x2, b1);
+                    u32x4 w = {w0.x, w0.y, w1.x, w1.y};
+                    if (kCareful) {
+                        // Values that are not finite leave the product (0 times
+                        // one of them is not 0) and are counted apart, over the
+                        // keys that the row sees (whose score is not that of a
+                        // masked one): ones where they are +inf or NaN, and
+                        // where they are -inf or NaN.
+                        u32x4 here, up, down;
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            here[x] = up[x] = down[x] = 0;
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                const uint32_t h = w[x] >> (16 * y) & 0xFFFFu, one = 0x3F80u << (16 * y);
+                                const bool odd = (h & 0x7F80u) == 0x7F80u, nan = odd && (h & 0x7Fu);
+                                if (s[t][8 * st + 2 * x + y] != -__builtin_inff()) here[x] |= one;
+                                if (nan || h == 0x7F80u) up[x] |= one;
+                                if (nan || h == 0xFF80u) down[x] |= one;
+                                if (odd) w[x] &= 0xFFFF0000u >> (16 * y);
+                            }
+                        }
+                        f32x16 n = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(up), as_bf16x8(here), f32x16{}, 0, 0, 0);
+#pragma unroll
+                        for (int x = 0; x < 16; ++x)
+                            if (n[x] > 0) o[i][x] += __builtin_inff();
+                        __builtin_amdgcn_sched_barrier(0);
+                        n = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(down), as_bf16x8(here), f32x16{}, 0, 0, 0);
+#pragma unroll
+                        for (int x = 0; x < 16; ++x)
+                            if (n[x] > 0) o[i][x] -= __builtin_inff();
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                    o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(w), as_bf16x8(p), o[i], 0, 0, 0);
+                }
+            }
+        }
+    };
+
+    start();
+    if (step_begin < step_end) read_entries(steps.key(step_begin));
+    if constexpr (kInt8) {
+        if (step_begin < step_end) {
+            load_codes(steps.key(step_begin));
+            if (step_begin + 1 < step_end) need_entries(steps.key(step_begin + 1));
+            store_codes(kt0, vt0, sc0);
+        }
+        const auto go = [&](uint32_t i, const uint8_t *kt, const uint8_t *vt, const float *sc, uint8_t *kt_next, uint8_t *vt_next, float *sc_next) {
+            __syncthreads();
+            const bool more = i + 1 < step_end;
+            if (more) load_codes(steps.key(i + 1));
+            if (i + 2 < step_end) need_entries(steps.key(i + 2));
+            step(std::false_type{}, steps.key(i), kt, vt, sc);
+            if (more) store_codes(kt_next, vt_next, sc_next);
+        };
+        for (uint32_t i = step_begin; i < step_end; i += 2) {
+            go(i, kt0, vt0, sc0, kt1, vt1, sc1);
+            if (i + 1 < step_end) go(i + 1, kt1, vt1, sc1, kt0, vt0, sc0);
+        }
+    } else {
+        if (step_begin < step_end) load(steps.key(step_begin), kt0, vt0);
+        if (step_begin + 1 < step_end) need_entries(steps.key(step_begin + 1));
+        const auto go = [&](uint32_t i, const uint8_t *kt, const uint8_t *vt, uint8_t *kt_next, uint8_t *vt_next) {
+            arrived();
+            if (i + 1 < step_end) load(steps.key(i + 1), kt_next, vt_next);
+            if (i + 2 < step_end) need_entries(steps.key(i + 2));
+            step(std::false_type{}, steps.key(i), kt, vt, nullptr);
+        };
+        for (uint32_t i = step_begin; i < step_end; i += 2) {
+            go(i, kt0, vt0, kt1, vt1);
+            if (i + 1 < step_end) go(i + 1, kt1, vt1, kt0, vt0);
+        }
+        if (a.causal) {
+            // A result that is not finite may come from a value that its row does
+            // not see: the product of its weight, 0, with an infinity is NaN.  Then
+            // the workgroup takes its keys once more, with care.
+            float most = 0;       // (NaN where one is)
+#pragma unroll
+            for (int i = 0; i < kDTiles; ++i)
+#pragma unroll
+                for (int x = 0; x < 16; ++x) most = __builtin_elementwise_maximum(most, __builtin_fabsf(o[i][x]));
+            if (__syncthreads_or(!(most < __builtin_inff()))) {
+                start();
+                for (uint32_t i = step_begin; i < step_end; ++i) {
+                    need_entries(steps.key(i));
+                    load(steps.key(i), kt0, vt0);
+                    arrived();
+                    step(std::true_type{}, steps.key(i), kt0, vt0, nullptr);
+                    __syncthreads();
+                }
+            }
+        }
+    }
+    const f32x2 l_halves = with_lane_32(l);
+    l = l_halves.x + l_halves.y;
+    if (kSplit && !whole) {
+        if (wave_first >= n_rows) return;
+        // as the lanes hold them, for the lanes of the join
+        const uint64_t at = ((uint64_t)(p.place + p.part) * a.c.kv_heads + kv_head) * kWaves + wave;
+        f32x4 *const part = reinterpret_cast<f32x4 *>(a.part) + at * (kDTiles * 4 * 64) + lane;
+#pragma unroll
+        for (int i = 0; i < kDTiles; ++i)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) part[(4 * i + g) * 64] = f32x4{o[i][4 * g], o[i][4 * g + 1], o[i][4 * g + 2], o[i][4 * g + 3]};
+        if (half == 0) reinterpret_cast<f32x2 *>(a.part_ml)[at * kWaveRows + col] = f32x2{m, l};
+        return;
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    uint16_t *const op = a.out.data + (int64_t)(p.q0 + query) * a.out.row + head * a.out.head;
+#pragma unroll
+    for (int i = 0; i < kDTiles; ++i) store_tile(o[i] * inv, op + 32 * i, half, real);
+}
+
+// Joins the parts of 32 rows (those of wave blockIdx.y of a split tile):
+// out = sum_a w_a o_a / sum_a w_a l_a with w_a = 2^(m_a - max m), the maximum
+// taken as the parts come.  A wave takes 32 columns.
+template <int D>
+__global__ __launch_bounds__(64 * D / 32) void join_chunk_kernel(ChunkArgs a) {
+    constexpr int kDTiles = D / 32;
+    constexpr int kBatch = 2;       // parts in flight
+    const uint32_t lane = threadIdx.x & 63u, i = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t col = lane & 31u, half = lane >> 5, kv_head = blockIdx.x % a.c.kv_heads;
+    Piece p;
+    if (!find_piece<true, true>(a, blockIdx.x / a.c.kv_heads, &p)) return;
+    const uint32_t first = p.tile * kPromptTile + blockIdx.y * kWaveRows, row = first + col, n_rows = p.n_q * a.group;
+    const uint32_t n_steps = steps_of(a, p).n;
+    if (first >= n_rows || n_steps <= p.per) return;
+    const uint32_t parts = (n_steps + p.per - 1) / p.per;
+    const uint64_t at = ((uint64_t)p.place * a.c.kv_heads + kv_head) * kWaves + blockIdx.y, next_part = (uint64_t)a.c.kv_heads * kWaves;
+    const f32x2 *const ml = reinterpret_cast<const f32x2 *>(a.part_ml) + at * kWaveRows + col;
+    const f32x4 *const part = reinterpret_cast<const f32x4 *>(a.part) + (at * kDTiles + i) * 256 + lane;
+    f32x16 o = {};
+    float l = 0, m = -__builtin_inff();
+    for (uint32_t s = 0; s < parts; s += kBatch) {
+        f32x2 stat[kBatch];
+        f32x4 v[kBatch][4];
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x) {
+            const uint32_t from = min(s + x, parts - 1);
+            stat[x] = ml[from * next_part * kWaveRows];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) v[x][g] = __builtin_nontemporal_load(part + from * next_part * (kDTiles * 256) + g * 64);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        float next = m;
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x)
+            if (s + x < parts) next = fmaxf(next, stat[x].x);
+        const float base = next == -__builtin_inff() ? 0.0f : next, keep = exp2_fast(m - base);
+        m = next;
+        l *= keep;
+        o *= keep;
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x) {
+            if (s + x >= parts) break;      // (a part past the last was not written)
+            const float w = exp2_fast(stat[x].x - base);
+            l += w * stat[x].y;
+#pragma unroll
+            for (int y = 0; y < 16; ++y) o[y] += w * v[x][y / 4][y % 4];
+        }
+    }
+    const uint32_t query = over_group(a, row), head = kv_head * a.group + row - query * a.group;
+    store_tile(o * (l == 0.0f ? 0.0f : 1.0f / l), a.out.data + (int64_t)(p.q0 + query) * a.out.row + head * a.out.head + 32 * i, half, row < n_rows);
+}
+
+template <int D, bool kInt8>
+auto kernel_of(bool split) {
+    return split ? attend_chunk_kernel<D, kInt8, true> : attend_chunk_kernel<D, kInt8, false>;
+}
+
+}  // namespace
+
+hipError_t launch_attend_chunk(const ChunkArgs &a, uint32_t head_dim, bool int8, hipStream_t stream) {
+    const bool split = a.places != 0;
+    const auto kernel = head_dim == 64 ? (int8 ? kernel_of<64, true>(split) : kernel_of<64, false>(split))
+                                       : (int8 ? kernel_of<128, true>(split) : kernel_of<128, false>(split));
+    hipLaunchKernelGGL(kernel, dim3((a.tile_slots + a.places) * a.c.kv_heads), dim3(kThreads), 0, stream, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !split) return e;
+    // (a split tile has two parts at least)
+    const uint32_t tiles = a.places / 2 < a.tile_slots ? a.places / 2 : a.tile_slots;
+    hipLaunchKernelGGL(head_dim == 64 ? join_chunk_kernel<64> : join_chunk_kernel<128>, dim3(tiles * a.c.kv_heads, kWaves), dim3(2 * head_dim), 0,
+                       stream, a);
+    return hipGetLastError();
+}
+
+}  // namespace df11

@@ -107,6 +107,14 @@ df11_status launched(hipError_t e, const char *what) {
     return e == hipSuccess ? DF11_OK : report_error(DF11_E_HIP, "%s launch: %s", what, hipGetErrorString(e));
 }
 
+// x / n = (x * magic >> 32) >> shift for n > 1: with 2^shift < n <= 2^(shift + 1)
+// and the multiplier rounded up from 2^(32 + shift) / n, the quotient is exact
+// for x < 2^31.
+void divide_by(uint32_t n, uint32_t *magic, uint32_t *shift) {
+    *shift = n > 1 ? 31 - (uint32_t)__builtin_clz(n - 1) : 0;
+    *magic = n > 1 ? (uint32_t)((((uint64_t)1 << (32 + *shift)) + n - 1) / n) : 0;
+}
+
 float log2_scale(float scale) { return (float)((double)scale * 1.4426950408889634074); }
 
 df11_status check_rotation(const df11_rotation &r, uint32_t head_dim) {
@@ -252,6 +260,50 @@ df11_status check_prompt_sizes(const df11_attend_prompt_args &a) {
     if (a.n_q * (a.n_heads / a.n_kv_heads) > 0x7FFFFFFFu || a.n_kv_heads > kMostGroups || a.n_seqs > kMostGroups ||
         prompt_tile_slots(a) * a.n_kv_heads > kMostGroups)
         return report_error(DF11_E_UNSUPPORTED, "%llu rows of %u heads in %u sequences", (unsigned long long)a.n_q, a.n_heads, a.n_seqs);
+    return DF11_OK;
+}
+
+// What attend_chunk's workgroups need for dividing a call's work, whose lengths
+// the host does not know: the places of parts, two workgroups for each compute
+// unit, and the least steps of a part.  Sequences of many are taken whole: each
+// workgroup would read all their lengths.
+struct ChunkSplit {
+    uint32_t most_steps, places, least_shift;
+};
+
+constexpr uint32_t kChunkMostPlanned = 512;     // sequences
+
+uint64_t chunk_tile_slots(const df11_attend_chunk_args &a) { return a.n_q * (a.n_heads / a.cache.n_kv_heads) / kPromptTile + a.n_seqs; }
+
+ChunkSplit chunk_split(const df11_attend_chunk_args &a, int dev) {
+    ChunkSplit s{~0u, 0, 2};
+    const uint64_t group = a.n_heads / a.cache.n_kv_heads, positions = (uint64_t)a.table.width * a.cache.page_size;
+    // (a tile's queries are (kPromptTile - 1) / group + 2 at most, the windows of n of
+    // them w + n - 1 keys, which lie in so many steps)
+    if (a.window && a.window < positions)
+        s.most_steps = (uint32_t)((a.window + (kPromptTile - 1) / group + 1 + 2 * (kPromptKeys - 1)) / kPromptKeys +
+                                  ceil_div(std::min<uint64_t>(a.sinks, positions), kPromptKeys));
+    const uint64_t steps = std::min<uint64_t>(ceil_div(positions, kPromptKeys), s.most_steps);
+    const uint64_t places = 2 * compute_units(dev) / a.cache.n_kv_heads, parts = steps >> s.least_shift;
+    if (a.n_q == 0 || a.n_seqs == 0 || a.n_seqs > kChunkMostPlanned || places < 2 || parts < 2) return s;
+    s.places = (uint32_t)std::min(places, chunk_tile_slots(a) * parts);
+    return s;
+}
+
+uint64_t chunk_bytes(const df11_attend_chunk_args &a, const ChunkSplit &s) {
+    return (uint64_t)s.places * a.cache.n_kv_heads * kPromptTile * (a.cache.head_dim + 2) * sizeof(float);
+}
+
+df11_status check_chunk_sizes(const df11_attend_chunk_args &a) {
+    df11_status st = check_cache_sizes(a.cache);
+    if (st) return st;
+    const uint32_t kv = a.cache.n_kv_heads;
+    if (a.n_heads == 0 || a.n_heads % kv) return report_error(DF11_E_ARG, "%u heads over %u kv heads", a.n_heads, kv);
+    if (a.n_q > 0x7FFFFFFFu || a.n_q * (a.n_heads / kv) > 0x7FFFFFFFu || a.n_seqs > kMostGroups ||
+        chunk_tile_slots(a) * kv > kMostGroups - 2048)     // (and two places a compute unit)
+        return report_error(DF11_E_UNSUPPORTED, "%llu rows of %u heads in %u sequences", (unsigned long long)a.n_q, a.n_heads, a.n_seqs);
+    if (a.flags & ~DF11_ATTEND_CAUSAL) return report_error(DF11_E_ARG, "attend_chunk: flags %u", a.flags);
+    if (a.window && !(a.flags & DF11_ATTEND_CAUSAL)) return report_error(DF11_E_ARG, "attend_chunk: a window needs DF11_ATTEND_CAUSAL");
     return DF11_OK;
 }
 
@@ -405,6 +457,52 @@ extern "C" df11_status df11_attend_token(const df11_attend_token_args *a, int hi
     return launched(launch_attend_token(t, d, a->cache.store == DF11_KV_INT8, stream), "attend_token");
 }
 
+extern "C" uint64_t df11_attend_chunk_workspace(const df11_attend_chunk_args *a, int hip_device) {
+    if (!a || check_chunk_sizes(*a) || a->table.width == 0) return 0;
+    return chunk_bytes(*a, chunk_split(*a, hip_device));
+}
+
+extern "C" df11_status df11_attend_chunk(const df11_attend_chunk_args *a, int hip_device, hipStream_t stream) {
+    if (!a) return report_error(DF11_E_ARG, "attend_chunk: NULL arguments");
+    TRY(check_chunk_sizes(*a));
+    TRY(check_cache(a->cache));
+    TRY(check_scale(a->scale));
+    const uint32_t d = a->cache.head_dim, kv = a->cache.n_kv_heads;
+    TRY(check_rows("q", a->q, a->n_q, a->n_heads, d, false));
+    TRY(check_rows("out", a->out, a->n_q, a->n_heads, d, true));
+    if (a->n_q == 0 || a->n_seqs == 0) return DF11_OK;
+    TRY(check_table(a->table, a->cache));
+    if (bad_index(a->q_starts, 4) || bad_index(a->lens, 4)) return report_error(DF11_E_ARG, "attend_chunk: q_starts or lens NULL or misaligned");
+    const ChunkSplit s = chunk_split(*a, hip_device);
+    TRY(check_workspace(a->workspace, a->workspace_bytes, chunk_bytes(*a, s)));
+    ON_DEVICE(hip_device);
+    ChunkArgs c{};
+    c.c = view_of(a->cache);
+    c.t = tables_of(a->table);
+    c.q = rows_of(a->q);
+    c.out = rows_of(a->out);
+    c.q_starts = a->q_starts;
+    c.lens = a->lens;
+    c.log2_scale = log2_scale(a->scale);
+    c.n_seqs = a->n_seqs;
+    c.n_q = (uint32_t)a->n_q;
+    c.group = a->n_heads / kv;
+    c.causal = a->flags & DF11_ATTEND_CAUSAL;
+    // (a window as long as the table is none)
+    const uint32_t positions = a->table.width * a->cache.page_size;
+    c.window = a->window < positions ? a->window : 0;
+    c.sinks = c.window ? std::min(a->sinks, positions) : 0;
+    divide_by(c.group, &c.group_magic, &c.group_shift);
+    c.most_steps = s.most_steps;
+    c.tile_slots = (uint32_t)chunk_tile_slots(*a);
+    c.places = s.places;
+    c.least_shift = s.least_shift;
+    c.by_places = s.places ? 1.0f / s.places : 0;
+    c.part = (float *)a->workspace;
+    c.part_ml = c.part + (uint64_t)s.places * kv * kPromptTile * d;
+    return launched(launch_attend_chunk(c, d, a->cache.store == DF11_KV_INT8, stream), "attend_chunk");
+}
+
 extern "C" uint64_t df11_attend_prompt_workspace(const df11_attend_prompt_args *a, int hip_device) {
     if (!a || check_prompt_sizes(*a)) return 0;
     return prompt_bytes(*a, prompt_split(*a, hip_device).splits);
@@ -441,10 +539,7 @@ extern "C" df11_status df11_attend_prompt(const df11_attend_prompt_args *a, int 
     p.heads = a->n_heads;
     p.kv_heads = a->n_kv_heads;
     p.group = a->n_heads / a->n_kv_heads;
-    // (with 2^shift < group <= 2^(shift + 1) and the multiplier rounded up from
-    // 2^(32 + shift) / group, the quotient is exact for x < 2^31)
-    p.group_shift = p.group > 1 ? 31 - (uint32_t)__builtin_clz(p.group - 1) : 0;
-    p.group_magic = p.group > 1 ? (uint32_t)((((uint64_t)1 << (32 + p.group_shift)) + p.group - 1) / p.group) : 0;
+    divide_by(p.group, &p.group_magic, &p.group_shift);
     p.causal = a->flags & DF11_ATTEND_CAUSAL;
     p.tile_slots = (uint32_t)prompt_tile_slots(*a);
     p.splits = splits;

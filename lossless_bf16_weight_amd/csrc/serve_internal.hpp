@@ -87,6 +87,22 @@ struct PromptArgs {
     float *part, *part_ml;     // [split][workgroup][wave][register / 4][lane][4], then [split][workgroup][wave][row][2]
 };
 
+struct ChunkArgs {
+    CacheView c;
+    Tables t;
+    Rows q, out;
+    const int32_t *q_starts, *lens;
+    float log2_scale;
+    uint32_t n_seqs, n_q, group, causal;
+    uint32_t window, sinks;              // window 0: none
+    uint32_t group_magic, group_shift;   // as in PromptArgs
+    uint32_t most_steps;                 // of a tile with the window, whatever the length
+    uint32_t tile_slots;                 // at least as many as tiles
+    uint32_t places, least_shift;        // parts of a kv head's tiles that the workspace holds (0: none are split); log2 of the least steps of one
+    float by_places;                     // 1 / places
+    float *part, *part_ml;               // [place][kv_head][wave][register / 4][lane][4], then [place][kv_head][wave][row][2]
+};
+
 constexpr uint32_t kWriteChunks = 512;   // 16-byte chunks of rows that a workgroup of kv_write takes
 constexpr uint32_t kReadTile = 16;       // tokens of a tile that kv_read reads back
 constexpr uint32_t kReadSlice = 256;     // 16-byte chunks of its rows that a wave takes
@@ -101,5 +117,7 @@ hipError_t launch_kv_read(const ReadArgs &a, uint32_t head_dim, bool int8, hipSt
 hipError_t launch_heads(const HeadsArgs &a, uint32_t head_dim, int store, bool neighbours, hipStream_t stream);
 hipError_t launch_attend_token(const TokenArgs &a, uint32_t head_dim, bool int8, hipStream_t stream);
 hipError_t launch_attend_prompt(const PromptArgs &a, uint32_t head_dim, hipStream_t stream);
+
+hipError_t launch_attend_chunk(const ChunkArgs &a, uint32_t head_dim, bool int8, hipStream_t stream);
 
 }  // namespace df11
