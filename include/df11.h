@@ -533,6 +533,16 @@ typedef struct {
 uint64_t df11_attend_token_workspace(const df11_attend_token_args *args, int hip_device);
 df11_status df11_attend_token(const df11_attend_token_args *args, int hip_device, hipStream_t stream);
 
+/* df11_attend_token with a sliding window: of sequence s the last `window`
+ * positions below lens[s] are seen, and its first `sinks`.  window 0:
+ * df11_attend_token.  The split goes by the window and the sinks. */
+typedef struct {
+    df11_attend_token_args token;
+    uint32_t window, sinks;
+} df11_attend_token_window_args;
+uint64_t df11_attend_token_window_workspace(const df11_attend_token_window_args *args, int hip_device);
+df11_status df11_attend_token_window(const df11_attend_token_window_args *args, int hip_device, hipStream_t stream);
+
 #define DF11_ATTEND_CAUSAL 1u
 
 /* Attention of packed sequences: the queries of sequence s are rows

@@ -65,6 +65,7 @@ EXPORTS = [
     "df11_nf12_bound", "df11_nf12_encode", "df11_nf12_validate", "df11_nf12_decode",
     "df11_nf12_decode_batch",
     "df11_kv_write", "df11_kv_append", "df11_rotate_heads", "df11_kv_read", "df11_attend_token_workspace", "df11_attend_token",
+    "df11_attend_token_window_workspace", "df11_attend_token_window",
     "df11_attend_prompt_workspace", "df11_attend_prompt", "df11_attend_chunk_workspace", "df11_attend_chunk",
 ]
 
@@ -137,11 +138,11 @@ def lib():
                                          ctypes.c_int, ctypes.c_int, vp]
     L.df11_nf12_decode_batch.restype = ctypes.c_int
     # (the serving calls take one argument struct: _serve.py packs its bytes)
-    for name in ("df11_kv_write", "df11_kv_append", "df11_rotate_heads", "df11_kv_read", "df11_attend_token", "df11_attend_prompt",
-                 "df11_attend_chunk"):
+    for name in ("df11_kv_write", "df11_kv_append", "df11_rotate_heads", "df11_kv_read", "df11_attend_token", "df11_attend_token_window",
+                 "df11_attend_prompt", "df11_attend_chunk"):
         getattr(L, name).argtypes = [ctypes.c_char_p, ctypes.c_int, vp]
         getattr(L, name).restype = ctypes.c_int
-    for name in ("df11_attend_token_workspace", "df11_attend_prompt_workspace", "df11_attend_chunk_workspace"):
+    for name in ("df11_attend_token_workspace", "df11_attend_token_window_workspace", "df11_attend_prompt_workspace", "df11_attend_chunk_workspace"):
         getattr(L, name).argtypes = [ctypes.c_char_p, ctypes.c_int]
         getattr(L, name).restype = u64
     _lib = L

@@ -34,6 +34,7 @@ _HEADS = struct.Struct("<" + _ROTATION + 4 * _ROWS + "QQQIIIf")
 _APPEND = struct.Struct("<" + _CACHE + _ROTATION + 5 * _ROWS + "QQQQIf")
 _READ = struct.Struct("<" + _CACHE + _TABLE + 2 * _ROWS + "QQII")
 _TOKEN = struct.Struct("<" + _CACHE + _TABLE + 2 * _ROWS + "QQQIIfI")
+_TOKEN_WINDOW = struct.Struct(_TOKEN.format + "II")
 _PROMPT = struct.Struct("<" + 4 * _ROWS + "QQQQQQIIIIIf")
 
 _CHUNK = struct.Struct("<" + _CACHE + _TABLE + 2 * _ROWS + "QQQQQIIIIIf")
@@ -283,19 +284,21 @@ def kv_read(cache: KVCache, pages: torch.Tensor, starts: torch.Tensor, k_out: to
 
 
 @lru_cache(maxsize=4096)
-def token_workspace(n_seqs: int, n_heads: int, n_kv_heads: int, head_dim: int, page_size: int, entries: int, device: int = 0) -> int:
+def token_workspace(n_seqs: int, n_heads: int, n_kv_heads: int, head_dim: int, page_size: int, entries: int, device: int = 0,
+                    window: int = 0, sinks: int = 0) -> int:
     """Bytes of workspace that attend_token needs for these sizes (`entries`:
     the page table's width)."""
-    args = _TOKEN.pack(0, 0, 0, 0, 1, page_size, n_kv_heads, head_dim, 0, 0, 0, 0, entries, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0,
-                       n_seqs, n_heads, 1.0, 0)
-    return lib().df11_attend_token_workspace(args, device)
+    args = _TOKEN_WINDOW.pack(0, 0, 0, 0, 1, page_size, n_kv_heads, head_dim, 0, 0, 0, 0, entries, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0,
+                              n_seqs, n_heads, 1.0, 0, *_window(window, sinks))
+    return lib().df11_attend_token_window_workspace(args, device)
 
 
 def attend_token(q: torch.Tensor, cache: KVCache, pages: torch.Tensor, lens: torch.Tensor, out: torch.Tensor, scale=None,
-                 workspace: Optional[torch.Tensor] = None, stream=None):
+                 workspace: Optional[torch.Tensor] = None, stream=None, window: int = 0, sinks: int = 0):
     """Attention of one query row a sequence (q, out: [sequences, n_heads,
     head_dim] bfloat16) over the first lens[s] (int32) positions of its pages
-    (int32 [sequences, entries]).  scale: 1 / sqrt(head_dim) by default.
+    (int32 [sequences, entries]); with a window above 0 over the last `window`
+    of them and the first `sinks`.  scale: 1 / sqrt(head_dim) by default.
     workspace: at least token_workspace() bytes that no other call uses
     meanwhile; by default taken from torch's allocator."""
     dev, hk, d, c = _cache_fields(cache)
@@ -303,9 +306,15 @@ def attend_token(q: torch.Tensor, cache: KVCache, pages: torch.Tensor, lens: tor
     _, _, orow = _rows(out, "out", dev, d, n, h)
     t = _table(pages, dev, n)
     at = _index(lens, "lens", dev, I32, n)
+    if scale is None:
+        scale = d ** -0.5
+    if window or sinks:
+        window, sinks = _window(window, sinks)
+        p, size, keep = _workspace(token_workspace(n, h, hk, d, c[5], t[2], dev, window, sinks), workspace, dev, stream)
+        _launch(lib().df11_attend_token_window, _TOKEN_WINDOW.pack(*c, *t, *qr, *orow, at, p, size, n, h, scale, 0, window, sinks), dev, stream)
+        return
     p, size, keep = _workspace(token_workspace(n, h, hk, d, c[5], t[2], dev), workspace, dev, stream)
-    _launch(lib().df11_attend_token, _TOKEN.pack(*c, *t, *qr, *orow, at, p, size, n, h, d ** -0.5 if scale is None else scale, 0),
-            dev, stream)
+    _launch(lib().df11_attend_token, _TOKEN.pack(*c, *t, *qr, *orow, at, p, size, n, h, scale, 0), dev, stream)
 
 
 @lru_cache(maxsize=4096)

@@ -340,7 +340,8 @@ __global__ __launch_bounds__(kThreads, 2) void attend_chunk_kernel(ChunkArgs a) 
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const uint32_t key = key0 + 32 * t + 8 * (i / 4) + 4 * half + i % 4;
-                    if (key >= seen.end || (key < seen.begin && key >= a.sinks)) s[t][i] = -__builtin_inff();
+                    const bool hidden = (key >= seen.end) | ((key < seen.begin) & (key >= a.sinks));     // (without branches)
+                    s[t][i] = hidden ? -__builtin_inff() : s[t][i];
                 }
         }
         float top = -__builtin_inff();

@@ -58,8 +58,29 @@ __device__ __forceinline__ uint32_t v_at(uint32_t row, uint32_t chunk) {
     return row * kRowBytes + ((chunk ^ x) << 4);
 }
 
+// What a window and its sinks leave of a sequence of `len` keys: those before
+// `end` keys, without the ones in [hidden, shown).  Keys are counted in halves of
+// a step, 16 of them, with those left out that hold no key which is seen: key v
+// counted so is key v of the sequence, or from the window's first half on
+// v + skipped.
+struct Visible {
+    uint32_t end, hidden, shown, window, skipped;
+};
+
+__device__ __forceinline__ Visible visible_of(const TokenArgs &a, uint32_t len) {
+    const uint32_t first = len > a.window ? len - a.window : 0;
+    Visible v;
+    v.window = min((a.sinks + 15) >> 4, first >> 4) << 4;
+    v.skipped = (first & ~15u) - v.window;
+    v.end = len - v.skipped;
+    v.shown = first - v.skipped;
+    v.hidden = min(a.sinks, v.shown);
+    return v;
+}
+
 // kOnce: no other workgroup reads the same rows (at most 16 heads share a kv head).
-template <int D, bool kInt8, uint32_t kWaves, bool kOnce>
+// kWindow: the keys of a window and its sinks.
+template <int D, bool kInt8, uint32_t kWaves, bool kOnce, bool kWindow>
 __global__ __launch_bounds__(64 * kWaves, 3) void attend_token_kernel(TokenArgs a) {
     constexpr uint32_t kThreads = 64 * kWaves;
     constexpr int kRow = kInt8 ? D : 2 * D;            // bytes of a stored row
@@ -84,16 +105,32 @@ __global__ __launch_bounds__(64 * kWaves, 3) void attend_token_kernel(TokenArgs 
     const uint32_t kv_head = unit % a.c.kv_heads, seq = unit / a.c.kv_heads;
     const uint32_t split = blockIdx.z * gridDim.y + blockIdx.y;     // (past the last: begins past every length)
 
-    const uint32_t len = (uint32_t)min((int64_t)max(a.lens[seq], 0), (int64_t)a.t.width << a.c.shift);
+    uint32_t len = (uint32_t)min((int64_t)max(a.lens[seq], 0), (int64_t)a.t.width << a.c.shift);
+    Visible seen;
+    if (kWindow) {
+        seen = visible_of(a, len);
+        len = seen.end;
+    }
     const uint32_t begin = split * a.range;
     if (begin >= len && split) return;
     const uint32_t n = min(len - begin, a.range);      // this workgroup's keys
 
     // the first row of this head in each page of the range (the host keeps the
     // number of rows below 2^32)
-    const int32_t *const pages = a.t.pages + seq * a.t.stride + (begin >> a.c.shift);
-    for (uint32_t i = threadIdx.x; i < ((n + (1u << a.c.shift) - 1) >> a.c.shift); i += kThreads)
-        table[i] = (min((uint32_t)pages[i], a.c.n_pages - 1) * a.c.kv_heads + kv_head) << a.c.shift;
+    // (with a window: of each half of 16 keys)
+    if (kWindow) {
+        const int32_t *const pages = a.t.pages + seq * a.t.stride;
+        for (uint32_t i = threadIdx.x; i < (n + 15) >> 4; i += kThreads) {
+            const uint32_t at = begin + 16 * i, key = at + (at < seen.window ? 0 : seen.skipped);
+            table[i] = ((min((uint32_t)pages[key >> a.c.shift], a.c.n_pages - 1) * a.c.kv_heads + kv_head) << a.c.shift) + (key & ((1u << a.c.shift) - 1));
+        }
+    } else {
+        const int32_t *const pages = a.t.pages + seq * a.t.stride + (begin >> a.c.shift);
+        for (uint32_t i = threadIdx.x; i < ((n + (1u << a.c.shift) - 1) >> a.c.shift); i += kThreads)
+            table[i] = (min((uint32_t)pages[i], a.c.n_pages - 1) * a.c.kv_heads + kv_head) << a.c.shift;
+    }
+    // the keys of this workgroup that are not seen
+    const uint32_t hidden = kWindow ? max(seen.hidden, begin) - begin : 0, shown = kWindow ? max(seen.shown, begin) - begin : 0;
 
     // queries: columns past the group are zero
     const uint32_t in_group = q_tile * 16 + col;
@@ -132,7 +169,7 @@ __global__ __launch_bounds__(64 * kWaves, 3) void attend_token_kernel(TokenArgs 
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             const uint32_t key = min(key0 + 16 * t, last_half);
-            half_row[t] = __builtin_amdgcn_readfirstlane(table[key >> a.c.shift] + (key & in_page));
+            half_row[t] = __builtin_amdgcn_readfirstlane(kWindow ? table[key >> 4] : table[key >> a.c.shift] + (key & in_page));
         }
     };
     const auto load = [&](const uint8_t *pages, u32x4 *w) {
@@ -194,11 +231,15 @@ __global__ __launch_bounds__(64 * kWaves, 3) void attend_token_kernel(TokenArgs 
                 }
             }
         }
-        if (key0 + kTokenKeys > n) {
+        const bool masked = key0 + kTokenKeys > n || (kWindow && key0 < shown && key0 + kTokenKeys > hidden);
+        // (without branches: where the second condition was one, the compiler
+        // left the first score of a lane unmasked)
+        const auto out_of_sight = [&](uint32_t key) { return kWindow ? (key >= n) | ((key >= hidden) & (key < shown)) : key >= n; };
+        if (masked) {
             // weights of rows past the end are 0, and 0 times an infinity would be NaN
 #pragma unroll
             for (int i = 0; i < kLoads; ++i)
-                if (key0 + (i * 64 + lane) / kChunks >= n) vw[i] = u32x4{0, 0, 0, 0};
+                if (out_of_sight(key0 + (i * 64 + lane) / kChunks)) vw[i] = u32x4{0, 0, 0, 0};
         }
         handed_over();
 #pragma unroll
@@ -218,12 +259,12 @@ __global__ __launch_bounds__(64 * kWaves, 3) void attend_token_kernel(TokenArgs 
             load_scales();
         }
         const float scale = kInt8 ? 1.0f : a.log2_scale;
-        if (key0 + kTokenKeys > n) {
+        if (masked) {
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (key0 + 16 * t + 4 * grp + i >= n) {
+                    if (out_of_sight(key0 + 16 * t + 4 * grp + i)) {
                         s[t][i] = -__builtin_inff();
                         if (kInt8) v_scale[t][i] = 0;
                     }
@@ -340,13 +381,14 @@ __global__ __launch_bounds__(64 * kWaves, 3) void attend_token_kernel(TokenArgs 
 
 // Joins the parts of one query head: out = sum_a w_a o_a / sum_a w_a l_a with
 // w_a = 2^(m_a - max m).
-template <int D>
+template <int D, bool kWindow>
 __global__ __launch_bounds__(256) void join_token_kernel(TokenArgs a) {
     __shared__ float sums[4][D];
     __shared__ float ls[4];
     const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t seq = blockIdx.x / a.heads, h = blockIdx.x % a.heads;
-    const uint32_t len = (uint32_t)min((int64_t)max(a.lens[seq], 0), (int64_t)a.t.width << a.c.shift);
+    uint32_t len = (uint32_t)min((int64_t)max(a.lens[seq], 0), (int64_t)a.t.width << a.c.shift);
+    if (kWindow) len = visible_of(a, len).end;
     const uint32_t n = max(1u, (len + a.range - 1) / a.range);     // parts that were written
     const uint64_t first = (uint64_t)blockIdx.x * a.splits;
     const f32x2 *const ml = reinterpret_cast<const f32x2 *>(a.part_ml) + first;
@@ -377,17 +419,28 @@ __global__ __launch_bounds__(256) void join_token_kernel(TokenArgs a) {
     }
 }
 
-template <uint32_t kWaves, bool kOnce>
+template <uint32_t kWaves, bool kOnce, bool kWindow>
 void launch_as(const TokenArgs &a, uint32_t head_dim, bool int8, dim3 grid, hipStream_t stream) {
-    const auto kernel = head_dim == 64 ? (int8 ? attend_token_kernel<64, true, kWaves, kOnce> : attend_token_kernel<64, false, kWaves, kOnce>)
-                                       : (int8 ? attend_token_kernel<128, true, kWaves, kOnce> : attend_token_kernel<128, false, kWaves, kOnce>);
+    const auto kernel = head_dim == 64 ? (int8 ? attend_token_kernel<64, true, kWaves, kOnce, kWindow> : attend_token_kernel<64, false, kWaves, kOnce, kWindow>)
+                                       : (int8 ? attend_token_kernel<128, true, kWaves, kOnce, kWindow> : attend_token_kernel<128, false, kWaves, kOnce, kWindow>);
     hipLaunchKernelGGL(kernel, grid, dim3(64 * kWaves), 0, stream, a);
 }
 
-template <uint32_t kWaves>
+template <uint32_t kWaves, bool kWindow>
 void launch(const TokenArgs &a, uint32_t head_dim, bool int8, dim3 grid, hipStream_t stream) {
-    if (a.q_tiles == 1) launch_as<kWaves, true>(a, head_dim, int8, grid, stream);
-    else launch_as<kWaves, false>(a, head_dim, int8, grid, stream);
+    if (a.q_tiles == 1) launch_as<kWaves, true, kWindow>(a, head_dim, int8, grid, stream);
+    else launch_as<kWaves, false, kWindow>(a, head_dim, int8, grid, stream);
+}
+
+template <bool kWindow>
+hipError_t launch_all(const TokenArgs &a, uint32_t head_dim, bool int8, dim3 grid, hipStream_t stream) {
+    if (a.whole) launch<12, kWindow>(a, head_dim, int8, grid, stream);
+    else launch<4, kWindow>(a, head_dim, int8, grid, stream);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.splits == 1) return e;
+    hipLaunchKernelGGL((head_dim == 64 ? join_token_kernel<64, kWindow> : join_token_kernel<128, kWindow>), dim3(a.n_seqs * a.heads), dim3(256), 0,
+                       stream, a);
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -397,13 +450,7 @@ hipError_t launch_attend_token(const TokenArgs &a, uint32_t head_dim, bool int8,
     const uint32_t parts = a.splits < 65535 ? a.splits : 65535;
     const dim3 grid(a.q_tiles == 1 ? a.n_seqs * a.c.kv_heads : (a.n_seqs * a.c.kv_heads + 7) / 8 * 8 * a.q_tiles, parts,
                     (a.splits + parts - 1) / parts);
-    if (a.whole) launch<12>(a, head_dim, int8, grid, stream);
-    else launch<4>(a, head_dim, int8, grid, stream);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || a.splits == 1) return e;
-    hipLaunchKernelGGL(head_dim == 64 ? join_token_kernel<64> : join_token_kernel<128>, dim3(a.n_seqs * a.heads), dim3(256), 0,
-                       stream, a);
-    return hipGetLastError();
+    return a.window ? launch_all<true>(a, head_dim, int8, grid, stream) : launch_all<false>(a, head_dim, int8, grid, stream);
 }
 
 }  // namespace df11

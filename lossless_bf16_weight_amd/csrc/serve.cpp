@@ -186,12 +186,24 @@ struct TokenSplit {
     uint32_t q_tiles, range, splits, whole;
 };
 
-TokenSplit token_split(const df11_attend_token_args &a, int dev) {
+// With a window the keys are those of its halves of 16 and the sinks', whose
+// ranges begin anywhere.
+struct Window {
+    uint32_t keys, sinks;       // keys 0: none
+};
+
+// (one as long as the table is none)
+Window window_of(uint32_t window, uint32_t sinks, uint64_t positions) {
+    return window < positions ? Window{window, window ? (uint32_t)std::min<uint64_t>(sinks, positions) : 0} : Window{0, 0};
+}
+
+TokenSplit token_split(const df11_attend_token_args &a, const Window &w, int dev) {
     TokenSplit s;
-    const uint64_t most = (uint64_t)a.table.width * a.cache.page_size;
+    uint64_t most = (uint64_t)a.table.width * a.cache.page_size;
+    if (w.keys) most = std::min<uint64_t>(most, (uint64_t)w.keys + 15 + ceil_div(w.sinks, 16) * 16);
     s.q_tiles = (uint32_t)ceil_div(a.n_heads / a.cache.n_kv_heads, 16);
     const uint64_t units = (uint64_t)a.n_seqs * a.cache.n_kv_heads * s.q_tiles;
-    const uint64_t step = std::max(kTokenKeys * 4, a.cache.page_size);
+    const uint64_t step = w.keys ? kTokenKeys * 4 : std::max(kTokenKeys * 4, a.cache.page_size);
     const uint64_t want = std::max<uint64_t>(1, 3 * compute_units(dev) / std::max<uint64_t>(units, 1));
     const uint64_t range = ceil_div(ceil_div(most, want), step) * step;
     const uint64_t longest = std::max<uint64_t>(kTokenRangeMax / step, 1) * step;   // (ranges begin with a page)
@@ -280,9 +292,8 @@ ChunkSplit chunk_split(const df11_attend_chunk_args &a, int dev) {
     const uint64_t group = a.n_heads / a.cache.n_kv_heads, positions = (uint64_t)a.table.width * a.cache.page_size;
     // (a tile's queries are (kPromptTile - 1) / group + 2 at most, the windows of n of
     // them w + n - 1 keys, which lie in so many steps)
-    if (a.window && a.window < positions)
-        s.most_steps = (uint32_t)((a.window + (kPromptTile - 1) / group + 1 + 2 * (kPromptKeys - 1)) / kPromptKeys +
-                                  ceil_div(std::min<uint64_t>(a.sinks, positions), kPromptKeys));
+    const Window w = window_of(a.window, a.sinks, positions);
+    if (w.keys) s.most_steps = (uint32_t)((w.keys + (kPromptTile - 1) / group + 1 + 2 * (kPromptKeys - 1)) / kPromptKeys + ceil_div(w.sinks, kPromptKeys));
     const uint64_t steps = std::min<uint64_t>(ceil_div(positions, kPromptKeys), s.most_steps);
     const uint64_t places = 2 * compute_units(dev) / a.cache.n_kv_heads, parts = steps >> s.least_shift;
     if (a.n_q == 0 || a.n_seqs == 0 || a.n_seqs > kChunkMostPlanned || places < 2 || parts < 2) return s;
@@ -419,13 +430,18 @@ extern "C" df11_status df11_kv_read(const df11_kv_read_args *a, int hip_device, 
     return launched(launch_kv_read(r, d, a->cache.store == DF11_KV_INT8, stream), "kv_read");
 }
 
-extern "C" uint64_t df11_attend_token_workspace(const df11_attend_token_args *a, int hip_device) {
+static uint64_t token_workspace(const df11_attend_token_args *a, uint32_t window, uint32_t sinks, int hip_device) {
     if (!a || a->n_seqs == 0 || check_token_sizes(*a) || a->table.width == 0) return 0;
-    return token_bytes(*a, token_split(*a, hip_device));
+    return token_bytes(*a, token_split(*a, window_of(window, sinks, (uint64_t)a->table.width * a->cache.page_size), hip_device));
 }
 
-extern "C" df11_status df11_attend_token(const df11_attend_token_args *a, int hip_device, hipStream_t stream) {
-    if (!a) return report_error(DF11_E_ARG, "attend_token: NULL arguments");
+extern "C" uint64_t df11_attend_token_workspace(const df11_attend_token_args *a, int hip_device) { return token_workspace(a, 0, 0, hip_device); }
+
+extern "C" uint64_t df11_attend_token_window_workspace(const df11_attend_token_window_args *a, int hip_device) {
+    return a ? token_workspace(&a->token, a->window, a->sinks, hip_device) : 0;
+}
+
+static df11_status attend_token(const df11_attend_token_args *a, uint32_t window, uint32_t sinks, int hip_device, hipStream_t stream) {
     TRY(check_token_sizes(*a));
     TRY(check_cache(a->cache));
     TRY(check_scale(a->scale));
@@ -435,7 +451,8 @@ extern "C" df11_status df11_attend_token(const df11_attend_token_args *a, int hi
     if (a->n_seqs == 0) return DF11_OK;
     TRY(check_table(a->table, a->cache));
     if (bad_index(a->lens, 4)) return report_error(DF11_E_ARG, "attend_token: lens NULL or misaligned");
-    const TokenSplit s = token_split(*a, hip_device);
+    const Window w = window_of(window, sinks, (uint64_t)a->table.width * a->cache.page_size);
+    const TokenSplit s = token_split(*a, w, hip_device);
     TRY(check_workspace(a->workspace, a->workspace_bytes, token_bytes(*a, s)));
     ON_DEVICE(hip_device);
     TokenArgs t{};
@@ -452,9 +469,19 @@ extern "C" df11_status df11_attend_token(const df11_attend_token_args *a, int hi
     t.range = s.range;
     t.splits = s.splits;
     t.whole = s.whole;
+    t.window = w.keys;
+    t.sinks = w.sinks;
     t.part = (float *)a->workspace;
     t.part_ml = t.part + (uint64_t)a->n_seqs * a->n_heads * s.splits * d;
     return launched(launch_attend_token(t, d, a->cache.store == DF11_KV_INT8, stream), "attend_token");
+}
+
+extern "C" df11_status df11_attend_token(const df11_attend_token_args *a, int hip_device, hipStream_t stream) {
+    return a ? attend_token(a, 0, 0, hip_device, stream) : report_error(DF11_E_ARG, "attend_token: NULL arguments");
+}
+
+extern "C" df11_status df11_attend_token_window(const df11_attend_token_window_args *a, int hip_device, hipStream_t stream) {
+    return a ? attend_token(&a->token, a->window, a->sinks, hip_device, stream) : report_error(DF11_E_ARG, "attend_token_window: NULL arguments");
 }
 
 extern "C" uint64_t df11_attend_chunk_workspace(const df11_attend_chunk_args *a, int hip_device) {
@@ -488,10 +515,9 @@ extern "C" df11_status df11_attend_chunk(const df11_attend_chunk_args *a, int hi
     c.n_q = (uint32_t)a->n_q;
     c.group = a->n_heads / kv;
     c.causal = a->flags & DF11_ATTEND_CAUSAL;
-    // (a window as long as the table is none)
-    const uint32_t positions = a->table.width * a->cache.page_size;
-    c.window = a->window < positions ? a->window : 0;
-    c.sinks = c.window ? std::min(a->sinks, positions) : 0;
+    const Window w = window_of(a->window, a->sinks, (uint64_t)a->table.width * a->cache.page_size);
+    c.window = w.keys;
+    c.sinks = w.sinks;
     divide_by(c.group, &c.group_magic, &c.group_shift);
     c.most_steps = s.most_steps;
     c.tile_slots = (uint32_t)chunk_tile_slots(*a);

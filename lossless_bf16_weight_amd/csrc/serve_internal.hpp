@@ -72,6 +72,7 @@ struct TokenArgs {
     uint32_t n_seqs, heads, group, q_tiles;   // group = heads / kv_heads, in q_tiles tiles of 16
     uint32_t range, splits;    // keys a workgroup takes, workgroups along a sequence
     uint32_t whole;            // twelve waves a workgroup instead of four
+    uint32_t window, sinks;    // window 0: none
     float *part;               // [seq][head][split][head_dim] unnormalised, then [..][2] maximum and sum
     float *part_ml;
 };
