@@ -216,14 +216,15 @@ __global__ __launch_bounds__(kThreads, 2) void attend_chunk_kernel(ChunkArgs a) 
     const auto read_entries = [&](uint32_t key0) {
         entries_from = key0 >> a.c.shift;
         const uint32_t at = min(entries_from + lane, (n_k - 1) >> a.c.shift);
-        entries = min((uint32_t)a.t.pages[p.seq * a.t.stride + at], a.c.n_pages - 1);
+        entries = (uint32_t)a.t.pages[p.seq * a.t.stride + at];
     };
     const auto need_entries = [&](uint32_t key0) {
         if (key0 >> a.c.shift < entries_from || (key0 + kPromptKeys - 1) >> a.c.shift > entries_from + 63) read_entries(key0);
     };
     // The cache's row of 16 keys' first (the host keeps their number below 2^32).
     const auto row_of = [&](uint32_t key) {
-        return ((of_lane(entries, (key >> a.c.shift) - entries_from) * a.c.kv_heads + kv_head) << a.c.shift) + (key & ((1u << a.c.shift) - 1));
+        const uint32_t page = min(of_lane(entries, (key >> a.c.shift) - entries_from), a.c.n_pages - 1);
+        return ((page * a.c.kv_heads + kv_head) << a.c.shift) + (key & ((1u << a.c.shift) - 1));
     };
 
     // Words: a step's K and V rows go from memory into LDS without passing
@@ -252,36 +253,31 @@ __global__ __launch_bounds__(kThreads, 2) void attend_chunk_kernel(ChunkArgs a) 
     };
 
     // 8 bits: codes go through registers, one step ahead, and become words on
-    // their way into LDS; scales beside them, K's of 64 rows and then V's.
+    // their way into LDS; scales beside them, K's of 64 rows and then V's.  Rows
+    // past the sequence's end are what the last page holds: codes are finite, and
+    // masked scores and weights of 0 do not look at the scales.
     constexpr uint32_t kCodeChunks = D / 16, kCodeRows = kThreads / kCodeChunks;
     const uint32_t code_row = threadIdx.x / kCodeChunks, code_chunk = threadIdx.x % kCodeChunks;
     u32x4 kw[kCodeLoads], vw[kCodeLoads];
-    float scale_w = 0;
+    float scale_w;
     const auto load_codes = [&](uint32_t key0) {
-        const uint32_t left = n_k - key0;
 #pragma unroll
         for (int i = 0; i < kCodeLoads; ++i) {
             // (a wave's rows: 8 or 16 neighbours)
             const uint32_t first = key0 + i * kCodeRows + wave * (64 / kCodeChunks);
             const uint64_t at = ((uint64_t)row_of(first & ~15u) + (first & 15)) * D;
             const uint32_t from = (lane / kCodeChunks) * D + 16 * code_chunk;
-            kw[i] = vw[i] = u32x4{0, 0, 0, 0};
-            if (code_row + i * kCodeRows < left) {
-                kw[i] = *reinterpret_cast<const u32x4 *>(a.c.k + at + from);
-                vw[i] = *reinterpret_cast<const u32x4 *>(a.c.v + at + from);
-            }
+            kw[i] = *reinterpret_cast<const u32x4 *>(a.c.k + at + from);
+            vw[i] = *reinterpret_cast<const u32x4 *>(a.c.v + at + from);
         }
-        scale_w = 0;
-        if (wave < 2) {
-            // (16 lanes share a page's row)
-            uint32_t r = row_of(key0);
+        // (16 lanes share a page's row; waves 2 and 3 repeat 0 and 1)
+        uint32_t r = row_of(key0);
 #pragma unroll
-            for (int g = 1; g < 4; ++g) {
-                const uint32_t other = row_of(key0 + 16 * g);
-                if ((int)(lane >> 4) == g) r = other;
-            }
-            if (lane < left) scale_w = (wave ? a.c.v_scale : a.c.k_scale)[(uint64_t)r + (lane & 15)];
+        for (int g = 1; g < 4; ++g) {
+            const uint32_t other = row_of(key0 + 16 * g);
+            r = (int)(lane >> 4) == g ? other : r;
         }
+        scale_w = (wave & 1 ? a.c.v_scale : a.c.k_scale)[r + (lane & 15)];
     };
     const auto store_codes = [&](uint8_t *kt, uint8_t *vt, float *sc) {
 #pragma unroll
@@ -292,7 +288,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_chunk_kernel(ChunkArgs a) 
             *reinterpret_cast<u32x4 *>(vt + v_at<D>(r, 2 * code_chunk)) = bf16_of_bytes8(u32x2{vw[i].x, vw[i].y});
             *reinterpret_cast<u32x4 *>(vt + v_at<D>(r, 2 * code_chunk + 1)) = bf16_of_bytes8(u32x2{vw[i].z, vw[i].w});
         }
-        if (wave < 2) sc[threadIdx.x] = scale_w;
+        if (wave < 2) sc[threadIdx.x] = scale_w;     // (K's from wave 0, V's from wave 1)
     };
 
     // One step's keys.  kCareful: values that are infinite or NaN at keys which
@@ -443,6 +439,9 @@ __global__ __launch_bounds__(kThreads, 2) void attend_chunk_kernel(ChunkArgs a) 
             step(std::false_type{}, steps.key(i), kt, vt, sc);
             if (more) store_codes(kt_next, vt_next, sc_next);
         };
+        // (the queries are here too: said outside the loop, so that its products
+        // do not wait for what is loaded in it)
+        __builtin_amdgcn_s_waitcnt(0x0F70);
         for (uint32_t i = step_begin; i < step_end; i += 2) {
             go(i, kt0, vt0, sc0, kt1, vt1, sc1);
             if (i + 1 < step_end) go(i + 1, kt1, vt1, sc1, kt0, vt0, sc0);
