@@ -72,9 +72,8 @@ __device__ __forceinline__ bool find_piece(const ChunkArgs &a, uint32_t item, Pi
         }
 #pragma unroll
         for (int d = 1; d < 64; d *= 2) total += __shfl_xor(total, d);
-        // (above the quotient, whatever the sum's rounding: the parts of all
-        // split tiles are then no more than the places)
-        quota = (uint32_t)fminf(total * a.by_places * (1.0f + 0x1p-18f), 4.0e9f) + 1;
+        // (above the quotient, whatever the sum's rounding: see chunk_split)
+        quota = (uint32_t)fminf(total * a.by_parts * (1.0f + 0x1p-18f), 4.0e9f) + 1;
     } else if (a.n_seqs > 64) {
         uint32_t tile;
         const uint32_t s = sequence_of_slot(a.q_starts, a.n_seqs, item, a.group, 7, &tile);
@@ -90,14 +89,21 @@ __device__ __forceinline__ bool find_piece(const ChunkArgs &a, uint32_t item, Pi
     uint32_t items_before = 0, places_before = 0;
     for (uint32_t s0 = 0; s0 < a.n_seqs; s0 += 64) {
         if (!kSplit || a.n_seqs > 64 || s0 == 0) look(s0);
-        const uint32_t parts = kSplit ? max(1u, min(steps / quota, steps >> a.least_shift)) : 1;
+        const uint32_t parts = kSplit ? max(1u, min((steps + quota / 2) / quota, steps >> a.least_shift)) : 1;
         const uint32_t places = parts > 1 ? tiles * parts : 0, items = kJoin ? (parts > 1 ? tiles : 0) : tiles * parts;
         uint32_t items_to = items, places_to = places;     // sums up to this lane
         for (uint32_t d = 1; d < min(a.n_seqs, 64u); d *= 2) {
             const uint32_t x = __shfl_up(items_to, d), y = kSplit ? __shfl_up(places_to, d) : 0;
             if (lane >= d) items_to += x, places_to += y;
         }
-        const uint32_t before = items_before + items_to - items;
+        uint32_t before = items_before + items_to - items;
+        if (kSplit && !kJoin && a.n_seqs <= 64) {
+            // the sequences with the longest parts first: one of them at the end
+            // would keep the others' compute units waiting
+            const uint32_t rank = (steps + parts - 1) / parts << 6 | lane;
+            before = 0;
+            for (uint32_t j = 0; j < a.n_seqs; ++j) before += of_lane(rank, j) > rank ? of_lane(items, j) : 0;
+        }
         const uint64_t found = __ballot(item >= before && item - before < items);
         if (found) {
             const uint32_t x = (uint32_t)__builtin_ctzll(found);

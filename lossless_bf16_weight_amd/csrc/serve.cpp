@@ -276,11 +276,15 @@ df11_status check_prompt_sizes(const df11_attend_prompt_args &a) {
 }
 
 // What attend_chunk's workgroups need for dividing a call's work, whose lengths
-// the host does not know: the places of parts, two workgroups for each compute
-// unit, and the least steps of a part.  Sequences of many are taken whole: each
-// workgroup would read all their lengths.
+// the host does not know: the parts of equal size that it would be (a quarter
+// more than the workgroups that run at a time, two for each compute unit, for
+// parts are not equal), and the least steps of one.  A tile's steps over the
+// quota, rounded, are its parts: two from one and a half on, so that all split
+// tiles have at most four thirds of the parts asked for, and so many places the
+// workspace has.  Sequences of many are taken whole: each workgroup would read
+// all their lengths.
 struct ChunkSplit {
-    uint32_t most_steps, places, least_shift;
+    uint32_t most_steps, parts, places, least_shift;
 };
 
 constexpr uint32_t kChunkMostPlanned = 512;     // sequences
@@ -288,16 +292,17 @@ constexpr uint32_t kChunkMostPlanned = 512;     // sequences
 uint64_t chunk_tile_slots(const df11_attend_chunk_args &a) { return a.n_q * (a.n_heads / a.cache.n_kv_heads) / kPromptTile + a.n_seqs; }
 
 ChunkSplit chunk_split(const df11_attend_chunk_args &a, int dev) {
-    ChunkSplit s{~0u, 0, 2};
+    ChunkSplit s{~0u, 0, 0, 2};
     const uint64_t group = a.n_heads / a.cache.n_kv_heads, positions = (uint64_t)a.table.width * a.cache.page_size;
     // (a tile's queries are (kPromptTile - 1) / group + 2 at most, the windows of n of
     // them w + n - 1 keys, which lie in so many steps)
     const Window w = window_of(a.window, a.sinks, positions);
     if (w.keys) s.most_steps = (uint32_t)((w.keys + (kPromptTile - 1) / group + 1 + 2 * (kPromptKeys - 1)) / kPromptKeys + ceil_div(w.sinks, kPromptKeys));
     const uint64_t steps = std::min<uint64_t>(ceil_div(positions, kPromptKeys), s.most_steps);
-    const uint64_t places = 2 * compute_units(dev) / a.cache.n_kv_heads, parts = steps >> s.least_shift;
-    if (a.n_q == 0 || a.n_seqs == 0 || a.n_seqs > kChunkMostPlanned || places < 2 || parts < 2) return s;
-    s.places = (uint32_t)std::min(places, chunk_tile_slots(a) * parts);
+    const uint64_t parts = 5 * compute_units(dev) / 2 / a.cache.n_kv_heads, of_tile = steps >> s.least_shift;
+    if (a.n_q == 0 || a.n_seqs == 0 || a.n_seqs > kChunkMostPlanned || parts < 2 || of_tile < 2) return s;
+    s.parts = (uint32_t)parts;
+    s.places = (uint32_t)std::min(4 * parts / 3, chunk_tile_slots(a) * of_tile);
     return s;
 }
 
@@ -311,7 +316,7 @@ df11_status check_chunk_sizes(const df11_attend_chunk_args &a) {
     const uint32_t kv = a.cache.n_kv_heads;
     if (a.n_heads == 0 || a.n_heads % kv) return report_error(DF11_E_ARG, "%u heads over %u kv heads", a.n_heads, kv);
     if (a.n_q > 0x7FFFFFFFu || a.n_q * (a.n_heads / kv) > 0x7FFFFFFFu || a.n_seqs > kMostGroups ||
-        chunk_tile_slots(a) * kv > kMostGroups - 2048)     // (and two places a compute unit)
+        chunk_tile_slots(a) * kv > kMostGroups - 2048)     // (and the places)
         return report_error(DF11_E_UNSUPPORTED, "%llu rows of %u heads in %u sequences", (unsigned long long)a.n_q, a.n_heads, a.n_seqs);
     if (a.flags & ~DF11_ATTEND_CAUSAL) return report_error(DF11_E_ARG, "attend_chunk: flags %u", a.flags);
     if (a.window && !(a.flags & DF11_ATTEND_CAUSAL)) return report_error(DF11_E_ARG, "attend_chunk: a window needs DF11_ATTEND_CAUSAL");
@@ -523,7 +528,7 @@ extern "C" df11_status df11_attend_chunk(const df11_attend_chunk_args *a, int hi
     c.tile_slots = (uint32_t)chunk_tile_slots(*a);
     c.places = s.places;
     c.least_shift = s.least_shift;
-    c.by_places = s.places ? 1.0f / s.places : 0;
+    c.by_parts = s.parts ? 1.0f / s.parts : 0;
     c.part = (float *)a->workspace;
     c.part_ml = c.part + (uint64_t)s.places * kv * kPromptTile * d;
     return launched(launch_attend_chunk(c, d, a->cache.store == DF11_KV_INT8, stream), "attend_chunk");

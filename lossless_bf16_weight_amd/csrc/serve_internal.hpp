@@ -100,7 +100,7 @@ struct ChunkArgs {
     uint32_t most_steps;                 // of a tile with the window, whatever the length
     uint32_t tile_slots;                 // at least as many as tiles
     uint32_t places, least_shift;        // parts of a kv head's tiles that the workspace holds (0: none are split); log2 of the least steps of one
-    float by_places;                     // 1 / places
+    float by_parts;                      // 1 / the parts that a kv head's work is divided into
     float *part, *part_ml;               // [place][kv_head][wave][register / 4][lane][4], then [place][kv_head][wave][row][2]
 };
 
