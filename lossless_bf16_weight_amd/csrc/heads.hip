@@ -25,7 +25,6 @@ namespace df11 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 3;      // rows of a lane in flight
 
 __device__ __forceinline__ float low(uint32_t w) { return __builtin_bit_cast(float, w << 16); }
 __device__ __forceinline__ float high(uint32_t w) { return __builtin_bit_cast(float, w & 0xFFFF0000u); }
@@ -48,7 +47,7 @@ __device__ __forceinline__ float row_sum(float x) {
 }
 
 template <int D, int kStore, bool kNeighbours>
-__global__ __launch_bounds__(kThreads) void heads_kernel(HeadsArgs a) {
+__global__ __launch_bounds__(kThreads, 4) void heads_kernel(HeadsArgs a) {
     constexpr uint32_t kLanes = D / 16, kRows = 64 / kLanes;
     const uint32_t lane = threadIdx.x & 63u, l = lane % kLanes, in_step = lane / kLanes;
     const uint32_t item = blockIdx.x * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -99,16 +98,13 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(HeadsArgs a) {
     };
 
     bool begun = false;
-    for (uint32_t r0 = first; r0 < end; r0 += kBatch * kRows) {
-        u32x4 w[kBatch][2];
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const uint32_t r = r0 + i * kRows + in_step;
-            if (r < end) {
-                const uint16_t *const from = source(r);
-                w[i][0] = *reinterpret_cast<const u32x4 *>(from + at0);
-                w[i][1] = *reinterpret_cast<const u32x4 *>(from + at1);
-            }
+    for (uint32_t r0 = first; r0 < end; r0 += kRows) {
+        const uint32_t r = r0 + in_step;
+        u32x4 w[2];
+        if (r < end) {
+            const uint16_t *const from = source(r);
+            w[0] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(from + at0));
+            w[1] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(from + at1));
         }
         if (!begun) {
             begun = true;
@@ -120,83 +116,79 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(HeadsArgs a) {
             }
             angles();
         }
+        if (r >= end) continue;        // (a row's lanes go together)
+        const bool is_q = r < a.heads, is_v = r >= a.heads + a.kv_heads, is_k = !is_q && !is_v;
+        const uint32_t head = r - (is_q ? 0 : is_k ? a.heads : a.heads + a.kv_heads);
+        float y[16];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const uint32_t r = r0 + i * kRows + in_step;
-            if (r >= end) continue;        // (a row's lanes go together)
-            const bool is_q = r < a.heads, is_v = r >= a.heads + a.kv_heads, is_k = !is_q && !is_v;
-            const uint32_t head = r - (is_q ? 0 : is_k ? a.heads : a.heads + a.kv_heads);
-            float y[16];
+        for (int x = 0; x < 8; ++x) {
+            y[2 * x] = low(w[x / 4][x % 4]);
+            y[2 * x + 1] = high(w[x / 4][x % 4]);
+        }
+        if (is_q ? a.q_weight != nullptr : is_k && a.k_weight) {
+            float sum = 0;
+#pragma unroll
+            for (int x = 0; x < 16; ++x) sum = __builtin_fmaf(y[x], y[x], sum);
+            sum = row_sum<kLanes>(sum);
+            float eps = a.eps;
+            if (!(sum < __builtin_inff())) {
+                // squares that pass 32 bits (or an infinity): of values 2^-100 as
+                // large, and eps 2^-200 of itself
+                sum = 0, eps = 0;
+#pragma unroll
+                for (int x = 0; x < 16; ++x) {
+                    y[x] *= 0x1p-100f;
+                    sum = __builtin_fmaf(y[x], y[x], sum);
+                }
+                sum = row_sum<kLanes>(sum);
+            }
+            const float by = __builtin_amdgcn_rsqf(__builtin_fmaf(sum, 1.0f / D, eps));
 #pragma unroll
             for (int x = 0; x < 8; ++x) {
-                y[2 * x] = low(w[i][x / 4][x % 4]);
-                y[2 * x + 1] = high(w[i][x / 4][x % 4]);
+                const uint32_t two = is_q ? wq[x / 4][x % 4] : wk[x / 4][x % 4];
+                y[2 * x] *= by * low(two);
+                y[2 * x + 1] *= by * high(two);
             }
-            if (is_q ? a.q_weight != nullptr : is_k && a.k_weight) {
-                float sum = 0;
+        }
+        if (turned && !is_v) {
 #pragma unroll
-                for (int x = 0; x < 16; ++x) sum = __builtin_fmaf(y[x], y[x], sum);
-                sum = row_sum<kLanes>(sum);
-                float eps = a.eps;
-                if (!(sum < __builtin_inff())) {
-                    // squares that pass 32 bits (or an infinity): of values 2^-100 as
-                    // large, and eps 2^-200 of itself
-                    sum = 0, eps = 0;
-#pragma unroll
-                    for (int x = 0; x < 16; ++x) {
-                        y[x] *= 0x1p-100f;
-                        sum = __builtin_fmaf(y[x], y[x], sum);
-                    }
-                    sum = row_sum<kLanes>(sum);
-                }
-                const float by = __builtin_amdgcn_rsqf(__builtin_fmaf(sum, 1.0f / D, eps));
-#pragma unroll
-                for (int x = 0; x < 8; ++x) {
-                    const uint32_t two = is_q ? wq[x / 4][x % 4] : wk[x / 4][x % 4];
-                    y[2 * x] *= by * low(two);
-                    y[2 * x + 1] *= by * high(two);
-                }
+            for (int x = 0; x < 8; ++x) {
+                float &p = kNeighbours ? y[2 * x] : y[x], &q = kNeighbours ? y[2 * x + 1] : y[x + 8];
+                const float p0 = p, q0 = q;
+                p = __builtin_fmaf(p0, c[x], -(q0 * s[x]));
+                q = __builtin_fmaf(q0, c[x], p0 * s[x]);
             }
-            if (turned && !is_v) {
+        }
+        u32x4 out[2];
 #pragma unroll
-                for (int x = 0; x < 8; ++x) {
-                    float &p = kNeighbours ? y[2 * x] : y[x], &q = kNeighbours ? y[2 * x + 1] : y[x + 8];
-                    const float p0 = p, q0 = q;
-                    p = __builtin_fmaf(p0, c[x], -(q0 * s[x]));
-                    q = __builtin_fmaf(q0, c[x], p0 * s[x]);
-                }
+        for (int x = 0; x < 8; ++x) out[x / 4][x % 4] = is_v ? w[x / 4][x % 4] : pack_bf16(y[2 * x], y[2 * x + 1]);
+        const Rows &to = is_q ? a.q_out : a.k_out;
+        if (is_q || (is_k && a.k_out.data)) {
+            uint16_t *const row = to.data + token * to.row + head * to.head;
+            __builtin_nontemporal_store(out[0], reinterpret_cast<u32x4 *>(row + at0));
+            __builtin_nontemporal_store(out[1], reinterpret_cast<u32x4 *>(row + at1));
+        }
+        if (kStore == kHeadsOnly || is_q || slot < 0) continue;
+        const uint64_t row = ((((uint64_t)slot >> a.c.shift) * a.c.kv_heads + head) << a.c.shift) + (slot & ((1 << a.c.shift) - 1));
+        uint8_t *const store = is_v ? a.c.v : a.c.k;
+        if (kStore == kHeadsInt8) {
+            uint32_t m = 0x0D800000u;      // 2^-100
+#pragma unroll
+            for (int x = 0; x < 16; ++x) m = max(m, __float_as_uint(y[x]) & 0x7FFFFFFFu);
+            const float top = __uint_as_float(row_max<kLanes>(m)), inv = 127.0f / top;
+            uint32_t codes[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                codes[x] = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) codes[x] |= (uint32_t)((int)__builtin_rintf(y[4 * x + j] * inv) & 255) << (8 * j);
             }
-            u32x4 out[2];
-#pragma unroll
-            for (int x = 0; x < 8; ++x) out[x / 4][x % 4] = is_v ? w[i][x / 4][x % 4] : pack_bf16(y[2 * x], y[2 * x + 1]);
-            const Rows &to = is_q ? a.q_out : a.k_out;
-            if (is_q || (is_k && a.k_out.data)) {
-                uint16_t *const row = to.data + token * to.row + head * to.head;
-                *reinterpret_cast<u32x4 *>(row + at0) = out[0];
-                *reinterpret_cast<u32x4 *>(row + at1) = out[1];
-            }
-            if (kStore == kHeadsOnly || is_q || slot < 0) continue;
-            const uint64_t row = ((((uint64_t)slot >> a.c.shift) * a.c.kv_heads + head) << a.c.shift) + (slot & ((1 << a.c.shift) - 1));
-            uint8_t *const store = is_v ? a.c.v : a.c.k;
-            if (kStore == kHeadsInt8) {
-                uint32_t m = 0x0D800000u;      // 2^-100
-#pragma unroll
-                for (int x = 0; x < 16; ++x) m = max(m, __float_as_uint(y[x]) & 0x7FFFFFFFu);
-                const float top = __uint_as_float(row_max<kLanes>(m)), inv = 127.0f / top;
-                uint32_t codes[4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    codes[x] = 0;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) codes[x] |= (uint32_t)((int)__builtin_rintf(y[4 * x + j] * inv) & 255) << (8 * j);
-                }
-                *reinterpret_cast<u32x2 *>(store + row * D + at0) = u32x2{codes[0], codes[1]};
-                *reinterpret_cast<u32x2 *>(store + row * D + at1) = u32x2{codes[2], codes[3]};
-                if (l == 0) (is_v ? a.c.v_scale : a.c.k_scale)[row] = top / 127.0f;
-            } else {
-                *reinterpret_cast<u32x4 *>(store + 2 * (row * D + at0)) = out[0];
-                *reinterpret_cast<u32x4 *>(store + 2 * (row * D + at1)) = out[1];
-            }
+            *reinterpret_cast<u32x2 *>(store + row * D + at0) = u32x2{codes[0], codes[1]};
+            *reinterpret_cast<u32x2 *>(store + row * D + at1) = u32x2{codes[2], codes[3]};
+            if (l == 0) (is_v ? a.c.v_scale : a.c.k_scale)[row] = top / 127.0f;
+        } else {
+            __builtin_nontemporal_store(out[0], reinterpret_cast<u32x4 *>(store + 2 * (row * D + at0)));
+            __builtin_nontemporal_store(out[1], reinterpret_cast<u32x4 *>(store + 2 * (row * D + at1)));
         }
     }
 }
