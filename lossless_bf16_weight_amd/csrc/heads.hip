@@ -165,8 +165,8 @@ __global__ __launch_bounds__(kThreads, 4) void heads_kernel(HeadsArgs a) {
         const Rows &to = is_q ? a.q_out : a.k_out;
         if (is_q || (is_k && a.k_out.data)) {
             uint16_t *const row = to.data + token * to.row + head * to.head;
-            __builtin_nontemporal_store(out[0], reinterpret_cast<u32x4 *>(row + at0));
-            __builtin_nontemporal_store(out[1], reinterpret_cast<u32x4 *>(row + at1));
+            *reinterpret_cast<u32x4 *>(row + at0) = out[0];
+            *reinterpret_cast<u32x4 *>(row + at1) = out[1];
         }
         if (kStore == kHeadsOnly || is_q || slot < 0) continue;
         const uint64_t row = ((((uint64_t)slot >> a.c.shift) * a.c.kv_heads + head) << a.c.shift) + (slot & ((1 << a.c.shift) - 1));
@@ -187,8 +187,8 @@ __global__ __launch_bounds__(kThreads, 4) void heads_kernel(HeadsArgs a) {
             *reinterpret_cast<u32x2 *>(store + row * D + at1) = u32x2{codes[2], codes[3]};
             if (l == 0) (is_v ? a.c.v_scale : a.c.k_scale)[row] = top / 127.0f;
         } else {
-            __builtin_nontemporal_store(out[0], reinterpret_cast<u32x4 *>(store + 2 * (row * D + at0)));
-            __builtin_nontemporal_store(out[1], reinterpret_cast<u32x4 *>(store + 2 * (row * D + at1)));
+            *reinterpret_cast<u32x4 *>(store + 2 * (row * D + at0)) = out[0];
+            *reinterpret_cast<u32x4 *>(store + 2 * (row * D + at1)) = out[1];
         }
     }
 }
