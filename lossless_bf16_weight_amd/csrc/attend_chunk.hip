@@ -21,8 +21,6 @@
 // of all tiles over `places` workgroups give a quota, and a sequence's tiles
 // are split into as many parts as their steps hold quotas.  A second kernel
 // joins the parts.
-#include <type_traits>
-
 #include "attend_tiles.hpp"
 
 namespace df11 {
@@ -70,8 +68,7 @@ __device__ __forceinline__ bool find_piece(const ChunkArgs &a, uint32_t item, Pi
             look(s0);
             total += (float)tiles * (float)steps;
         }
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) total += __shfl_xor(total, d);
+        total = __uint_as_float(of_lane(__float_as_uint(sum_to_lane(total)), 63));
         // (above the quotient, whatever the sum's rounding: see chunk_split)
         quota = (uint32_t)fminf(total * a.by_parts * (1.0f + 0x1p-18f), 4.0e9f) + 1;
     } else if (a.n_seqs > 64) {
@@ -91,11 +88,7 @@ __device__ __forceinline__ bool find_piece(const ChunkArgs &a, uint32_t item, Pi
         if (!kSplit || a.n_seqs > 64 || s0 == 0) look(s0);
         const uint32_t parts = kSplit ? max(1u, min((steps + quota / 2) / quota, steps >> a.least_shift)) : 1;
         const uint32_t places = parts > 1 ? tiles * parts : 0, items = kJoin ? (parts > 1 ? tiles : 0) : tiles * parts;
-        uint32_t items_to = items, places_to = places;     // sums up to this lane
-        for (uint32_t d = 1; d < min(a.n_seqs, 64u); d *= 2) {
-            const uint32_t x = __shfl_up(items_to, d), y = kSplit ? __shfl_up(places_to, d) : 0;
-            if (lane >= d) items_to += x, places_to += y;
-        }
+        const uint32_t items_to = sum_to_lane(items), places_to = kSplit ? sum_to_lane(places) : 0;
         uint32_t before = items_before + items_to - items;
         if (kSplit && !kJoin && a.n_seqs <= 64) {
             // the sequences with the longest parts first: one of them at the end

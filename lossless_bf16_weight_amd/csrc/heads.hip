@@ -15,8 +15,6 @@
 // part apart, with neighbours two chunks side by side, pairs 8 l .. 8 l + 7 of
 // lane l either way.  A wave takes the rows of one token eight (heads of 64:
 // sixteen) at a time, whose sines it computes once.
-#include <type_traits>
-
 #include "serve_device.hpp"
 #include "serve_internal.hpp"
 

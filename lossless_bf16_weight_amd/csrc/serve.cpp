@@ -276,13 +276,16 @@ df11_status check_prompt_sizes(const df11_attend_prompt_args &a) {
 }
 
 // What attend_chunk's workgroups need for dividing a call's work, whose lengths
-// the host does not know: the parts of equal size that it would be (a quarter
-// more than the workgroups that run at a time, two for each compute unit, for
-// parts are not equal), and the least steps of one.  A tile's steps over the
-// quota, rounded, are its parts: two from one and a half on, so that all split
-// tiles have at most four thirds of the parts asked for, and so many places the
-// workspace has.  Sequences of many are taken whole: each workgroup would read
-// all their lengths.
+// the host does not know: the parts of equal size that it would be, as many as
+// workgroups run at a time, two for each compute unit, and the least steps of
+// one, four (64 queries on 2001 keys 18 us, with eight 22, with two 20).  A
+// tile's steps over the quota, rounded, are its parts: two from one and a half
+// on, so that all split tiles have at most four thirds of the parts asked for,
+// and so many places the workspace has.  (A quarter more parts, which level out
+// better, are a second round of workgroups where parts are equal: 256 queries
+// on 4256 keys 45 us and 38, four pieces on 8700 to 5000 keys 123 us and 131.)
+// Sequences of many are taken whole: each workgroup would read all their
+// lengths.
 struct ChunkSplit {
     uint32_t most_steps, parts, places, least_shift;
 };
@@ -299,7 +302,7 @@ ChunkSplit chunk_split(const df11_attend_chunk_args &a, int dev) {
     const Window w = window_of(a.window, a.sinks, positions);
     if (w.keys) s.most_steps = (uint32_t)((w.keys + (kPromptTile - 1) / group + 1 + 2 * (kPromptKeys - 1)) / kPromptKeys + ceil_div(w.sinks, kPromptKeys));
     const uint64_t steps = std::min<uint64_t>(ceil_div(positions, kPromptKeys), s.most_steps);
-    const uint64_t parts = 5 * compute_units(dev) / 2 / a.cache.n_kv_heads, of_tile = steps >> s.least_shift;
+    const uint64_t parts = 2 * compute_units(dev) / a.cache.n_kv_heads, of_tile = steps >> s.least_shift;
     if (a.n_q == 0 || a.n_seqs == 0 || a.n_seqs > kChunkMostPlanned || parts < 2 || of_tile < 2) return s;
     s.parts = (uint32_t)parts;
     s.places = (uint32_t)std::min(4 * parts / 3, chunk_tile_slots(a) * of_tile);

@@ -4,6 +4,8 @@
 #pragma once
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 namespace df11 {
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -38,6 +40,22 @@ __device__ __forceinline__ f32x2 with_lane_16(float x) {
     const uint32_t a = __float_as_uint(x);
     const auto r = __builtin_amdgcn_permlane16_swap(a, a, false, false);
     return f32x2{__uint_as_float(r[0]), __uint_as_float(r[1])};
+}
+
+// Sums over the lanes of a wave up to this one; the last lane has the whole sum.
+template <class T>
+__device__ __forceinline__ T sum_to_lane(T x) {
+    const auto more = [&](auto ctrl, auto rows) {
+        x += __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), decltype(ctrl)::value, decltype(rows)::value, 0xF, false));
+    };
+    constexpr std::integral_constant<int, 0xF> all{};
+    more(std::integral_constant<int, 0x111>{}, all);      // from 1, 2, 4 and 8 lanes below, in 16
+    more(std::integral_constant<int, 0x112>{}, all);
+    more(std::integral_constant<int, 0x114>{}, all);
+    more(std::integral_constant<int, 0x118>{}, all);
+    more(std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xA>{});   // the 16 below, the 32 below
+    more(std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xC>{});
+    return x;
 }
 
 // Softmax sums are kept against a base, m below, that is raised only when a

@@ -132,7 +132,7 @@ def test_workspaces():
     assert df11.chunk_workspace(64, 1000, 32, 8, 128, 16, 512) == 0
     need = df11.chunk_workspace(64, 1, 32, 8, 128, 16, 512)
     tile = 128 * 130 * 4
-    most = 5 * 256 // 2 // 8 * 4 // 3 * 8 * tile
+    most = 2 * 256 // 8 * 4 // 3 * 8 * tile
     assert need and need % (8 * tile) == 0 and need <= most
     assert df11.chunk_workspace(64, 1, 32, 8, 128, 16, 1 << 20) == most
     assert df11.chunk_workspace(64, 1, 32, 8, 128, 16, 1 << 20, 100, 4) == 0       # (a window of few steps)
