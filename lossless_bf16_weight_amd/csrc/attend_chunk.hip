@@ -501,11 +501,12 @@ __global__ __launch_bounds__(kThreads, 2) void attend_chunk_kernel(ChunkArgs a) 
 
 // Joins the parts of 32 rows (those of wave blockIdx.y of a split tile):
 // out = sum_a w_a o_a / sum_a w_a l_a with w_a = 2^(m_a - max m), the maximum
-// taken as the parts come.  A wave takes 32 columns.
+// taken as the parts come.  A wave takes 16 columns, so that few tiles are many
+// waves' work and the parts of most are all in flight at once.
 template <int D>
-__global__ __launch_bounds__(64 * D / 32) void join_chunk_kernel(ChunkArgs a) {
+__global__ __launch_bounds__(64 * D / 16) void join_chunk_kernel(ChunkArgs a) {
     constexpr int kDTiles = D / 32;
-    constexpr int kBatch = 2;       // parts in flight
+    constexpr int kBatch = 8;       // parts in flight
     const uint32_t lane = threadIdx.x & 63u, i = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t col = lane & 31u, half = lane >> 5, kv_head = blockIdx.x % a.c.kv_heads;
     Piece p;
@@ -516,39 +517,42 @@ __global__ __launch_bounds__(64 * D / 32) void join_chunk_kernel(ChunkArgs a) {
     const uint32_t parts = (n_steps + p.per - 1) / p.per;
     const uint64_t at = ((uint64_t)p.place * a.c.kv_heads + kv_head) * kWaves + blockIdx.y, next_part = (uint64_t)a.c.kv_heads * kWaves;
     const f32x2 *const ml = reinterpret_cast<const f32x2 *>(a.part_ml) + at * kWaveRows + col;
-    const f32x4 *const part = reinterpret_cast<const f32x4 *>(a.part) + (at * kDTiles + i) * 256 + lane;
-    f32x16 o = {};
+    const f32x4 *const part = reinterpret_cast<const f32x4 *>(a.part) + at * (kDTiles * 256) + i * 128 + lane;
+    f32x4 o[2] = {};
     float l = 0, m = -__builtin_inff();
     for (uint32_t s = 0; s < parts; s += kBatch) {
         f32x2 stat[kBatch];
-        f32x4 v[kBatch][4];
-#pragma unroll
-        for (int x = 0; x < kBatch; ++x) {
-            const uint32_t from = min(s + x, parts - 1);
-            stat[x] = ml[from * next_part * kWaveRows];
-#pragma unroll
-            for (int g = 0; g < 4; ++g) v[x][g] = __builtin_nontemporal_load(part + from * next_part * (kDTiles * 256) + g * 64);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        float next = m;
-#pragma unroll
-        for (int x = 0; x < kBatch; ++x)
-            if (s + x < parts) next = fmaxf(next, stat[x].x);
-        const float base = next == -__builtin_inff() ? 0.0f : next, keep = exp2_fast(m - base);
-        m = next;
-        l *= keep;
-        o *= keep;
+        f32x4 v[kBatch][2];
 #pragma unroll
         for (int x = 0; x < kBatch; ++x) {
             if (s + x >= parts) break;      // (a part past the last was not written)
+            stat[x] = ml[(s + x) * next_part * kWaveRows];
+#pragma unroll
+            for (int g = 0; g < 2; ++g) v[x][g] = part[(s + x) * next_part * (kDTiles * 256) + g * 64];
+        }
+        float next = m;
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x) {
+            if (s + x >= parts) break;
+            next = fmaxf(next, stat[x].x);
+        }
+        const float base = next == -__builtin_inff() ? 0.0f : next, keep = exp2_fast(m - base);
+        m = next;
+        l *= keep;
+        o[0] *= keep;
+        o[1] *= keep;
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x) {
+            if (s + x >= parts) break;
             const float w = exp2_fast(stat[x].x - base);
             l += w * stat[x].y;
-#pragma unroll
-            for (int y = 0; y < 16; ++y) o[y] += w * v[x][y / 4][y % 4];
+            o[0] += w * v[x][0];
+            o[1] += w * v[x][1];
         }
     }
     const uint32_t query = over_group(a, row), head = kv_head * a.group + row - query * a.group;
-    store_tile(o * (l == 0.0f ? 0.0f : 1.0f / l), a.out.data + (int64_t)(p.q0 + query) * a.out.row + head * a.out.head + 32 * i, half, row < n_rows);
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    store_16(o[0] * inv, o[1] * inv, a.out.data + (int64_t)(p.q0 + query) * a.out.row + head * a.out.head + 16 * i, half, row < n_rows);
 }
 
 template <int D, bool kInt8>
@@ -567,7 +571,7 @@ hipError_t launch_attend_chunk(const ChunkArgs &a, uint32_t head_dim, bool int8,
     if (e != hipSuccess || !split) return e;
     // (a split tile has two parts at least)
     const uint32_t tiles = a.places / 2 < a.tile_slots ? a.places / 2 : a.tile_slots;
-    hipLaunchKernelGGL(head_dim == 64 ? join_chunk_kernel<64> : join_chunk_kernel<128>, dim3(tiles * a.c.kv_heads, kWaves), dim3(2 * head_dim), 0,
+    hipLaunchKernelGGL(head_dim == 64 ? join_chunk_kernel<64> : join_chunk_kernel<128>, dim3(tiles * a.c.kv_heads, kWaves), dim3(4 * head_dim), 0,
                        stream, a);
     return hipGetLastError();
 }

@@ -42,9 +42,22 @@ __device__ __forceinline__ uint32_t over_group(const Args &a, uint32_t row) {
     return a.group == 1 ? row : __umulhi(row, a.group_magic) >> a.group_shift;
 }
 
-// Writes a product's 32 x 32 results as BF16, the lane's column to 32 words
-// from `to`.  The lane has four of each eight neighbours, the lane 32 away the
-// others: with two such eights they exchange halves and write one each.
+// Writes 16 of a product's 32 rows as BF16, the lane's column to 16 words from
+// `to`.  The lane has four of each eight neighbours (a, then b), the lane 32
+// away the others: they exchange halves and write eight each.
+__device__ __forceinline__ void store_16(f32x4 a, f32x4 b, uint16_t *to, uint32_t half, bool real) {
+    uint32_t w[2][2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const auto r = __builtin_amdgcn_permlane32_swap(pack_bf16(a[2 * x], a[2 * x + 1]), pack_bf16(b[2 * x], b[2 * x + 1]), false, false);
+        w[0][x] = r[0];
+        w[1][x] = r[1];
+    }
+    if (real) *reinterpret_cast<u32x4 *>(to + 8 * half) = u32x4{w[0][0], w[0][1], w[1][0], w[1][1]};
+}
+
+// All 32 rows.  (The same steps: through store_16 attend_prompt's kernels came
+// out otherwise.)
 __device__ __forceinline__ void store_tile(const f32x16 &o, uint16_t *to, uint32_t half, bool real) {
 #pragma unroll
     for (int g = 0; g < 4; g += 2) {
