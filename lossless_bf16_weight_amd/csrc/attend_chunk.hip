@@ -15,12 +15,15 @@
 // from memory into LDS without passing through registers; codes pass through
 // them, converted once by the workgroup.  The steps of a tile are those of the
 // sinks and those of the window.
+// Sequences of one new token, whose rows are few, go another way: see
+// attend_single.
 //
 // How long the sequences are the host does not know.  Each workgroup finds
 // from q_starts and lens how the work of the whole call is divided: the steps
 // of all tiles over `places` workgroups give a quota, and a sequence's tiles
 // are split into as many parts as their steps hold quotas.  A second kernel
 // joins the parts.
+#include "attend_columns.hpp"
 #include "attend_tiles.hpp"
 
 namespace df11 {
@@ -149,6 +152,206 @@ __device__ __forceinline__ Steps steps_of(const ChunkArgs &a, const Piece &p) {
     return s;
 }
 
+// 64 entries of a sequence's table, a lane each, asked for before they are used.
+struct Entries {
+    const int32_t *pages;
+    uint32_t last, from, held;      // the last entry of the sequence; the first in `held`
+    __device__ __forceinline__ void read(const ChunkArgs &a, uint32_t key) {
+        from = key >> a.c.shift;
+        held = (uint32_t)pages[min(from + (threadIdx.x & 63u), last)];
+    }
+    // those of n keys from `key` on
+    __device__ __forceinline__ void need(const ChunkArgs &a, uint32_t key, uint32_t n) {
+        if (key >> a.c.shift < from || (key + n - 1) >> a.c.shift > from + 63) read(a, key);
+    }
+    // The cache's row of key `key`, the first of 16 (the host keeps the rows'
+    // number below 2^32).
+    __device__ __forceinline__ uint32_t row(const ChunkArgs &a, uint32_t kv_head, uint32_t key) const {
+        const uint32_t page = min(of_lane(held, (key >> a.c.shift) - from), a.c.n_pages - 1);
+        return ((page * a.c.kv_heads + kv_head) << a.c.shift) + (key & ((1u << a.c.shift) - 1));
+    }
+};
+
+// A part of a sequence of one new token (the queries of a kv head's group, at
+// most 16, are columns): its waves take 32 keys in turn, as in attend_token.hip,
+// each with the next ones' rows in registers and a tile of its own in LDS, and
+// are joined through LDS at the end.  Bound by HBM traffic: 128 KB in flight on
+// a compute unit, where the tiles of 128 rows have 64 (32 sequences of 1 to
+// 8192 keys, 470 MB: see the head of this file).  own: the wave's LDS, of
+// max(32 rows, 16 columns of D + 4 floats) bytes; area(w): wave w's.
+template <int D, bool kInt8, class Area>
+__device__ __forceinline__ void attend_single(const ChunkArgs &a, const Piece &p, const Steps &steps, uint32_t step_begin, uint32_t step_end, bool whole,
+                                              uint32_t kv_head, uint32_t wave, const Area &area, float (*ml)[2][16]) {
+    constexpr int kRow = kInt8 ? D : 2 * D;            // bytes of a stored row
+    constexpr int kChunks = kRow / 16;                 // 16-byte chunks of it
+    constexpr int kLoads = kTokenKeys * kChunks / 64;  // chunks a lane loads of 32 K rows, and of V rows
+    constexpr int kDTiles = D / 16;
+    constexpr int kOStride = D + 4;
+    const uint32_t lane0 = threadIdx.x & 63u, lane = lane0, col = lane & 15u, grp = lane >> 4;
+    const Seen seen = seen_by(a, 0, 1, p.n_k);
+    const uint32_t n_k = p.n_k;
+    u32x4 q[D / 32];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+        q[i] = u32x4{0, 0, 0, 0};
+        if (col < a.group)
+            q[i] = *reinterpret_cast<const u32x4 *>(a.q.data + (int64_t)p.q0 * a.q.row + (kv_head * a.group + col) * a.q.head + column_operand_at<kInt8>(i, grp));
+    }
+    f32x4 o[kDTiles];
+#pragma unroll
+    for (int i = 0; i < kDTiles; ++i) o[i] = f32x4{0, 0, 0, 0};
+    float m = -__builtin_inff(), l = 0;
+    const float log2_n = log2_up(n_k);
+    uint8_t *const tile = area(wave);
+
+    Entries entries{a.t.pages + p.seq * a.t.stride, (n_k - 1) >> a.c.shift, 0, 0};
+    u32x4 kw[kLoads], vw[kLoads];
+    f32x4 ks[2], vs[2];
+    uint32_t half_row[2];
+    const uint32_t last_half = (n_k - 1) & ~15u;
+    const auto key_of = [&](uint32_t turn) { return steps.key(turn >> 1) + (turn & 1) * kTokenKeys; };
+    // (halves past the end repeat the last one)
+    const auto find_rows = [&](uint32_t key0) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) half_row[t] = entries.row(a, kv_head, min(key0 + 16 * t, last_half));
+    };
+    const auto load = [&](const uint8_t *pages, u32x4 *w) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const u32x4 *const half = reinterpret_cast<const u32x4 *>(pages + (uint64_t)half_row[2 * i / kLoads] * kRow);
+            w[i] = __builtin_nontemporal_load(half + i % (kLoads / 2) * 64 + lane0);
+        }
+    };
+    const auto load_scales = [&] {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            ks[t] = reinterpret_cast<const f32x4 *>(a.c.k_scale + half_row[t])[grp];
+            vs[t] = reinterpret_cast<const f32x4 *>(a.c.v_scale + half_row[t])[grp];
+        }
+    };
+    // LDS keeps a wave's accesses in order; this keeps the compiler's.
+    const auto handed_over = [] {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+        __builtin_amdgcn_wave_barrier();
+    };
+    uint32_t turn = 2 * step_begin + wave;
+    const uint32_t turns = 2 * step_end;
+    if (turn < turns) entries.read(a, min(key_of(turn), last_half));
+    // (the queries are here before the loop, so that its products do not wait for
+    // what is loaded in it)
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) asm volatile("" : "+v"(q[i]));
+    __builtin_amdgcn_s_waitcnt(0x0F70);
+    if (turn < turns) {
+        // (a turn past the sequence's end is not taken)
+        find_rows(key_of(turn));
+        if (turn + kWaves < turns) entries.need(a, min(key_of(turn + kWaves), last_half), kTokenKeys);
+        load(a.c.k, kw);
+        load(a.c.v, vw);
+        if (kInt8) load_scales();
+    }
+    for (; turn < turns; turn += kWaves) {
+        const uint32_t key0 = key_of(turn), next = turn + kWaves;
+        if (key0 >= n_k) break;
+        uint32_t lane = lane0;
+        asm volatile("" : "+v"(lane));
+        const uint32_t grp = lane >> 4;
+        handed_over();
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const uint32_t at = i * 64 + lane;
+            *reinterpret_cast<u32x4 *>(tile + column_k_at<kRow>(at / kChunks, at % kChunks)) = kw[i];
+        }
+        handed_over();
+        if (next < turns) find_rows(key_of(next));
+        if (next + kWaves < turns) entries.need(a, min(key_of(next + kWaves), last_half), kTokenKeys);
+        load(a.c.k, kw);                       // (past the end: the last rows once more, which nobody uses)
+        __builtin_amdgcn_sched_barrier(0);
+        f32x4 s[2];
+        column_scores<D, kInt8>(tile, lane, [&](int i) { return q[i]; }, s);
+        const bool masked = key0 + kTokenKeys > seen.end || (key0 < seen.begin && key0 + kTokenKeys > a.sinks);
+        const auto out_of_sight = [&](uint32_t key) { return (key >= seen.end) | ((key < seen.begin) & (key >= a.sinks)); };
+        if (masked) {
+            // weights of rows that are not seen are 0, and 0 times an infinity would be NaN
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const bool out = out_of_sight(key0 + (i * 64 + lane) / kChunks);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) vw[i][x] = out ? 0 : vw[i][x];
+            }
+        }
+        handed_over();
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const uint32_t at = i * 64 + lane;
+            *reinterpret_cast<u32x4 *>(tile + column_v_at<kRow, kInt8>(at / kChunks, at % kChunks)) = vw[i];
+        }
+        handed_over();
+        load(a.c.v, vw);
+        f32x4 v_scale[2];
+        if (kInt8) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                s[t] *= ks[t] * a.log2_scale;
+                v_scale[t] = vs[t];
+            }
+            load_scales();
+        }
+        if (masked) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const bool out = out_of_sight(key0 + 16 * t + 4 * grp + i);
+                    s[t][i] = out ? -__builtin_inff() : s[t][i];
+                    if (kInt8) v_scale[t][i] = out ? 0 : v_scale[t][i];
+                }
+        }
+        column_update<D, kInt8>(tile, lane, s, v_scale, kInt8 ? 1.0f : a.log2_scale, log2_n, o, m, l);
+    }
+    f32x2 two = with_lane_16(l);
+    two = with_lane_32(two.x + two.y);
+    l = two.x + two.y;
+
+    // join the waves
+    if (lane < 16) {
+        ml[wave][0][lane] = m;
+        ml[wave][1][lane] = l;
+    }
+    __syncthreads();
+    float most = -__builtin_inff();
+#pragma unroll
+    for (int w = 0; w < (int)kWaves; ++w) most = fmaxf(most, ml[w][0][col]);
+    const float weight = exp2_fast(m - (most == -__builtin_inff() ? 0.0f : most));
+#pragma unroll
+    for (int i = 0; i < kDTiles; ++i)
+        *reinterpret_cast<f32x4 *>(reinterpret_cast<float *>(tile) + col * kOStride + 16 * i + 4 * grp) = o[i] * weight;
+    __syncthreads();
+    for (uint32_t at = threadIdx.x; at < a.group * (D / 4); at += kThreads) {
+        const uint32_t c = at / (D / 4), d = at % (D / 4) * 4;
+        f32x4 sum = {0, 0, 0, 0};
+        float most_c = -__builtin_inff(), l_c = 0;
+#pragma unroll
+        for (int w = 0; w < (int)kWaves; ++w) most_c = fmaxf(most_c, ml[w][0][c]);
+        const float base_c = most_c == -__builtin_inff() ? 0.0f : most_c;
+#pragma unroll
+        for (int w = 0; w < (int)kWaves; ++w) {
+            sum += *reinterpret_cast<const f32x4 *>(reinterpret_cast<const float *>(area(w)) + c * kOStride + d);
+            l_c += ml[w][1][c] * exp2_fast(ml[w][0][c] - base_c);
+        }
+        if (whole) {
+            const float inv = l_c == 0.0f ? 0.0f : 1.0f / l_c;
+            *reinterpret_cast<u32x2 *>(a.out.data + (int64_t)p.q0 * a.out.row + (kv_head * a.group + c) * a.out.head + d) =
+                u32x2{pack_bf16(sum.x * inv, sum.y * inv), pack_bf16(sum.z * inv, sum.w * inv)};
+        } else {
+            // where the lanes of a tile of 32 rows would hold it, for the join
+            const uint64_t at_part = ((uint64_t)(p.place + p.part) * a.c.kv_heads + kv_head) * kWaves;
+            reinterpret_cast<f32x4 *>(a.part)[at_part * (D / 32 * 4 * 64) + d / 8 * 64 + (d / 4 & 1) * 32 + c] = sum;
+            if (d == 0) reinterpret_cast<f32x2 *>(a.part_ml)[at_part * kWaveRows + c] = f32x2{most_c, l_c};
+        }
+    }
+}
+
 template <int D, bool kInt8, bool kSplit>
 __global__ __launch_bounds__(kThreads, 2) void attend_chunk_kernel(ChunkArgs a) {
     constexpr int kChunks = D / 8;                           // 16-byte chunks of a row of words
@@ -180,6 +383,13 @@ __global__ __launch_bounds__(kThreads, 2) void attend_chunk_kernel(ChunkArgs a) 
         whole = steps.n <= p.per;
     }
 
+    if (n_q == 1 && a.group <= 16) {
+        __shared__ float ml[kWaves][2][16];
+        const auto area = [&](uint32_t w) { return w == 0 ? kt0 : w == 1 ? kt1 : w == 2 ? vt0 : vt1; };
+        attend_single<D, kInt8>(a, p, steps, step_begin, step_end, whole, kv_head, wave, area, ml);
+        return;
+    }
+
     const uint32_t wave_first = row0 + wave * kWaveRows, row = wave_first + col;
     const bool real = row < n_rows;
     const uint32_t query = over_group(a, row), head = kv_head * a.group + row - query * a.group;
@@ -209,22 +419,9 @@ __global__ __launch_bounds__(kThreads, 2) void attend_chunk_kernel(ChunkArgs a) 
         l = 0;
     };
 
-    // 64 entries of the sequence's table, a lane each, asked for a step before
-    // they are used.
-    uint32_t entries_from = 0, entries = 0;
-    const auto read_entries = [&](uint32_t key0) {
-        entries_from = key0 >> a.c.shift;
-        const uint32_t at = min(entries_from + lane, (n_k - 1) >> a.c.shift);
-        entries = (uint32_t)a.t.pages[p.seq * a.t.stride + at];
-    };
-    const auto need_entries = [&](uint32_t key0) {
-        if (key0 >> a.c.shift < entries_from || (key0 + kPromptKeys - 1) >> a.c.shift > entries_from + 63) read_entries(key0);
-    };
-    // The cache's row of 16 keys' first (the host keeps their number below 2^32).
-    const auto row_of = [&](uint32_t key) {
-        const uint32_t page = min(of_lane(entries, (key >> a.c.shift) - entries_from), a.c.n_pages - 1);
-        return ((page * a.c.kv_heads + kv_head) << a.c.shift) + (key & ((1u << a.c.shift) - 1));
-    };
+    Entries entries{a.t.pages + p.seq * a.t.stride, (n_k - 1) >> a.c.shift, 0, 0};
+    const auto need_entries = [&](uint32_t key0) { entries.need(a, key0, kPromptKeys); };
+    const auto row_of = [&](uint32_t key) { return entries.row(a, kv_head, key); };
 
     // Words: a step's K and V rows go from memory into LDS without passing
     // through registers, one step ahead: the chunk that lane `at` of the tile
@@ -423,7 +620,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_chunk_kernel(ChunkArgs a) 
     };
 
     start();
-    if (step_begin < step_end) read_entries(steps.key(step_begin));
+    if (step_begin < step_end) entries.read(a, steps.key(step_begin));
     if constexpr (kInt8) {
         if (step_begin < step_end) {
             load_codes(steps.key(step_begin));
