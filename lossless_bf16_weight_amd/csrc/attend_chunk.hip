@@ -484,7 +484,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_chunk_kernel(ChunkArgs a) 
             *reinterpret_cast<u32x4 *>(vt + v_at<D>(r, 2 * code_chunk)) = bf16_of_bytes8(u32x2{vw[i].x, vw[i].y});
             *reinterpret_cast<u32x4 *>(vt + v_at<D>(r, 2 * code_chunk + 1)) = bf16_of_bytes8(u32x2{vw[i].z, vw[i].w});
         }
-        if (wave < 2) sc[threadIdx.x] = scale_w;     // (K's from wave 0, V's from wave 1)
+        if (wave < 2) sc[threadIdx.x] = wave ? scale_w : scale_w * a.log2_scale;     // (V's from wave 1, K's, of scores in base 2, from wave 0)
     };
 
     // One step's keys.  kCareful: values that are infinite or NaN at keys which
@@ -516,16 +516,17 @@ __global__ __launch_bounds__(kThreads, 2) void attend_chunk_kernel(ChunkArgs a) 
             __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
         }
         __builtin_amdgcn_sched_group_barrier(0x008, kAhead, 0);
-        if (kInt8) {
+        // in base 2, less the maximum so far
+        const float base = m == -__builtin_inff() ? 0.0f : m;
 #pragma unroll
-            for (int t = 0; t < kHalves; ++t)
+        for (int t = 0; t < kHalves; ++t)
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const f32x4 w = *reinterpret_cast<const f32x4 *>(sc + 32 * t + 8 * g + 4 * half);
+            for (int g = 0; g < 4; ++g) {
+                f32x4 by = {a.log2_scale, a.log2_scale, a.log2_scale, a.log2_scale};
+                if (kInt8) by = *reinterpret_cast<const f32x4 *>(sc + 32 * t + 8 * g + 4 * half);     // (times the keys' scales)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) s[t][4 * g + i] *= w[i];
-                }
-        }
+                for (int i = 0; i < 4; ++i) s[t][4 * g + i] = __builtin_fmaf(s[t][4 * g + i], by[i], -base);
+            }
         if (key0 + kPromptKeys > clear_end || (key0 < clear_begin && key0 + kPromptKeys > a.sinks)) {
 #pragma unroll
             for (int t = 0; t < kHalves; ++t)
@@ -542,16 +543,19 @@ __global__ __launch_bounds__(kThreads, 2) void attend_chunk_kernel(ChunkArgs a) 
 #pragma unroll
             for (int i = 0; i < 16; ++i) top = fmaxf(top, s[t][i]);
         const f32x2 halves = with_lane_32(top);
-        top = fmaxf(halves.x, halves.y) * a.log2_scale;
-        if (__any(top > m - log2_n)) {
-            const float next = fmaxf(m, top + (kSlack + log2_n));
-            const float keep = exp2_fast(m - (next == -__builtin_inff() ? 0.0f : next));
+        top = fmaxf(halves.x, halves.y);
+        if (__any(top > -log2_n || m == -__builtin_inff())) {
+            const float next = fmaxf(m, base + top + (kSlack + log2_n)), more = (next == -__builtin_inff() ? 0.0f : next) - base;
+            const float keep = exp2_fast(m - base - more);
             m = next;
             l *= keep;
 #pragma unroll
             for (int i = 0; i < kDTiles; ++i) o[i] *= keep;
+#pragma unroll
+            for (int t = 0; t < kHalves; ++t)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[t][i] -= more;
         }
-        const float base = m == -__builtin_inff() ? 0.0f : m;
 #pragma unroll
         for (int t = 0; t < kHalves; ++t) {
 #pragma unroll
@@ -562,7 +566,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_chunk_kernel(ChunkArgs a) 
                     float e[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        e[i] = exp2_fast(__builtin_fmaf(s[t][8 * st + 4 * g + i], a.log2_scale, -base));
+                        e[i] = exp2_fast(s[t][8 * st + 4 * g + i]);
                         l += e[i];
                     }
                     if (kInt8) {
