@@ -10,7 +10,7 @@
 // scores, a value's scale its weights, in 32 bits.
 //
 // Rows, tiles, products and the steps of 64 keys through LDS are those of
-// attend_prompt.hip; rows come from pages, 16 at a time from one page, whose
+// attend_prompt.hip, but a workgroup may have eight waves and 256 rows; rows come from pages, 16 at a time from one page, whose
 // numbers lie in the lanes of a register (64 entries of the table).  Words go
 // from memory into LDS without passing through registers; codes pass through
 // them, converted once by the workgroup.  The steps of a tile are those of the
@@ -33,8 +33,7 @@ __device__ float mul_or_zero(float x, float y) __asm("llvm.amdgcn.fmul.legacy");
 
 namespace {
 
-constexpr uint32_t kWaves = 4, kThreads = 64 * kWaves;
-constexpr uint32_t kWaveRows = 32;
+constexpr uint32_t kWaveRows = 32;             // a workgroup has four waves or eight
 constexpr int kHalves = kPromptKeys / 32;      // of a step: 32 keys are a product's rows
 constexpr int kAhead = 4;                      // reads of K ahead of the products
 
@@ -48,10 +47,25 @@ struct Piece {
 
 __device__ __forceinline__ uint32_t of_lane(uint32_t x, uint32_t lane) { return __builtin_amdgcn_readlane(x, lane); }
 
+// Parts of the tiles of a single sequence of many rows: as they are equal, the
+// number that ends soonest, in steps of a workgroup among as many as run at a
+// time.  A part has two steps' time beside its own, and what is written and
+// joined of it.  (Few tiles have many parts, where rounding is harmless.)
+__device__ __forceinline__ uint32_t parts_of_one(const ChunkArgs &a, uint32_t tiles, uint32_t steps, uint32_t otherwise) {
+    if (tiles * 8 < a.at_a_time) return otherwise;
+    const uint32_t lane = threadIdx.x & 63u, parts = lane + 1, items = tiles * parts, rest = items % a.at_a_time;
+    float cost = (float)(items / a.at_a_time + (rest != 0)) * (float)((steps + parts - 1) / parts + (parts > 1 ? 2 : 1));
+    if (parts > 1) cost += 2.0f + 0.014f * (float)(items * a.c.kv_heads);
+    const bool possible = parts == 1 || (parts <= steps >> a.least_shift && items <= a.places);
+    const uint32_t key = possible ? (__float_as_uint(cost) & ~63u) | lane : ~0u;
+    return (of_lane(over_lanes(key, ~0u, Least{}), 63) & 63u) + 1;
+}
+
 // Finds work item `item` (kJoin: the tile of that number among those that are
 // split).  False where there is none.
-template <bool kSplit, bool kJoin>
+template <uint32_t kWaves, bool kSplit, bool kJoin>
 __device__ __forceinline__ bool find_piece(const ChunkArgs &a, uint32_t item, Piece *p) {
+    constexpr uint32_t kTile = kWaves * kWaveRows;
     const uint32_t lane = threadIdx.x & 63u;
     uint32_t q0 = 0, n_q = 0, n_k = 0, tiles = 0, steps = 0;
     const auto look = [&](uint32_t s0) {
@@ -61,7 +75,7 @@ __device__ __forceinline__ bool find_piece(const ChunkArgs &a, uint32_t item, Pi
         q0 = from;
         n_q = ok ? to - from : 0;
         n_k = (uint32_t)min((int64_t)max(a.lens[s], 0), (int64_t)a.t.width << a.c.shift);
-        tiles = (n_q * a.group + kPromptTile - 1) / kPromptTile;
+        tiles = (n_q * a.group + kTile - 1) / kTile;
         steps = min((n_k + kPromptKeys - 1) / kPromptKeys, a.most_steps);
     };
     uint32_t quota = 0;
@@ -71,16 +85,16 @@ __device__ __forceinline__ bool find_piece(const ChunkArgs &a, uint32_t item, Pi
             look(s0);
             total += (float)tiles * (float)steps;
         }
-        total = __uint_as_float(of_lane(__float_as_uint(sum_to_lane(total)), 63));
+        total = __uint_as_float(of_lane(__float_as_uint(over_lanes(total, 0.0f, Add{})), 63));
         // (above the quotient, whatever the sum's rounding: see chunk_split)
         quota = (uint32_t)fminf(total * a.by_parts * (1.0f + 0x1p-18f), 4.0e9f) + 1;
-    } else if (a.n_seqs > 64) {
+    } else if (kWaves == 4 && a.n_seqs > 64) {
         uint32_t tile;
         const uint32_t s = sequence_of_slot(a.q_starts, a.n_seqs, item, a.group, 7, &tile);
         const int32_t from = a.q_starts[s], to = a.q_starts[s + 1];
         if (from < 0 || to < from || (uint32_t)to > a.n_q) return false;
         const uint32_t n_rows = (uint32_t)(to - from) * a.group;
-        if (tile > n_rows / kPromptTile || tile * kPromptTile >= n_rows) return false;
+        if (tile > n_rows / kTile || tile * kTile >= n_rows) return false;
         p->seq = s, p->q0 = from, p->n_q = to - from;
         p->n_k = (uint32_t)min((int64_t)max(a.lens[s], 0), (int64_t)a.t.width << a.c.shift);
         p->tile = tile, p->part = 0, p->parts = 1, p->per = ~0u, p->place = 0;
@@ -89,11 +103,12 @@ __device__ __forceinline__ bool find_piece(const ChunkArgs &a, uint32_t item, Pi
     uint32_t items_before = 0, places_before = 0;
     for (uint32_t s0 = 0; s0 < a.n_seqs; s0 += 64) {
         if (!kSplit || a.n_seqs > 64 || s0 == 0) look(s0);
-        const uint32_t parts = kSplit ? max(1u, min((steps + quota / 2) / quota, steps >> a.least_shift)) : 1;
+        uint32_t parts = kSplit ? max(1u, min((steps + quota / 2) / quota, steps >> a.least_shift)) : 1;
+        if (kSplit && kWaves == 8) parts = parts_of_one(a, of_lane(tiles, 0), of_lane(steps, 0), parts);
         const uint32_t places = parts > 1 ? tiles * parts : 0, items = kJoin ? (parts > 1 ? tiles : 0) : tiles * parts;
-        const uint32_t items_to = sum_to_lane(items), places_to = kSplit ? sum_to_lane(places) : 0;
+        const uint32_t items_to = over_lanes(items, 0u, Add{}), places_to = kSplit ? over_lanes(places, 0u, Add{}) : 0;
         uint32_t before = items_before + items_to - items;
-        if (kSplit && !kJoin && a.n_seqs <= 64) {
+        if (kWaves == 4 && kSplit && !kJoin && a.n_seqs <= 64) {
             // the sequences with the longest parts first: one of them at the end
             // would keep the others' compute units waiting
             const uint32_t rank = (steps + parts - 1) / parts << 6 | lane;
@@ -141,10 +156,10 @@ struct Steps {
     __device__ __forceinline__ uint32_t key(uint32_t step) const { return (step < sinks ? step : step + skipped) * kPromptKeys; }
 };
 
-__device__ __forceinline__ Steps steps_of(const ChunkArgs &a, const Piece &p) {
-    const uint32_t row0 = p.tile * kPromptTile, n_rows = p.n_q * a.group;
+__device__ __forceinline__ Steps steps_of(const ChunkArgs &a, const Piece &p, uint32_t tile_rows) {
+    const uint32_t row0 = p.tile * tile_rows, n_rows = p.n_q * a.group;
     const Seen first = seen_by(a, over_group(a, row0), p.n_q, p.n_k);
-    const uint32_t end = seen_by(a, over_group(a, min(row0 + kPromptTile, n_rows) - 1), p.n_q, p.n_k).end;
+    const uint32_t end = seen_by(a, over_group(a, min(row0 + tile_rows, n_rows) - 1), p.n_q, p.n_k).end;
     Steps s;
     s.sinks = min((a.sinks + kPromptKeys - 1) / kPromptKeys, first.begin / kPromptKeys);
     s.skipped = first.begin / kPromptKeys - s.sinks;
@@ -182,6 +197,7 @@ struct Entries {
 template <int D, bool kInt8, class Area>
 __device__ __forceinline__ void attend_single(const ChunkArgs &a, const Piece &p, const Steps &steps, uint32_t step_begin, uint32_t step_end, bool whole,
                                               uint32_t kv_head, uint32_t wave, const Area &area, float (*ml)[2][16]) {
+    constexpr uint32_t kWaves = 4, kThreads = 64 * kWaves;
     constexpr int kRow = kInt8 ? D : 2 * D;            // bytes of a stored row
     constexpr int kChunks = kRow / 16;                 // 16-byte chunks of it
     constexpr int kLoads = kTokenKeys * kChunks / 64;  // chunks a lane loads of 32 K rows, and of V rows
@@ -352,11 +368,12 @@ __device__ __forceinline__ void attend_single(const ChunkArgs &a, const Piece &p
     }
 }
 
-template <int D, bool kInt8, bool kSplit>
-__global__ __launch_bounds__(kThreads, 2) void attend_chunk_kernel(ChunkArgs a) {
+template <int D, bool kInt8, bool kSplit, uint32_t kWaves>
+__global__ __launch_bounds__(64 * kWaves, 2) void attend_chunk_kernel(ChunkArgs a) {
+    constexpr uint32_t kThreads = 64 * kWaves, kTile = kWaves * kWaveRows;
     constexpr int kChunks = D / 8;                           // 16-byte chunks of a row of words
     constexpr int kLoads = kPromptKeys * kChunks / kThreads; // chunks of words a thread stages
-    constexpr int kCodeLoads = kLoads / 2;                   // chunks of codes
+    constexpr int kCodeLoads = (kLoads + 1) / 2;             // chunks of codes
     constexpr int kDTiles = D / 32;
     constexpr int kDSteps = D / 16;
     __shared__ __attribute__((aligned(16))) uint8_t kt0[kPromptKeys * D * 2], kt1[kPromptKeys * D * 2];
@@ -370,10 +387,10 @@ __global__ __launch_bounds__(kThreads, 2) void attend_chunk_kernel(ChunkArgs a) 
     // so that the tiles of one meet in one L2)
     const uint32_t kv_head = blockIdx.x % a.c.kv_heads;
     Piece p;
-    if (!find_piece<kSplit, false>(a, blockIdx.x / a.c.kv_heads, &p)) return;
+    if (!find_piece<kWaves, kSplit, false>(a, blockIdx.x / a.c.kv_heads, &p)) return;
     const uint32_t n_q = p.n_q, n_k = p.n_k, n_rows = n_q * a.group;
-    const uint32_t row0 = p.tile * kPromptTile;
-    const Steps steps = steps_of(a, p);
+    const uint32_t row0 = p.tile * kTile;
+    const Steps steps = steps_of(a, p, kTile);
     uint32_t step_begin = 0, step_end = steps.n;
     bool whole = true;
     if (kSplit) {
@@ -383,11 +400,13 @@ __global__ __launch_bounds__(kThreads, 2) void attend_chunk_kernel(ChunkArgs a) 
         whole = steps.n <= p.per;
     }
 
-    if (n_q == 1 && a.group <= 16) {
-        __shared__ float ml[kWaves][2][16];
-        const auto area = [&](uint32_t w) { return w == 0 ? kt0 : w == 1 ? kt1 : w == 2 ? vt0 : vt1; };
-        attend_single<D, kInt8>(a, p, steps, step_begin, step_end, whole, kv_head, wave, area, ml);
-        return;
+    if constexpr (kWaves == 4) {
+        if (n_q == 1 && a.group <= 16) {
+            __shared__ float ml[kWaves][2][16];
+            const auto area = [&](uint32_t w) { return w == 0 ? kt0 : w == 1 ? kt1 : w == 2 ? vt0 : vt1; };
+            attend_single<D, kInt8>(a, p, steps, step_begin, step_end, whole, kv_head, wave, area, ml);
+            return;
+        }
     }
 
     const uint32_t wave_first = row0 + wave * kWaveRows, row = wave_first + col;
@@ -435,7 +454,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_chunk_kernel(ChunkArgs a) 
         const uint32_t left = n_k - key0;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            const uint64_t at = (uint64_t)row_of(key0 + i * kRowsALoad + (D == 64 ? 16 * (wave >> 1) : 0)) * (2 * D);
+            const uint64_t at = (uint64_t)row_of(key0 + i * kRowsALoad + (kRowsALoad > 16 ? wave * (64 / kChunks) & ~15u : 0)) * (2 * D);
             const __amdgpu_buffer_rsrc_t kr = __builtin_amdgcn_make_buffer_rsrc((void *)(a.c.k + at), 0, kOutOfRange, 0x00020000);
             const __amdgpu_buffer_rsrc_t vr = __builtin_amdgcn_make_buffer_rsrc((void *)(a.c.v + at), 0, kOutOfRange, 0x00020000);
             const bool in = tile_row + i * kRowsALoad < left;
@@ -454,11 +473,13 @@ __global__ __launch_bounds__(kThreads, 2) void attend_chunk_kernel(ChunkArgs a) 
     // masked scores and weights of 0 do not look at the scales.
     constexpr uint32_t kCodeChunks = D / 16, kCodeRows = kThreads / kCodeChunks;
     const uint32_t code_row = threadIdx.x / kCodeChunks, code_chunk = threadIdx.x % kCodeChunks;
+    const bool codes_here = kCodeRows <= kPromptKeys || wave < kWaves / 2;      // (eight waves, heads of 64: half of them have none)
     u32x4 kw[kCodeLoads], vw[kCodeLoads];
     float scale_w;
     const auto load_codes = [&](uint32_t key0) {
 #pragma unroll
         for (int i = 0; i < kCodeLoads; ++i) {
+            if (!codes_here) break;
             // (a wave's rows: 8 or 16 neighbours)
             const uint32_t first = key0 + i * kCodeRows + wave * (64 / kCodeChunks);
             const uint64_t at = ((uint64_t)row_of(first & ~15u) + (first & 15)) * D;
@@ -466,7 +487,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_chunk_kernel(ChunkArgs a) 
             kw[i] = *reinterpret_cast<const u32x4 *>(a.c.k + at + from);
             vw[i] = *reinterpret_cast<const u32x4 *>(a.c.v + at + from);
         }
-        // (16 lanes share a page's row; waves 2 and 3 repeat 0 and 1)
+        // (16 lanes share a page's row; the waves from 2 on repeat 0 and 1)
         uint32_t r = row_of(key0);
 #pragma unroll
         for (int g = 1; g < 4; ++g) {
@@ -478,6 +499,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_chunk_kernel(ChunkArgs a) 
     const auto store_codes = [&](uint8_t *kt, uint8_t *vt, float *sc) {
 #pragma unroll
         for (int i = 0; i < kCodeLoads; ++i) {
+            if (!codes_here) break;
             const uint32_t r = code_row + i * kCodeRows;
             *reinterpret_cast<u32x4 *>(kt + k_at<D>(r, 2 * code_chunk)) = bf16_of_bytes8(u32x2{kw[i].x, kw[i].y});
             *reinterpret_cast<u32x4 *>(kt + k_at<D>(r, 2 * code_chunk + 1)) = bf16_of_bytes8(u32x2{kw[i].z, kw[i].w});
@@ -704,16 +726,16 @@ __global__ __launch_bounds__(kThreads, 2) void attend_chunk_kernel(ChunkArgs a) 
 // out = sum_a w_a o_a / sum_a w_a l_a with w_a = 2^(m_a - max m), the maximum
 // taken as the parts come.  A wave takes 16 columns, so that few tiles are many
 // waves' work and the parts of most are all in flight at once.
-template <int D>
+template <int D, uint32_t kWaves>
 __global__ __launch_bounds__(64 * D / 16) void join_chunk_kernel(ChunkArgs a) {
     constexpr int kDTiles = D / 32;
     constexpr int kBatch = 8;       // parts in flight
     const uint32_t lane = threadIdx.x & 63u, i = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t col = lane & 31u, half = lane >> 5, kv_head = blockIdx.x % a.c.kv_heads;
     Piece p;
-    if (!find_piece<true, true>(a, blockIdx.x / a.c.kv_heads, &p)) return;
-    const uint32_t first = p.tile * kPromptTile + blockIdx.y * kWaveRows, row = first + col, n_rows = p.n_q * a.group;
-    const uint32_t n_steps = steps_of(a, p).n;
+    if (!find_piece<kWaves, true, true>(a, blockIdx.x / a.c.kv_heads, &p)) return;
+    const uint32_t first = (p.tile * kWaves + blockIdx.y) * kWaveRows, row = first + col, n_rows = p.n_q * a.group;
+    const uint32_t n_steps = steps_of(a, p, kWaves * kWaveRows).n;
     if (first >= n_rows || n_steps <= p.per) return;
     const uint32_t parts = (n_steps + p.per - 1) / p.per;
     const uint64_t at = ((uint64_t)p.place * a.c.kv_heads + kv_head) * kWaves + blockIdx.y, next_part = (uint64_t)a.c.kv_heads * kWaves;
@@ -756,25 +778,30 @@ __global__ __launch_bounds__(64 * D / 16) void join_chunk_kernel(ChunkArgs a) {
     store_16(o[0] * inv, o[1] * inv, a.out.data + (int64_t)(p.q0 + query) * a.out.row + head * a.out.head + 16 * i, half, row < n_rows);
 }
 
-template <int D, bool kInt8>
+template <int D, bool kInt8, uint32_t kWaves>
 auto kernel_of(bool split) {
-    return split ? attend_chunk_kernel<D, kInt8, true> : attend_chunk_kernel<D, kInt8, false>;
+    return split ? attend_chunk_kernel<D, kInt8, true, kWaves> : attend_chunk_kernel<D, kInt8, false, kWaves>;
+}
+
+template <uint32_t kWaves>
+hipError_t launch(const ChunkArgs &a, uint32_t head_dim, bool int8, hipStream_t stream) {
+    const bool split = a.places != 0;
+    const auto kernel = head_dim == 64 ? (int8 ? kernel_of<64, true, kWaves>(split) : kernel_of<64, false, kWaves>(split))
+                                       : (int8 ? kernel_of<128, true, kWaves>(split) : kernel_of<128, false, kWaves>(split));
+    hipLaunchKernelGGL(kernel, dim3((a.tile_slots + a.places) * a.c.kv_heads), dim3(64 * kWaves), 0, stream, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !split) return e;
+    // (a split tile has two parts at least)
+    const uint32_t tiles = a.places / 2 < a.tile_slots ? a.places / 2 : a.tile_slots;
+    hipLaunchKernelGGL((head_dim == 64 ? join_chunk_kernel<64, kWaves> : join_chunk_kernel<128, kWaves>), dim3(tiles * a.c.kv_heads, kWaves),
+                       dim3(4 * head_dim), 0, stream, a);
+    return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_attend_chunk(const ChunkArgs &a, uint32_t head_dim, bool int8, hipStream_t stream) {
-    const bool split = a.places != 0;
-    const auto kernel = head_dim == 64 ? (int8 ? kernel_of<64, true>(split) : kernel_of<64, false>(split))
-                                       : (int8 ? kernel_of<128, true>(split) : kernel_of<128, false>(split));
-    hipLaunchKernelGGL(kernel, dim3((a.tile_slots + a.places) * a.c.kv_heads), dim3(kThreads), 0, stream, a);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !split) return e;
-    // (a split tile has two parts at least)
-    const uint32_t tiles = a.places / 2 < a.tile_slots ? a.places / 2 : a.tile_slots;
-    hipLaunchKernelGGL(head_dim == 64 ? join_chunk_kernel<64> : join_chunk_kernel<128>, dim3(tiles * a.c.kv_heads, kWaves), dim3(4 * head_dim), 0,
-                       stream, a);
-    return hipGetLastError();
+    return a.tile_rows == 8 * kWaveRows ? launch<8>(a, head_dim, int8, stream) : launch<4>(a, head_dim, int8, stream);
 }
 
 }  // namespace df11

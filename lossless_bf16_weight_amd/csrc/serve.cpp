@@ -286,31 +286,42 @@ df11_status check_prompt_sizes(const df11_attend_prompt_args &a) {
 // on 4256 keys 45 us and 38, four pieces on 8700 to 5000 keys 123 us and 131.)
 // Sequences of many are taken whole: each workgroup would read all their
 // lengths.
+//
+// From 2048 rows on the tiles of a single sequence have 256 rows and eight
+// waves, one workgroup for each compute unit, which read keys and values half as
+// often (2048 queries on 32,049 keys 936 us, with 128 rows 993; in 8 bits, where
+// codes are converted half as often too, 1090 and 1187; 256 on 4256 39 and 36);
+// and as they are equal, the workgroups choose the parts that end soonest, among
+// up to three times as many as run at a time.  Of several sequences the larger
+// tiles are harder to level out (16 prompts of up to 1024 tokens 88 us and 83, 64
+// of up to 256 61 and 55).
 struct ChunkSplit {
-    uint32_t most_steps, parts, places, least_shift;
+    uint32_t most_steps, parts, places, least_shift, tile_rows;
 };
 
 constexpr uint32_t kChunkMostPlanned = 512;     // sequences
 
-uint64_t chunk_tile_slots(const df11_attend_chunk_args &a) { return a.n_q * (a.n_heads / a.cache.n_kv_heads) / kPromptTile + a.n_seqs; }
+uint32_t chunk_tile_rows(const df11_attend_chunk_args &a) { return a.n_seqs == 1 && a.n_q * (a.n_heads / a.cache.n_kv_heads) >= 2048 ? 256 : 128; }
+
+uint64_t chunk_tile_slots(const df11_attend_chunk_args &a) { return a.n_q * (a.n_heads / a.cache.n_kv_heads) / chunk_tile_rows(a) + a.n_seqs; }
 
 ChunkSplit chunk_split(const df11_attend_chunk_args &a, int dev) {
-    ChunkSplit s{~0u, 0, 0, 2};
+    ChunkSplit s{~0u, 0, 0, 2, chunk_tile_rows(a)};
     const uint64_t group = a.n_heads / a.cache.n_kv_heads, positions = (uint64_t)a.table.width * a.cache.page_size;
-    // (a tile's queries are (kPromptTile - 1) / group + 2 at most, the windows of n of
+    // (a tile's queries are (tile_rows - 1) / group + 2 at most, the windows of n of
     // them w + n - 1 keys, which lie in so many steps)
     const Window w = window_of(a.window, a.sinks, positions);
-    if (w.keys) s.most_steps = (uint32_t)((w.keys + (kPromptTile - 1) / group + 1 + 2 * (kPromptKeys - 1)) / kPromptKeys + ceil_div(w.sinks, kPromptKeys));
+    if (w.keys) s.most_steps = (uint32_t)((w.keys + (s.tile_rows - 1) / group + 1 + 2 * (kPromptKeys - 1)) / kPromptKeys + ceil_div(w.sinks, kPromptKeys));
     const uint64_t steps = std::min<uint64_t>(ceil_div(positions, kPromptKeys), s.most_steps);
-    const uint64_t parts = 2 * compute_units(dev) / a.cache.n_kv_heads, of_tile = steps >> s.least_shift;
+    const uint64_t parts = 256 / s.tile_rows * compute_units(dev) / a.cache.n_kv_heads, of_tile = steps >> s.least_shift;
     if (a.n_q == 0 || a.n_seqs == 0 || a.n_seqs > kChunkMostPlanned || parts < 2 || of_tile < 2) return s;
     s.parts = (uint32_t)parts;
-    s.places = (uint32_t)std::min(4 * parts / 3, chunk_tile_slots(a) * of_tile);
+    s.places = (uint32_t)std::min(s.tile_rows == 256 ? 3 * parts : 4 * parts / 3, chunk_tile_slots(a) * of_tile);
     return s;
 }
 
 uint64_t chunk_bytes(const df11_attend_chunk_args &a, const ChunkSplit &s) {
-    return (uint64_t)s.places * a.cache.n_kv_heads * kPromptTile * (a.cache.head_dim + 2) * sizeof(float);
+    return (uint64_t)s.places * a.cache.n_kv_heads * s.tile_rows * (a.cache.head_dim + 2) * sizeof(float);
 }
 
 df11_status check_chunk_sizes(const df11_attend_chunk_args &a) {
@@ -319,7 +330,7 @@ df11_status check_chunk_sizes(const df11_attend_chunk_args &a) {
     const uint32_t kv = a.cache.n_kv_heads;
     if (a.n_heads == 0 || a.n_heads % kv) return report_error(DF11_E_ARG, "%u heads over %u kv heads", a.n_heads, kv);
     if (a.n_q > 0x7FFFFFFFu || a.n_q * (a.n_heads / kv) > 0x7FFFFFFFu || a.n_seqs > kMostGroups ||
-        chunk_tile_slots(a) * kv > kMostGroups - 2048)     // (and the places)
+        chunk_tile_slots(a) * kv > kMostGroups / 2 - 4096)     // (512 threads, and the places)
         return report_error(DF11_E_UNSUPPORTED, "%llu rows of %u heads in %u sequences", (unsigned long long)a.n_q, a.n_heads, a.n_seqs);
     if (a.flags & ~DF11_ATTEND_CAUSAL) return report_error(DF11_E_ARG, "attend_chunk: flags %u", a.flags);
     if (a.window && !(a.flags & DF11_ATTEND_CAUSAL)) return report_error(DF11_E_ARG, "attend_chunk: a window needs DF11_ATTEND_CAUSAL");
@@ -528,12 +539,14 @@ extern "C" df11_status df11_attend_chunk(const df11_attend_chunk_args *a, int hi
     c.sinks = w.sinks;
     divide_by(c.group, &c.group_magic, &c.group_shift);
     c.most_steps = s.most_steps;
+    c.tile_rows = s.tile_rows;
     c.tile_slots = (uint32_t)chunk_tile_slots(*a);
+    c.at_a_time = s.parts;
     c.places = s.places;
     c.least_shift = s.least_shift;
     c.by_parts = s.parts ? 1.0f / s.parts : 0;
     c.part = (float *)a->workspace;
-    c.part_ml = c.part + (uint64_t)s.places * kv * kPromptTile * d;
+    c.part_ml = c.part + (uint64_t)s.places * kv * s.tile_rows * d;
     return launched(launch_attend_chunk(c, d, a->cache.store == DF11_KV_INT8, stream), "attend_chunk");
 }
 

@@ -42,11 +42,21 @@ __device__ __forceinline__ f32x2 with_lane_16(float x) {
     return f32x2{__uint_as_float(r[0]), __uint_as_float(r[1])};
 }
 
-// Sums over the lanes of a wave up to this one; the last lane has the whole sum.
-template <class T>
-__device__ __forceinline__ T sum_to_lane(T x) {
+struct Add {
+    template <class T>
+    __device__ __forceinline__ T operator()(T x, T y) const { return x + y; }
+};
+struct Least {
+    template <class T>
+    __device__ __forceinline__ T operator()(T x, T y) const { return x < y ? x : y; }
+};
+
+// op over the lanes of a wave up to this one; the last lane has all of them.
+template <class T, class Op>
+__device__ __forceinline__ T over_lanes(T x, T identity, Op op) {
     const auto more = [&](auto ctrl, auto rows) {
-        x += __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), decltype(ctrl)::value, decltype(rows)::value, 0xF, false));
+        x = op(x, __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, identity), __builtin_bit_cast(int, x), decltype(ctrl)::value,
+                                                                    decltype(rows)::value, 0xF, false)));
     };
     constexpr std::integral_constant<int, 0xF> all{};
     more(std::integral_constant<int, 0x111>{}, all);      // from 1, 2, 4 and 8 lanes below, in 16

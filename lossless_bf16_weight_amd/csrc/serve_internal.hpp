@@ -98,7 +98,9 @@ struct ChunkArgs {
     uint32_t window, sinks;              // window 0: none
     uint32_t group_magic, group_shift;   // as in PromptArgs
     uint32_t most_steps;                 // of a tile with the window, whatever the length
+    uint32_t tile_rows;                  // 128 or 256
     uint32_t tile_slots;                 // at least as many as tiles
+    uint32_t at_a_time;                  // workgroups of a kv head that run at a time
     uint32_t places, least_shift;        // parts of a kv head's tiles that the workspace holds (0: none are split); log2 of the least steps of one
     float by_parts;                      // 1 / the parts that a kv head's work is divided into
     float *part, *part_ml;               // [place][kv_head][wave][register / 4][lane][4], then [place][kv_head][wave][row][2]

@@ -85,6 +85,33 @@ def test_split(new, lens, window, sinks, int8):
     assert torch.equal(a.view(torch.int16), b.view(torch.int16))
 
 
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("new,lens,window,sinks", [(600, 600, 0, 0), (517, 1100, 0, 0), (1025, 1025, 100, 70), (700, 3000, 900, 3), (520, 250, 0, 0),
+                                                   (512, 9000, 0, 0)])
+def test_one_sequence_of_many_rows(new, lens, window, sinks, int8):
+    """Tiles of 256 rows, whole and in parts."""
+    for i, (h, hk, d, ps) in enumerate([(8, 2, 128, 16), (8, 2, 64, 64), (20, 1, 64, 32), (5, 1, 128, 128)]):
+        log(f"one sequence, {new} of {lens}, window {window} sinks {sinks}, {h}/{hk} heads of {d}, int8 {int8}")
+        c = CU.Cached([lens], hk, d, ps, int8, seed=30 + i)
+        q = CU.rand((new + 1, h, d), 70 + i)
+        need = df11.chunk_workspace(new + 1, 1, h, hk, d, ps, c.pages.shape[1], window, sinks)
+        ws = torch.full((max(need // 4, 1),), float("nan"), device=DEV)
+        _check(c, q, [new], (new, lens, i), window=window, sinks=sinks, workspace=ws)
+        if not window:
+            _check(c, q, [new], (new, lens, i, "not causal"), causal=False)
+
+
+@pytest.mark.parametrize("new,lens", [(600, 700), (520, 4000)])
+def test_odd_values_in_many_rows(new, lens):
+    c = CU.Cached([lens], 2, 128, 16, False, seed=40)
+    for key, what in ((lens - 150, float("inf")), (lens - 3, float("nan")), (lens - 290, -float("inf"))):
+        c.cache.v[int(c.table[0, key // 16]), 0, key % 16, 40] = what
+    c.cache.k[int(c.table[0, (lens - 20) // 16]), 1, (lens - 20) % 16, 3] = float("nan")
+    q = CU.rand((new, 8, 128), 71)
+    _check(c, q, [new], (new, lens))
+    _check(c, q, [new], (new, lens, "window"), window=100, sinks=5)
+
+
 @pytest.mark.parametrize("n_seqs", [17, 64, 65, 200, 513, 700])
 def test_many_sequences(n_seqs):
     log(f"{n_seqs} sequences")

@@ -29,15 +29,15 @@ def test_waves_a_simd(compiled):
 
 
 def test_products_do_not_wait_for_memory(compiled):
-    """The next step's loads stay in flight: no block of matrix instructions
-    waits for vector memory (but the careful pass, which loads in it)."""
+    """The next step's loads stay in flight: no block of the tiles' matrix
+    instructions waits for vector memory (but the careful pass, which loads in it)."""
     asm, _ = compiled["attend_chunk.hip"]
     bodies = re.findall(r"^(\S*attend_chunk_kernel\S*):(.*?)^\s*\.section", asm, re.S | re.M)
-    assert len(bodies) == 8
+    assert len(bodies) == 16
     for name, body in bodies:
         words = "ELb0E" in name.split("attend_chunk_kernel")[1][:10]
         assert not words or ("buffer_load_dwordx4" in body and " lds" in body), name
-        blocks = [b for b in re.split(r"^\.LBB\S+:", body, flags=re.M) if b.count("v_mfma") >= 4 and not re.search(r"buffer_load[^\n]* lds", b)]
+        blocks = [b for b in re.split(r"^\.LBB\S+:", body, flags=re.M) if b.count("v_mfma_f32_32x32x16") >= 4 and not re.search(r"buffer_load[^\n]* lds", b)]
         assert len(blocks) >= 4, name
         for b in blocks:
             assert not re.search(r"s_waitcnt [^\n]*vmcnt", b), name

@@ -135,6 +135,8 @@ def test_workspaces():
     most = 2 * 256 // 8 * 4 // 3 * 8 * tile
     assert need and need % (8 * tile) == 0 and need <= most
     assert df11.chunk_workspace(64, 1, 32, 8, 128, 16, 1 << 20) == most
+    assert df11.chunk_workspace(640, 2, 32, 8, 128, 16, 1 << 20) == most
+    assert df11.chunk_workspace(640, 1, 32, 8, 128, 16, 1 << 20) == 3 * 256 * 2 * tile       # (tiles of 256 rows)
     assert df11.chunk_workspace(64, 1, 32, 8, 128, 16, 1 << 20, 100, 4) == 0       # (a window of few steps)
     good = dict(GOOD["df11_attend_chunk"], **{"table.width": 4096, "window": 0})
     need = df11.chunk_workspace(5, 2, 4, 2, 128, 16, 4096)
