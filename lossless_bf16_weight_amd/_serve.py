@@ -159,14 +159,25 @@ def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tens
     _launch(lib().df11_kv_write, _WRITE.pack(*c, *kr, *vr, _index(slots, "slots", dev, I64, n), n), dev, stream)
 
 
-class Rotation(NamedTuple):
+class Rotation:
     """The position rotation of a head's first 2 * len(turns) elements (made by
-    rotation()): frequencies as fractions of a turn a position, times 2^64."""
-    turns: torch.Tensor                    # int64 [pairs]
-    axes: Optional[torch.Tensor] = None    # uint8 [pairs]
-    n_axes: int = 1
-    interleaved: bool = False
-    factor: float = 1.0
+    rotation()).  turns: int64 [pairs], frequencies as fractions of a turn a
+    position, times 2^64; axes: uint8 [pairs], the axis of each pair, or None;
+    n_axes: how many a position has.  What it holds is checked here, once, and
+    does not change."""
+    __slots__ = ("turns", "axes", "n_axes", "interleaved", "factor", "_device", "_fields")
+
+    def __init__(self, turns: torch.Tensor, axes: Optional[torch.Tensor] = None, n_axes: int = 1, interleaved: bool = False, factor: float = 1.0):
+        if turns.dtype is not I64 or turns.dim() != 1 or not turns.is_contiguous():
+            raise ValueError("rotation: contiguous int64 turns [pairs] are needed")
+        if axes is not None and (axes.dtype is not torch.uint8 or axes.shape != turns.shape or axes.device != turns.device or not axes.is_contiguous()):
+            raise ValueError("rotation: axes must be contiguous uint8 [pairs] on the turns' device")
+        fields = (turns.data_ptr(), 0 if axes is None else axes.data_ptr()), (turns.shape[0], ROTATE_NEIGHBOURS if interleaved else 0, float(factor))
+        for name, value in zip(self.__slots__, (turns, axes, int(n_axes), bool(interleaved), float(factor), turns.get_device(), fields)):
+            object.__setattr__(self, name, value)
+
+    def __setattr__(self, name, value):
+        raise AttributeError("a Rotation does not change")
 
 
 def rotation(rotary_dim: int, base: float = 10000.0, freqs=None, axes=None, interleaved: bool = False, factor: float = 1.0,
@@ -195,18 +206,12 @@ def rotation(rotary_dim: int, base: float = 10000.0, freqs=None, axes=None, inte
 
 
 def _rotation_fields(r: Optional[Rotation], positions, dev: int, n: int):
-    if r is None or r.turns.shape[0] == 0:
+    if r is None or r._fields[1][0] == 0:
         return 0, 0, 0, 0, 0, 0, 0, 0.0
-    turns, axes, n_axes, interleaved, factor = r
-    pairs = turns.shape[0]
-    if turns.dtype is not I64 or turns.dim() != 1 or turns.get_device() != dev or not turns.is_contiguous():
-        raise ValueError(f"rotation: contiguous int64 turns [pairs] on cuda:{dev} are needed")
-    at = 0
-    if axes is not None:
-        if axes.dtype is not torch.uint8 or axes.shape != turns.shape or axes.get_device() != dev or not axes.is_contiguous():
-            raise ValueError(f"rotation: contiguous uint8 axes [{pairs}] on cuda:{dev} are needed")
-        at = axes.data_ptr()
-    p = positions
+    (turns, axes), (pairs, flags, factor) = r._fields
+    p, n_axes = positions, r.n_axes
+    if r._device != dev:
+        raise ValueError(f"rotation: on cuda:{r._device}, not cuda:{dev}")
     if not isinstance(p, torch.Tensor) or p.dtype is not I32 or p.get_device() != dev or p.dim() not in (1, 2) or p.shape[0] != n:
         raise ValueError(f"positions: an int32 tensor [{n}] or [{n}, axes] on cuda:{dev} is needed")
     if p.dim() == 2:
@@ -215,7 +220,7 @@ def _rotation_fields(r: Optional[Rotation], positions, dev: int, n: int):
         n_axes = p.shape[1]
     elif n_axes > 1:
         raise ValueError(f"positions: [{n}, {n_axes}] is needed")
-    return turns.data_ptr(), at, p.data_ptr(), p.stride(0) if n > 1 else 0, pairs, n_axes, ROTATE_NEIGHBOURS if interleaved else 0, factor
+    return turns, axes, p.data_ptr(), p.stride(0) if n > 1 else 0, pairs, n_axes, flags, factor
 
 
 def _weight(w, what: str, dev: int, d: int):

@@ -1,9 +1,10 @@
 """A decoder stack served from compressed weights: the layer loop decodes
 layer l + 1 while layer l computes, with a paged key-value cache and the
 attention operators beside the products (a small example of the parts
-together; norms, rotary positions and the activation are plain torch).
+together; the norms of hidden states and the activation are plain torch, and
+so are rotary positions where the stack is given no rotation).
 
-    python -m lossless_bf16_weight_amd.serve [--layers N] [--prompts 500,37,1] [--tokens N] [--int8]
+    python -m lossless_bf16_weight_amd.serve [--layers N] [--prompts 500,37,1] [--tokens N] [--int8] [--window N] [--sinks N]
 
 runs Llama-3-8B-shaped layers of synthetic weights: a prompt of each sequence,
 a second piece behind it, then new tokens one at a time, and prints what each
@@ -12,14 +13,15 @@ from __future__ import annotations
 
 import argparse
 import time
-from typing import List, Sequence
+from typing import List, Optional, Sequence, Tuple
 
 import torch
 import torch.nn.functional as F
 
 from . import workloads
 from ._lib import Plan, encode
-from ._serve import attend_prompt, attend_token, kv_cache, kv_read, kv_write
+from ._serve import (Rotation, attend_chunk, attend_prompt, attend_token, kv_append, kv_cache, kv_read, kv_write,
+                     rotation as make_rotation)
 from .jit import LayerLoop
 
 
@@ -40,10 +42,22 @@ def norm(x: torch.Tensor) -> torch.Tensor:
 class DecoderStack:
     """Layers of the llama8b_block layout (q, k, v, o, gate, up, down) in a
     LayerLoop, with a cache of `n_pages` pages a layer for `n_seqs` sequences.
-    Pages are handed out as sequences grow."""
+    Pages are handed out as sequences grow.
+
+    With a rotation (rotation()), a layer's queries and keys are rotated in the
+    launch that writes keys and values to the cache (kv_append), normed before
+    where head_norms gives each layer's two weights, and prompts attend over the
+    pages (attend_chunk).  A window above 0 lets every token see the last
+    `window` tokens and the first `sinks` alone."""
 
     def __init__(self, loop: LayerLoop, n_heads: int, n_kv_heads: int, head_dim: int, n_seqs: int, n_pages: int,
-                 page_size: int = 64, max_len: int = 8192, int8: bool = False, device: str = "cuda"):
+                 page_size: int = 64, max_len: int = 8192, int8: bool = False, device: str = "cuda", rotation: Optional[Rotation] = None,
+                 head_norms: Optional[Sequence[Tuple[torch.Tensor, torch.Tensor]]] = None, window: int = 0, sinks: int = 0):
+        if head_norms is not None and (rotation is None or len(head_norms) != len(loop)):
+            raise ValueError("head_norms: two weights for each layer, beside a rotation, are needed")
+        if window < 0 or sinks < 0:
+            raise ValueError(f"window {window}, sinks {sinks}: numbers from 0 are needed")
+        self.rotation, self.head_norms, self.window, self.sinks = rotation, head_norms, window, sinks
         self.loop, self.heads, self.kv_heads, self.d, self.page_size = loop, n_heads, n_kv_heads, head_dim, page_size
         self.caches = [kv_cache(n_pages, n_kv_heads, page_size, head_dim, int8=int8, device=device) for _ in range(len(loop))]
         self.pages = torch.zeros(n_seqs, -(-max_len // page_size), dtype=torch.int32, device=device)
@@ -95,14 +109,19 @@ class DecoderStack:
             x = state[0]
             h = norm(x)
             q, k, v = (F.linear(h, w).unflatten(1, (n, self.d)) for w, n in ((wq, self.heads), (wk, self.kv_heads), (wv, self.kv_heads)))
-            q, k = rotary(q, positions), rotary(k, positions)
-            kv_write(self.caches[l], k, v, slots)
+            if self.rotation is None:
+                q, k = rotary(q, positions), rotary(k, positions)
+                kv_write(self.caches[l], k, v, slots)
+            else:
+                q_weight, k_weight = self.head_norms[l] if self.head_norms is not None else (None, None)
+                kv_append(self.caches[l], k, v, at, slots, self.rotation, k_weight=k_weight, q=q, q_out=q, q_weight=q_weight)
             x = x + F.linear(attend(l, q, k, v).flatten(1), wo)
             h = norm(x)
             state[0] = x + F.linear(F.silu(F.linear(h, gate)) * F.linear(h, up), down)
 
         try:
             positions, slots = self._grow(new)
+            at = positions.to(torch.int32)
             self.loop.run(layer)
         except BaseException:
             self.lens, self.free = held
@@ -116,8 +135,13 @@ class DecoderStack:
         after = [a + n for a, n in zip(self.lens, new)]
         cached = any(self.lens)
         q_starts, k_starts = self._starts(new), self._starts(after)
+        lens = torch.tensor(after, dtype=torch.int32, device=self.device)
 
         def attend(l, q, k, v):
+            if self.rotation is not None or self.window:
+                out = torch.empty_like(q)
+                attend_chunk(q, self.caches[l], self.pages, q_starts, lens, out, window=self.window, sinks=self.sinks)
+                return out
             if cached:     # what came before is in the cache
                 k, v = (torch.empty(sum(after), self.kv_heads, self.d, dtype=q.dtype, device=q.device) for _ in range(2))
                 kv_read(self.caches[l], self.pages, k_starts, k, v)
@@ -133,7 +157,10 @@ class DecoderStack:
 
         def attend(l, q, k, v):
             out = torch.empty_like(q)
-            attend_token(q, self.caches[l], self.pages, lens, out)
+            if self.window:
+                attend_token(q, self.caches[l], self.pages, lens, out, window=self.window, sinks=self.sinks)
+            else:
+                attend_token(q, self.caches[l], self.pages, lens, out)
             return out
 
         return self._run(x, [1] * len(self.lens), attend)
@@ -152,11 +179,14 @@ def main() -> None:
     ap.add_argument("--prompts", default="500,37,1")
     ap.add_argument("--tokens", type=int, default=8)
     ap.add_argument("--int8", action="store_true", help="keep the cache in 8 bits")
+    ap.add_argument("--window", type=int, default=0, help="tokens that a token sees back (0: all)")
+    ap.add_argument("--sinks", type=int, default=0, help="first tokens that stay visible beside the window")
     args = ap.parse_args()
     new = [int(n) for n in args.prompts.split(",")]
     loop = compressed_layers([[s.make() for s in workloads.llama8b_block(l)] for l in range(args.layers)])
     most = 2 * max(new) + args.tokens
-    stack = DecoderStack(loop, 32, 8, 128, len(new), n_pages=len(new) * (-(-most // 64)), max_len=most, int8=args.int8)
+    stack = DecoderStack(loop, 32, 8, 128, len(new), n_pages=len(new) * (-(-most // 64)), max_len=most, int8=args.int8,
+                         rotation=make_rotation(128, base=500000.0), window=args.window, sinks=args.sinks)
     gen = torch.Generator(device="cuda").manual_seed(0)
 
     def rows(n):
