@@ -57,7 +57,7 @@ __device__ __forceinline__ Visible visible_of(const TokenArgs &a, uint32_t len) 
 // kOnce: no other workgroup reads the same rows (at most 16 heads share a kv head).
 // kWindow: the keys of a window and its sinks.
 template <int D, bool kInt8, uint32_t kWaves, bool kOnce, bool kWindow>
-__global__ __launch_bounds__(64 * kWaves, 3) void attend_token_kernel(TokenArgs a) {
+__device__ __forceinline__ void attend_part(const TokenArgs &a) {
     constexpr uint32_t kThreads = 64 * kWaves;
     constexpr int kRow = kInt8 ? D : 2 * D;            // bytes of a stored row
     constexpr int kChunks = kRow / 16;                 // 16-byte chunks of it
@@ -277,6 +277,16 @@ __global__ __launch_bounds__(64 * kWaves, 3) void attend_token_kernel(TokenArgs 
     }
 }
 
+template <int D, bool kInt8, uint32_t kWaves, bool kOnce>
+__global__ __launch_bounds__(64 * kWaves, 3) void attend_token_kernel(TokenArgs a) {
+    attend_part<D, kInt8, kWaves, kOnce, false>(a);
+}
+
+template <int D, bool kInt8, uint32_t kWaves, bool kOnce>
+__global__ __launch_bounds__(64 * kWaves, 3) void attend_window_kernel(TokenArgs a) {
+    attend_part<D, kInt8, kWaves, kOnce, true>(a);
+}
+
 // Joins the parts of one query head: out = sum_a w_a o_a / sum_a w_a l_a with
 // w_a = 2^(m_a - max m).
 template <int D, bool kWindow>
@@ -317,10 +327,16 @@ __global__ __launch_bounds__(256) void join_token_kernel(TokenArgs a) {
     }
 }
 
+template <int D, bool kInt8, uint32_t kWaves, bool kOnce, bool kWindow>
+auto kernel_of() {
+    if constexpr (kWindow) return attend_window_kernel<D, kInt8, kWaves, kOnce>;
+    else return attend_token_kernel<D, kInt8, kWaves, kOnce>;
+}
+
 template <uint32_t kWaves, bool kOnce, bool kWindow>
 void launch_as(const TokenArgs &a, uint32_t head_dim, bool int8, dim3 grid, hipStream_t stream) {
-    const auto kernel = head_dim == 64 ? (int8 ? attend_token_kernel<64, true, kWaves, kOnce, kWindow> : attend_token_kernel<64, false, kWaves, kOnce, kWindow>)
-                                       : (int8 ? attend_token_kernel<128, true, kWaves, kOnce, kWindow> : attend_token_kernel<128, false, kWaves, kOnce, kWindow>);
+    const auto kernel = head_dim == 64 ? (int8 ? kernel_of<64, true, kWaves, kOnce, kWindow>() : kernel_of<64, false, kWaves, kOnce, kWindow>())
+                                       : (int8 ? kernel_of<128, true, kWaves, kOnce, kWindow>() : kernel_of<128, false, kWaves, kOnce, kWindow>());
     hipLaunchKernelGGL(kernel, grid, dim3(64 * kWaves), 0, stream, a);
 }
 

@@ -7,12 +7,13 @@ import re
 import pytest
 
 from test_kernel_build import _compile, _remark
+from test_serve_handover import READ, WRITE
 from test_serve_kernel_build import _occupancy
 
 
 @pytest.fixture(scope="module")
 def compiled(tmp_path_factory):
-    return {src: _compile(src, tmp_path_factory.mktemp("asm")) for src in ("heads.hip", "attend_chunk.hip")}
+    return {src: _compile(src, tmp_path_factory.mktemp("asm")) for src in ("heads.hip", "attend_chunk.hip", "attend_token.hip")}
 
 
 @pytest.mark.parametrize("src", ["heads.hip", "attend_chunk.hip"])
@@ -26,6 +27,23 @@ def test_no_scratch_flat_or_packed_arithmetic(src, compiled):
 def test_waves_a_simd(compiled):
     assert all(v >= 4 for v in _occupancy(compiled["heads.hip"][1], "heads_kernel"))
     assert all(v >= 2 for v in _occupancy(compiled["attend_chunk.hip"][1], "attend_chunk_kernel"))
+    assert all(v >= 3 for v in _occupancy(compiled["attend_token.hip"][1], "attend_window_kernel"))
+
+
+def test_writes_and_reads_of_a_wave_s_tile_are_apart(compiled):
+    """As test_serve_handover.py for attend_token: windows, and the chunk's
+    sequences of one token."""
+    found = re.findall(r"^(\S*attend_window_kernel\S*):(.*?)^\s*\.section", compiled["attend_token.hip"][0], re.S | re.M)
+    assert len(found) == 16
+    single = [(n, b) for n, b in re.findall(r"^(\S*attend_chunk_kernel\S*):(.*?)^\s*\.section", compiled["attend_chunk.hip"][0], re.S | re.M) if "Lj4E" in n]
+    assert len(single) == 8
+    for name, body in found + single:
+        parts = re.split(r"^\s*; wave barrier.*$", body, flags=re.M)
+        assert len(parts) >= 5, name
+        parts[4] = re.split(r"^\s*s_barrier", parts[4], flags=re.M)[0]
+        kinds = [(len(re.findall(WRITE, p, re.M)), len(re.findall(READ, p, re.M))) for p in parts[1:5]]
+        (k_written, a), (b, k_read), (v_written, c), (d, v_read) = kinds
+        assert k_written and v_written and k_read and v_read and not (a or b or c or d), (name, kinds)
 
 
 def test_products_do_not_wait_for_memory(compiled):
