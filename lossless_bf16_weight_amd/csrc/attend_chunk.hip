@@ -129,7 +129,8 @@ __device__ __forceinline__ bool find_piece(const ChunkArgs &a, uint32_t item, Pi
             // (the last tiles of a sequence, which see the most keys, come first)
             p->tile = of_lane(tiles, x) - 1 - at;
             p->place = places_before + of_lane(places_to - places, x) + at * p->parts;
-            return true;
+            // (starts that do not ascend may make more of them than there are places)
+            return p->parts == 1 || p->place + p->parts <= a.places;
         }
         items_before += of_lane(items_to, 63);
         places_before += of_lane(places_to, 63);

@@ -129,3 +129,23 @@ def test_scales_that_are_infinite(window):
     want, bound = CU.chunk64(q, c.cache, c.table, new, lens, 0.125, True, window, 0)
     assert torch.equal(torch.isnan(out).cpu(), torch.isnan(want)) and bool(torch.isnan(want).any()) and not bool(torch.isnan(want).all())
     U.within(out, want, bound, window)
+
+
+@pytest.mark.parametrize("n_seqs,width", [(9, 32), (131, 32), (9, 4096)])
+def test_starts_that_do_not_ascend_stay_inside(n_seqs, width):
+    """Sequences over the same rows: more tiles than the rows could hold.  The
+    results are not defined; the memory around workspace and output is."""
+    h, hk, d, n, guard = 8, 2, 64, 100, 1 << 20
+    lens = [width * 16] * n_seqs
+    g = torch.Generator().manual_seed(3)
+    k, v = (torch.randn(8, hk, 16, d, generator=g).to(torch.bfloat16).to(DEV) for _ in range(2))
+    pages = torch.randint(0, 8, (n_seqs, width), generator=g, dtype=torch.int32).to(DEV)
+    starts = torch.tensor([0, n] * ((n_seqs + 1) // 2), dtype=torch.int32, device=DEV)
+    size = df11.chunk_workspace(n, n_seqs, h, hk, d, 16, width)
+    assert size > 0
+    memory = torch.full((size + guard,), 0x5A, dtype=torch.uint8, device=DEV)
+    out = torch.full((n + 64, h, d), 7.0, dtype=torch.bfloat16, device=DEV)
+    for _ in range(2):
+        df11.attend_chunk(CU.rand((n, h, d), 4), df11.KVCache(k, v), pages, starts, torch.tensor(lens, dtype=torch.int32, device=DEV), out[:n], workspace=memory[:size])
+    torch.cuda.synchronize()
+    assert bool((memory[size:] == 0x5A).all()) and bool((out[n:] == 7.0).all())
