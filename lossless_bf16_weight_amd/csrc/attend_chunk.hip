@@ -723,60 +723,69 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_chunk_kernel(ChunkArgs 
     for (int i = 0; i < kDTiles; ++i) store_tile(o[i] * inv, op + 32 * i, half, real);
 }
 
-// Joins the parts of 32 rows (those of wave blockIdx.y of a split tile):
+// Tiles that may be split: of a kv head, each in two parts at least.
+__host__ __device__ __forceinline__ uint32_t split_tiles(const ChunkArgs &a) { return a.places / 2 < a.tile_slots ? a.places / 2 : a.tile_slots; }
+
+// Joins the parts of 32 rows (those of one wave of a split tile) after another:
 // out = sum_a w_a o_a / sum_a w_a l_a with w_a = 2^(m_a - max m), the maximum
 // taken as the parts come.  A wave takes 16 columns, so that few tiles are many
-// waves' work and the parts of most are all in flight at once.
+// waves' work and the parts of most are all in flight at once.  How many tiles
+// are split the host does not know: as many workgroups are launched as run at a
+// time, and end when there are no more (one for each tile that the workspace
+// could hold took 8 to 10 us to find nothing, JOINUS).
 template <int D, uint32_t kWaves>
 __global__ __launch_bounds__(64 * D / 16) void join_chunk_kernel(ChunkArgs a) {
     constexpr int kDTiles = D / 32;
     constexpr int kBatch = 8;       // parts in flight
     const uint32_t lane = threadIdx.x & 63u, i = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const uint32_t col = lane & 31u, half = lane >> 5, kv_head = blockIdx.x % a.c.kv_heads;
-    Piece p;
-    if (!find_piece<kWaves, true, true>(a, blockIdx.x / a.c.kv_heads, &p)) return;
-    const uint32_t first = (p.tile * kWaves + blockIdx.y) * kWaveRows, row = first + col, n_rows = p.n_q * a.group;
-    const uint32_t n_steps = steps_of(a, p, kWaves * kWaveRows).n;
-    if (first >= n_rows || n_steps <= p.per) return;
-    const uint32_t parts = (n_steps + p.per - 1) / p.per;
-    const uint64_t at = ((uint64_t)p.place * a.c.kv_heads + kv_head) * kWaves + blockIdx.y, next_part = (uint64_t)a.c.kv_heads * kWaves;
-    const f32x2 *const ml = reinterpret_cast<const f32x2 *>(a.part_ml) + at * kWaveRows + col;
-    const f32x4 *const part = reinterpret_cast<const f32x4 *>(a.part) + at * (kDTiles * 256) + i * 128 + lane;
-    f32x4 o[2] = {};
-    float l = 0, m = -__builtin_inff();
-    for (uint32_t s = 0; s < parts; s += kBatch) {
-        f32x2 stat[kBatch];
-        f32x4 v[kBatch][2];
+    const uint32_t col = lane & 31u, half = lane >> 5;
+    for (uint32_t n = blockIdx.x; n < split_tiles(a) * a.c.kv_heads * kWaves; n += gridDim.x) {
+        const uint32_t kv_head = n % a.c.kv_heads, wave = n / a.c.kv_heads % kWaves;
+        Piece p;
+        if (!find_piece<kWaves, true, true>(a, n / a.c.kv_heads / kWaves, &p)) return;
+        const uint32_t first = (p.tile * kWaves + wave) * kWaveRows, row = first + col, n_rows = p.n_q * a.group;
+        const uint32_t n_steps = steps_of(a, p, kWaves * kWaveRows).n;
+        if (first >= n_rows || n_steps <= p.per) continue;
+        const uint32_t parts = (n_steps + p.per - 1) / p.per;
+        const uint64_t at = ((uint64_t)p.place * a.c.kv_heads + kv_head) * kWaves + wave, next_part = (uint64_t)a.c.kv_heads * kWaves;
+        const f32x2 *const ml = reinterpret_cast<const f32x2 *>(a.part_ml) + at * kWaveRows + col;
+        const f32x4 *const part = reinterpret_cast<const f32x4 *>(a.part) + at * (kDTiles * 256) + i * 128 + lane;
+        f32x4 o[2] = {};
+        float l = 0, m = -__builtin_inff();
+        for (uint32_t s = 0; s < parts; s += kBatch) {
+            f32x2 stat[kBatch];
+            f32x4 v[kBatch][2];
 #pragma unroll
-        for (int x = 0; x < kBatch; ++x) {
-            if (s + x >= parts) break;      // (a part past the last was not written)
-            stat[x] = ml[(s + x) * next_part * kWaveRows];
+            for (int x = 0; x < kBatch; ++x) {
+                if (s + x >= parts) break;      // (a part past the last was not written)
+                stat[x] = ml[(s + x) * next_part * kWaveRows];
 #pragma unroll
-            for (int g = 0; g < 2; ++g) v[x][g] = part[(s + x) * next_part * (kDTiles * 256) + g * 64];
+                for (int g = 0; g < 2; ++g) v[x][g] = part[(s + x) * next_part * (kDTiles * 256) + g * 64];
+            }
+            float next = m;
+#pragma unroll
+            for (int x = 0; x < kBatch; ++x) {
+                if (s + x >= parts) break;
+                next = fmaxf(next, stat[x].x);
+            }
+            const float base = next == -__builtin_inff() ? 0.0f : next, keep = exp2_fast(m - base);
+            m = next;
+            l *= keep;
+            o[0] *= keep;
+            o[1] *= keep;
+#pragma unroll
+            for (int x = 0; x < kBatch; ++x) {
+                if (s + x >= parts) break;
+                const float w = exp2_fast(stat[x].x - base);
+                l += w * stat[x].y;
+                o[0] += w * v[x][0];
+                o[1] += w * v[x][1];
+            }
         }
-        float next = m;
-#pragma unroll
-        for (int x = 0; x < kBatch; ++x) {
-            if (s + x >= parts) break;
-            next = fmaxf(next, stat[x].x);
-        }
-        const float base = next == -__builtin_inff() ? 0.0f : next, keep = exp2_fast(m - base);
-        m = next;
-        l *= keep;
-        o[0] *= keep;
-        o[1] *= keep;
-#pragma unroll
-        for (int x = 0; x < kBatch; ++x) {
-            if (s + x >= parts) break;
-            const float w = exp2_fast(stat[x].x - base);
-            l += w * stat[x].y;
-            o[0] += w * v[x][0];
-            o[1] += w * v[x][1];
-        }
+        const uint32_t query = over_group(a, row), head = kv_head * a.group + row - query * a.group;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        store_16(o[0] * inv, o[1] * inv, a.out.data + (int64_t)(p.q0 + query) * a.out.row + head * a.out.head + 16 * i, half, row < n_rows);
     }
-    const uint32_t query = over_group(a, row), head = kv_head * a.group + row - query * a.group;
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    store_16(o[0] * inv, o[1] * inv, a.out.data + (int64_t)(p.q0 + query) * a.out.row + head * a.out.head + 16 * i, half, row < n_rows);
 }
 
 template <int D, bool kInt8, uint32_t kWaves>
@@ -789,12 +798,14 @@ hipError_t launch(const ChunkArgs &a, uint32_t head_dim, bool int8, hipStream_t 
     const bool split = a.places != 0;
     const auto kernel = head_dim == 64 ? (int8 ? kernel_of<64, true, kWaves>(split) : kernel_of<64, false, kWaves>(split))
                                        : (int8 ? kernel_of<128, true, kWaves>(split) : kernel_of<128, false, kWaves>(split));
-    hipLaunchKernelGGL(kernel, dim3((a.tile_slots + a.places) * a.c.kv_heads), dim3(64 * kWaves), 0, stream, a);
+    // (a single sequence is whole, or all of its parts have places)
+    const uint32_t items = kWaves == 4 ? a.tile_slots + a.places : a.tile_slots > a.places ? a.tile_slots : a.places;
+    hipLaunchKernelGGL(kernel, dim3(items * a.c.kv_heads), dim3(64 * kWaves), 0, stream, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !split) return e;
-    // (a split tile has two parts at least)
-    const uint32_t tiles = a.places / 2 < a.tile_slots ? a.places / 2 : a.tile_slots;
-    hipLaunchKernelGGL((head_dim == 64 ? join_chunk_kernel<64, kWaves> : join_chunk_kernel<128, kWaves>), dim3(tiles * a.c.kv_heads, kWaves),
+    // (2048 threads for each compute unit)
+    const uint32_t rows_32 = split_tiles(a) * a.c.kv_heads * kWaves, at_a_time = a.at_a_time * a.c.kv_heads * kWaves / 2 * (128 / head_dim);
+    hipLaunchKernelGGL((head_dim == 64 ? join_chunk_kernel<64, kWaves> : join_chunk_kernel<128, kWaves>), dim3(rows_32 < at_a_time ? rows_32 : at_a_time),
                        dim3(4 * head_dim), 0, stream, a);
     return hipGetLastError();
 }
