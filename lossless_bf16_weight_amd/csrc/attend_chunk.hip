@@ -47,16 +47,21 @@ struct Piece {
 
 __device__ __forceinline__ uint32_t of_lane(uint32_t x, uint32_t lane) { return __builtin_amdgcn_readlane(x, lane); }
 
-// Parts of the tiles of a single sequence of many rows: as they are equal, the
-// number that ends soonest, in steps of a workgroup among as many as run at a
-// time.  A part has two steps' time beside its own, and what is written and
-// joined of it.  (Few tiles have many parts, where rounding is harmless.)
-__device__ __forceinline__ uint32_t parts_of_one(const ChunkArgs &a, uint32_t tiles, uint32_t steps, uint32_t otherwise) {
+// Parts of the longest tiles of a single sequence of many rows: the number that
+// ends soonest, in steps of a workgroup among as many as run at a time.  A part
+// has two steps' time beside its own, and what is written and joined of it.
+// Tiles behind a long prefix are equal, and their parts take whole rounds;
+// where the first tiles are short (`least` steps, of `steps`), these even the
+// end out.  (Few tiles have many parts, where rounding is harmless.)
+__device__ __forceinline__ uint32_t parts_of_one(const ChunkArgs &a, uint32_t tiles, uint32_t least, uint32_t steps, uint32_t otherwise) {
     if (tiles * 8 < a.at_a_time) return otherwise;
-    const uint32_t lane = threadIdx.x & 63u, parts = lane + 1, items = tiles * parts, rest = items % a.at_a_time;
-    float cost = (float)(items / a.at_a_time + (rest != 0)) * (float)((steps + parts - 1) / parts + (parts > 1 ? 2 : 1));
-    if (parts > 1) cost += 2.0f + 0.014f * (float)(items * a.c.kv_heads);
-    const bool possible = parts == 1 || (parts <= steps >> a.least_shift && items <= a.places);
+    const uint32_t lane = threadIdx.x & 63u, parts = lane + 1, per = (steps + parts - 1) / parts;
+    const float at_once = 1.0f / (float)a.at_a_time, equal = (float)least / (float)steps, average = 0.5f * (float)(least + steps), over = parts > 1 ? 2.0f : 1.0f;
+    const float items = fminf((float)(tiles * parts), (float)tiles * fmaxf(average / (float)per + 0.5f, 1.0f));
+    const float in_rounds = __builtin_ceilf(items * at_once) * ((float)per + over), level = ((float)tiles * average + items * over) * at_once + 0.25f * (float)per;
+    float cost = fmaxf((float)per + over, equal * in_rounds + (1.0f - equal) * level);
+    if (parts > 1) cost += 2.0f + 0.028f * items * (float)a.c.kv_heads;
+    const bool possible = parts == 1 || (parts <= steps >> a.least_shift && tiles * parts <= a.places);
     const uint32_t key = possible ? (__float_as_uint(cost) & ~63u) | lane : ~0u;
     return (of_lane(over_lanes(key, ~0u, Least{}), 63) & 63u) + 1;
 }
@@ -104,7 +109,10 @@ __device__ __forceinline__ bool find_piece(const ChunkArgs &a, uint32_t item, Pi
     for (uint32_t s0 = 0; s0 < a.n_seqs; s0 += 64) {
         if (!kSplit || a.n_seqs > 64 || s0 == 0) look(s0);
         uint32_t parts = kSplit ? max(1u, min((steps + quota / 2) / quota, steps >> a.least_shift)) : 1;
-        if (kSplit && kWaves == 8) parts = parts_of_one(a, of_lane(tiles, 0), of_lane(steps, 0), parts);
+        if (kSplit && kWaves == 8) {
+            const uint32_t before = n_k > n_q ? n_k - n_q : 0;       // (the first tile's steps, without its own keys')
+            parts = parts_of_one(a, of_lane(tiles, 0), a.causal ? min(of_lane(steps, 0), of_lane(before, 0) / kPromptKeys + 1) : of_lane(steps, 0), of_lane(steps, 0), parts);
+        }
         const uint32_t places = parts > 1 ? tiles * parts : 0, items = kJoin ? (parts > 1 ? tiles : 0) : tiles * parts;
         const uint32_t items_to = over_lanes(items, 0u, Add{}), places_to = kSplit ? over_lanes(places, 0u, Add{}) : 0;
         uint32_t before = items_before + items_to - items;
@@ -732,7 +740,7 @@ __host__ __device__ __forceinline__ uint32_t split_tiles(const ChunkArgs &a) { r
 // waves' work and the parts of most are all in flight at once.  How many tiles
 // are split the host does not know: as many workgroups are launched as run at a
 // time, and end when there are no more (one for each tile that the workspace
-// could hold took 8 to 10 us to find nothing, JOINUS).
+// could hold took 8 to 10 us to find nothing).
 template <int D, uint32_t kWaves>
 __global__ __launch_bounds__(64 * D / 16) void join_chunk_kernel(ChunkArgs a) {
     constexpr int kDTiles = D / 32;

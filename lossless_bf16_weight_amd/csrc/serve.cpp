@@ -289,21 +289,29 @@ df11_status check_prompt_sizes(const df11_attend_prompt_args &a) {
 // Sequences of many are taken whole: each workgroup would read all their
 // lengths.
 //
-// From 2048 rows on the tiles of a single sequence have 256 rows and eight
-// waves, one workgroup for each compute unit, which read keys and values half as
-// often (2048 queries on 32,049 keys 936 us, with 128 rows 993; in 8 bits, where
-// codes are converted half as often too, 1090 and 1187; 256 on 4256 39 and 36);
-// and as they are equal, the workgroups choose the parts that end soonest, among
-// up to three times as many as run at a time.  Of several sequences the larger
-// tiles are harder to level out (16 prompts of up to 1024 tokens 88 us and 83, 64
-// of up to 256 61 and 55).
+// Behind a long prefix the tiles of a single sequence of 2048 rows and more have
+// 256 rows and eight waves, one workgroup for each compute unit, which read keys
+// and values half as often (2048 queries on 32,049 keys 936 us, with 128 rows
+// 993; 1500 on 17,500 413 and 471; in 8 bits, where codes are converted half as
+// often too, 1090 and 1187); and as they are nearly equal, the workgroups choose
+// the parts that end soonest, among up to three times as many as run at a time.
+// The length the host has from the table: a table of four times the queries is
+// taken for a long prefix (2048 on 8248 246 us and 250, 1024 on 4124 95 and 98;
+// 2048 on 6144 184 and 183, on 4096 125 and 118, on 2048 68 and 60; 256 on 4256 39
+// and 36).  Tiles of a whole prompt even out from 16,384 rows on (4096 tokens 151
+// us and 160, 6000 306 and 299, 8192 520 and 530).  Of several sequences the
+// larger tiles are harder to level out (16 prompts of up to 1024 tokens 88 us and
+// 83, 64 of up to 256 61 and 55).
 struct ChunkSplit {
     uint32_t most_steps, parts, places, least_shift, tile_rows;
 };
 
 constexpr uint32_t kChunkMostPlanned = 512;     // sequences
 
-uint32_t chunk_tile_rows(const df11_attend_chunk_args &a) { return a.n_seqs == 1 && a.n_q * (a.n_heads / a.cache.n_kv_heads) >= 2048 ? 256 : 128; }
+uint32_t chunk_tile_rows(const df11_attend_chunk_args &a) {
+    const uint64_t rows = a.n_q * (a.n_heads / a.cache.n_kv_heads), positions = (uint64_t)a.table.width * a.cache.page_size;
+    return a.n_seqs == 1 && rows >= 2048 && (rows >= 16384 || positions >= 4 * a.n_q) ? 256 : 128;
+}
 
 uint64_t chunk_tile_slots(const df11_attend_chunk_args &a) { return a.n_q * (a.n_heads / a.cache.n_kv_heads) / chunk_tile_rows(a) + a.n_seqs; }
 
