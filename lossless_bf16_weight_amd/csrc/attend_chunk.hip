@@ -109,6 +109,8 @@ __device__ __forceinline__ bool find_piece(const ChunkArgs &a, uint32_t item, Pi
     for (uint32_t s0 = 0; s0 < a.n_seqs; s0 += 64) {
         if (!kSplit || a.n_seqs > 64 || s0 == 0) look(s0);
         uint32_t parts = kSplit ? max(1u, min((steps + quota / 2) / quota, steps >> a.least_shift)) : 1;
+        // (a few parts more than run at a time would take as long as twice as many)
+        if (kSplit && kWaves == 4 && a.n_seqs == 1 && tiles * parts > a.at_a_time && tiles <= a.at_a_time) parts = a.at_a_time / tiles;
         if (kSplit && kWaves == 8) {
             const uint32_t before = n_k > n_q ? n_k - n_q : 0;       // (the first tile's steps, without its own keys')
             parts = parts_of_one(a, of_lane(tiles, 0), a.causal ? min(of_lane(steps, 0), of_lane(before, 0) / kPromptKeys + 1) : of_lane(steps, 0), of_lane(steps, 0), parts);
