@@ -36,6 +36,7 @@ namespace {
 constexpr uint32_t kWaveRows = 32;             // a workgroup has four waves or eight
 constexpr int kHalves = kPromptKeys / 32;      // of a step: 32 keys are a product's rows
 constexpr int kAhead = 4;                      // reads of K ahead of the products
+constexpr uint32_t kFewSteps = 8;              // of a tile: see the loops in 8 bits
 
 // What a workgroup does: a part of a tile of a sequence.
 struct Piece {
@@ -487,7 +488,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_chunk_kernel(ChunkArgs 
     const bool codes_here = kCodeRows <= kPromptKeys || wave < kWaves / 2;      // (eight waves, heads of 64: half of them have none)
     u32x4 kw[kCodeLoads], vw[kCodeLoads];
     float scale_w;
-    const auto load_codes = [&](uint32_t key0) {
+    const auto load_codes = [&](uint32_t key0) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < kCodeLoads; ++i) {
             if (!codes_here) break;
@@ -507,7 +508,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_chunk_kernel(ChunkArgs 
         }
         scale_w = (wave & 1 ? a.c.v_scale : a.c.k_scale)[r + (lane & 15)];
     };
-    const auto store_codes = [&](uint8_t *kt, uint8_t *vt, float *sc) {
+    const auto store_codes = [&](uint8_t *kt, uint8_t *vt, float *sc) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < kCodeLoads; ++i) {
             if (!codes_here) break;
@@ -521,8 +522,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_chunk_kernel(ChunkArgs 
     };
 
     // One step's keys.  kCareful: values that are infinite or NaN at keys which
-    // only some rows see do not reach the others.
-    const auto step = [&](auto careful, uint32_t key0, const uint8_t *kt, const uint8_t *vt, const float *sc) {
+    // only some rows see do not reach the others; in 8 bits (where values are
+    // finite) a weight is the sum of two operands, as in attend_columns.hpp.
+    const auto step = [&](auto careful, uint32_t key0, const uint8_t *kt, const uint8_t *vt, const float *sc) __attribute__((always_inline)) {
         constexpr bool kCareful = decltype(careful)::value;
         if (key0 >= wave_end || (key0 + kPromptKeys <= wave_begin && key0 >= a.sinks)) return;
         // (the careful pass computes its LDS addresses in each step: there are
@@ -530,6 +532,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_chunk_kernel(ChunkArgs 
         uint32_t own = lane_of_wave;
         if (kCareful) asm volatile("" : "+v"(own));
         const uint32_t lane = own, col = own & 31u, half = own >> 5;
+        // (in 8 bits with heads of 64 those of K, for registers of three waves)
+        uint32_t k_lane = own;
+        if (kInt8 && D == 64) asm volatile("" : "+v"(k_lane));
 
         f32x16 s[kHalves];
 #pragma unroll
@@ -538,7 +543,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_chunk_kernel(ChunkArgs 
         for (int i = 0; i < kDSteps; ++i)
 #pragma unroll
             for (int t = 0; t < kHalves; ++t) {
-                const u32x4 w = *reinterpret_cast<const u32x4 *>(kt + k_at<D>(32 * t + col, 2 * i + half));
+                const u32x4 w = *reinterpret_cast<const u32x4 *>(kt + k_at<D>(32 * t + (k_lane & 31u), 2 * i + (k_lane >> 5)));
                 s[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(w), as_bf16x8(q[i]), s[t], 0, 0, 0);
             }
         // (four reads of K ahead of the products)
@@ -593,7 +598,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_chunk_kernel(ChunkArgs 
         for (int t = 0; t < kHalves; ++t) {
 #pragma unroll
             for (int st = 0; st < 2; ++st) {
-                u32x4 p;
+                u32x4 p, p_low;
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
                     float e[4];
@@ -608,8 +613,16 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_chunk_kernel(ChunkArgs 
 #pragma unroll
                         for (int i = 0; i < 4; ++i) e[i] = mul_or_zero(e[i], w[i]);
                     }
-                    p[2 * g] = pack_bf16(e[0], e[1]);
-                    p[2 * g + 1] = pack_bf16(e[2], e[3]);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if constexpr (kInt8 && kCareful) {
+                            const u32x2 two = two_operands(e[2 * i], e[2 * i + 1]);
+                            p[2 * g + i] = two.x;
+                            p_low[2 * g + i] = two.y;
+                        } else {
+                            p[2 * g + i] = pack_bf16(e[2 * i], e[2 * i + 1]);
+                        }
+                    }
                 }
 #pragma unroll
                 for (int i = 0; i < kDTiles; ++i) {
@@ -619,7 +632,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_chunk_kernel(ChunkArgs 
                     const s16x4 b1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((DF11_LDS s16x4 *)(vt + v_at<D>(r + 8, chunk) + 8 * (j & 1)));
                     const u32x2 w0 = __builtin_bit_cast(u32x2, b0), w1 = __builtin_bit_cast(u32x2, b1);
                     u32x4 w = {w0.x, w0.y, w1.x, w1.y};
-                    if (kCareful) {
+                    if constexpr (kCareful && !kInt8) {
                         // Values that are not finite leave the product (0 times
                         // one of them is not 0) and are counted apart, over the
                         // keys that the row sees (whose score is not that of a
@@ -651,6 +664,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_chunk_kernel(ChunkArgs 
                         __builtin_amdgcn_sched_barrier(0);
                     }
                     o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(w), as_bf16x8(p), o[i], 0, 0, 0);
+                    if constexpr (kInt8 && kCareful) {
+                        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(w), as_bf16x8(p_low), o[i], 0, 0, 0);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
                 }
             }
         }
@@ -664,20 +681,33 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_chunk_kernel(ChunkArgs 
             if (step_begin + 1 < step_end) need_entries(steps.key(step_begin + 1));
             store_codes(kt0, vt0, sc0);
         }
-        const auto go = [&](uint32_t i, const uint8_t *kt, const uint8_t *vt, const float *sc, uint8_t *kt_next, uint8_t *vt_next, float *sc_next) {
+        const auto go = [&](auto careful, uint32_t i, const uint8_t *kt, const uint8_t *vt, const float *sc, uint8_t *kt_next, uint8_t *vt_next, float *sc_next) __attribute__((always_inline)) {
             __syncthreads();
             const bool more = i + 1 < step_end;
             if (more) load_codes(steps.key(i + 1));
             if (i + 2 < step_end) need_entries(steps.key(i + 2));
-            step(std::false_type{}, steps.key(i), kt, vt, sc);
+            step(careful, steps.key(i), kt, vt, sc);
             if (more) store_codes(kt_next, vt_next, sc_next);
         };
         // (the queries are here too: said outside the loop, so that its products
         // do not wait for what is loaded in it)
         __builtin_amdgcn_s_waitcnt(0x0F70);
-        for (uint32_t i = step_begin; i < step_end; i += 2) {
-            go(i, kt0, vt0, sc0, kt1, vt1, sc1);
-            if (i + 1 < step_end) go(i + 1, kt1, vt1, sc1, kt0, vt0, sc0);
+        // A weight times its value's scale is rounded: that of a key which carries
+        // most of a row, too, where words have a power of two.  Over many keys
+        // that adds as much as rounding the result does (0.0022 of the norm
+        // against 0.0017), where keys are few up to 0.0027; tiles of few steps
+        // therefore have weights of two operands (0.0017; 16 prompts of up to
+        // 1024 tokens 108 us and 96).
+        if (steps.n > kFewSteps) {
+            for (uint32_t i = step_begin; i < step_end; i += 2) {
+                go(std::false_type{}, i, kt0, vt0, sc0, kt1, vt1, sc1);
+                if (i + 1 < step_end) go(std::false_type{}, i + 1, kt1, vt1, sc1, kt0, vt0, sc0);
+            }
+        } else {
+            for (uint32_t i = step_begin; i < step_end; ++i) {
+                const bool odd = (i - step_begin) & 1;
+                go(std::true_type{}, i, odd ? kt1 : kt0, odd ? vt1 : vt0, odd ? sc1 : sc0, odd ? kt0 : kt1, odd ? vt0 : vt1, odd ? sc0 : sc1);
+            }
         }
     } else {
         if (step_begin < step_end) load(steps.key(step_begin), kt0, vt0);

@@ -86,13 +86,9 @@ __device__ __forceinline__ void column_update(const uint8_t *tile, uint32_t lane
         for (int i = 0; i < kDTiles; ++i) o[i] *= keep;
     }
     const float base = m == -__builtin_inff() ? 0.0f : m;
-    // weights as the sum of two BF16 operands, for the product has matrix
-    // rate to spare: rounded once they would add as much error as the
-    // rounding of the result (0.0027 of the norm against 0.0017).  The
-    // first is the BF16 number before the one that the weight begins with:
-    // what is left for the second is then above zero and within 2^-14 of
-    // the weight as a BF16, and a value that is infinite times both is
-    // that infinity (times 0 or less it would make the result NaN).
+    // weights as the sum of two operands, for the product has matrix rate to
+    // spare: rounded once they would add as much error as the rounding of the
+    // result (0.0027 of the norm against 0.0017)
     u32x4 p, p_low;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -105,10 +101,9 @@ __device__ __forceinline__ void column_update(const uint8_t *tile, uint32_t lane
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const uint32_t cut = __float_as_uint(e[2 * i]) >> 16 | (__float_as_uint(e[2 * i + 1]) & 0xFFFF0000u);
-            const uint32_t w = __builtin_bit_cast(uint32_t, __builtin_elementwise_sub_sat(__builtin_bit_cast(u16x2, cut), u16x2{1, 1}));
-            p[2 * t + i] = w;
-            p_low[2 * t + i] = pack_bf16(e[2 * i] - __uint_as_float(w << 16), e[2 * i + 1] - __uint_as_float(w & 0xFFFF0000u));
+            const u32x2 two = two_operands(e[2 * i], e[2 * i + 1]);
+            p[2 * t + i] = two.x;
+            p_low[2 * t + i] = two.y;
         }
     }
 #pragma unroll

@@ -28,6 +28,17 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
 }
 
+// Two weights from 0 on as sums of two BF16 operands each (.x, .y), the first of
+// them the BF16 number before the one that the weight begins with: what is left
+// for the second is then above zero and within 2^-14 of the weight as a BF16,
+// and a value that is infinite times both is that infinity (times 0 or less it
+// would make the result NaN).
+__device__ __forceinline__ u32x2 two_operands(float a, float b) {
+    const uint32_t cut = __float_as_uint(a) >> 16 | (__float_as_uint(b) & 0xFFFF0000u);
+    const uint32_t w = __builtin_bit_cast(uint32_t, __builtin_elementwise_sub_sat(__builtin_bit_cast(u16x2, cut), u16x2{1, 1}));
+    return u32x2{w, pack_bf16(a - __uint_as_float(w << 16), b - __uint_as_float(w & 0xFFFF0000u))};
+}
+
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // x and the value 32 (16) lanes away, in either order.
