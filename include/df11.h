@@ -410,8 +410,8 @@ typedef struct {
 /* A paged cache in the caller's memory: k and v are n_pages x n_kv_heads x
  * page_size x head_dim elements, BF16 words or (DF11_KV_INT8) signed bytes;
  * with bytes, k_scale and v_scale are n_pages x n_kv_heads x page_size floats
- * (else NULL), and element x stands for code * scale.  page_size: a power of
- * two from 16 to 1024; head_dim: 64 or 128; all 16-byte aligned; fewer than
+ * (else NULL), and element x stands for code * scale (a scale is not
+ * negative).  page_size: a power of two from 16 to 1024; head_dim: 64 or 128; all 16-byte aligned; fewer than
  * 2^32 rows (n_pages * n_kv_heads * page_size).  Slot page * page_size + i is
  * position i of a page. */
 typedef struct {
@@ -463,8 +463,8 @@ typedef struct {
     float factor;
 } df11_rotation;
 
-/* Queries and keys of n_tokens tokens (rows of n_heads and n_kv_heads heads;
- * either may be 0, its rows are then not looked at), each head normed where
+/* Queries and keys of n_tokens tokens (rows of n_heads and n_kv_heads heads,
+ * at most 65535; either may be 0, its rows are then not looked at), each head normed where
  * its weight (head_dim BF16 words) is not NULL, x * weight / sqrt(mean(x^2) +
  * eps), and rotated, into q_out and k_out.  All in 32 bits, rounded once.
  * eps: finite, at least 2^-100.  q_out may be q and k_out may be k (the same
@@ -485,7 +485,8 @@ df11_status df11_rotate_heads(const df11_rotate_heads_args *args, int hip_device
  * above 0) queries normed and rotated into q_out; keys also as rows of k_out
  * unless its data is NULL.  Slots as for df11_kv_write; a token that is left out
  * of the cache still has its rows of q_out and k_out.  Keys in 8 bits are
- * quantised from the 32-bit values, not from rounded ones. */
+ * quantised from the 32-bit values, not from rounded ones.  n_heads: at most
+ * 65535. */
 typedef struct {
     df11_kv_cache cache;
     df11_rotation rotation;
@@ -576,8 +577,10 @@ df11_status df11_attend_prompt(const df11_attend_prompt_args *args, int hip_devi
  * window and j < sinks (a window needs the flag; sinks without one do nothing).
  * Otherwise all.  A sequence may have one query or all its tokens, or none.
  * scale, workspace and out as for df11_attend_token; weights are rounded as in
- * df11_attend_prompt.  The division of the work follows lens, on the device: a
- * table wider than the lengths costs workspace, no time. */
+ * df11_attend_prompt (with 8 bits, of queries over few keys, as in
+ * df11_attend_token).  The division of the work follows lens, on the device: a
+ * table wider than the lengths costs workspace, hardly any time.  Starts that do
+ * not ascend give undefined rows of out, and harm nothing else. */
 typedef struct {
     df11_kv_cache cache;
     df11_page_table table;

@@ -10,19 +10,30 @@
 // scores, a value's scale its weights, in 32 bits.
 //
 // Rows, tiles, products and the steps of 64 keys through LDS are those of
-// attend_prompt.hip, but a workgroup may have eight waves and 256 rows; rows come from pages, 16 at a time from one page, whose
-// numbers lie in the lanes of a register (64 entries of the table).  Words go
-// from memory into LDS without passing through registers; codes pass through
-// them, converted once by the workgroup.  The steps of a tile are those of the
-// sinks and those of the window.
+// attend_prompt.hip, but a workgroup may have eight waves and 256 rows; rows
+// come from pages, 16 at a time from one page, whose numbers lie in the lanes of
+// a register (64 entries of the table).  Words go from memory into LDS without
+// passing through registers; codes pass through them, converted once by the
+// workgroup.  The steps of a tile are those of the sinks and those of the
+// window.
 // Sequences of one new token, whose rows are few, go another way: see
 // attend_single.
 //
 // How long the sequences are the host does not know.  Each workgroup finds
 // from q_starts and lens how the work of the whole call is divided: the steps
-// of all tiles over `places` workgroups give a quota, and a sequence's tiles
-// are split into as many parts as their steps hold quotas.  A second kernel
+// of all tiles over as many workgroups as run at a time give a quota, and a
+// sequence's tiles are split into as many parts as their steps hold quotas.  A second kernel
 // joins the parts.
+//
+// Long pieces are bound by the matrix units at the card's power limit: 2048
+// queries of 32 heads over 8 of 128 on 32,049 keys take 940 us (1.11 PFLOP/s,
+// where a 16,384-square product reaches 1.31), a prompt of 16,384 in a window of
+// 4096 928 us (1.04); heads of 64 575 to 595 us, of as many exponentials.  Codes
+// cost the vector units, which hide behind the products of words: 1075 us, and
+// six pieces of up to 701 queries 357 us for 294.  Four pieces of up to 512
+// behind up to 8192 with 28 single tokens take 156 to 172 us, for 520 MB, most of
+// them the tokens' (alone 96 us, 5.2 TB/s); 64 queries on 2001 keys 17.5 us, a
+// chain of reads, four steps and the join.
 #include "attend_columns.hpp"
 #include "attend_tiles.hpp"
 
@@ -204,7 +215,7 @@ struct Entries {
 // each with the next ones' rows in registers and a tile of its own in LDS, and
 // are joined through LDS at the end.  Bound by HBM traffic: 128 KB in flight on
 // a compute unit, where the tiles of 128 rows have 64 (32 sequences of 1 to
-// 8192 keys, 470 MB: see the head of this file).  own: the wave's LDS, of
+// 8192 keys, 500 MB: 96 us, 5.2 TB/s).  own: the wave's LDS, of
 // max(32 rows, 16 columns of D + 4 floats) bytes; area(w): wave w's.
 template <int D, bool kInt8, class Area>
 __device__ __forceinline__ void attend_single(const ChunkArgs &a, const Piece &p, const Steps &steps, uint32_t step_begin, uint32_t step_end, bool whole,
