@@ -47,6 +47,7 @@ namespace {
 constexpr uint32_t kWaveRows = 32;             // a workgroup has four waves or eight
 constexpr int kHalves = kPromptKeys / 32;      // of a step: 32 keys are a product's rows
 constexpr int kAhead = 4;                      // reads of K ahead of the products
+constexpr uint32_t kWorthLevelling = 24, kLevelled = 8;      // steps of a quota, sequences: see level_out
 constexpr uint32_t kFewSteps = 8;              // of a tile: see the loops in 8 bits
 
 // What a workgroup does: a part of a tile of a sequence.
@@ -66,6 +67,7 @@ __device__ __forceinline__ uint32_t of_lane(uint32_t x, uint32_t lane) { return 
 // where the first tiles are short (`least` steps, of `steps`), these even the
 // end out.  (Few tiles have many parts, where rounding is harmless.)
 __device__ __forceinline__ uint32_t parts_of_one(const ChunkArgs &a, uint32_t tiles, uint32_t least, uint32_t steps, uint32_t otherwise) {
+#pragma clang fp contract(off)      // (both kernels are to find the same)
     if (tiles * 8 < a.at_a_time) return otherwise;
     const uint32_t lane = threadIdx.x & 63u, parts = lane + 1, per = (steps + parts - 1) / parts;
     const float at_once = 1.0f / (float)a.at_a_time, equal = (float)least / (float)steps, average = 0.5f * (float)(least + steps), over = parts > 1 ? 2.0f : 1.0f;
@@ -78,10 +80,51 @@ __device__ __forceinline__ uint32_t parts_of_one(const ChunkArgs &a, uint32_t ti
     return (of_lane(over_lanes(key, ~0u, Least{}), 63) & 63u) + 1;
 }
 
+// Work items before those of this lane's sequence, the longest parts first (one
+// of them at the end would keep the others' compute units waiting).
+__device__ __forceinline__ uint32_t items_before(uint32_t n_seqs, uint32_t per, uint32_t items) {
+    const uint32_t rank = per << 6 | (threadIdx.x & 63u);
+    uint32_t before = 0;
+    for (uint32_t j = 0; j < n_seqs; ++j) before += of_lane(rank, j) > rank ? of_lane(items, j) : 0;
+    return before;
+}
+
+// The quota, or less of it, with which the parts of several sequences (a lane
+// each) end soonest, as far as these lower bounds say: the average, the longest
+// part, and for one more than run at a time (or than twice as many) the two (three)
+// that share a place.  A part has two steps' time beside its own, and what is
+// written and joined of it.  Up to eight sequences gain by it (three pieces of up
+// to 1000 on 10,000 keys 226 us, by the quota 250; six of the 8-bit case 354 and
+// 368), where parts are long; with 32 the search costs as much (28 single tokens
+// 105 us and 96).  0: no quota makes `item` one.
+__device__ __forceinline__ uint32_t level_out(const ChunkArgs &a, uint32_t tiles, uint32_t steps, float total, uint32_t quota, uint32_t item) {
+    float least = __builtin_inff();
+    uint32_t chosen = 0;
+    for (uint32_t sixteenths = 9; sixteenths <= 16; sixteenths += sixteenths == 9 ? 4 : 3) {
+        const uint32_t q = (quota * sixteenths + 15) / 16;
+        const uint32_t parts = max(1u, min((steps + q / 2) / q, steps >> a.least_shift)), per = (steps + parts - 1) / parts, items = tiles * parts;
+        const uint32_t all = of_lane(over_lanes(items, 0u, Add{}), 63), split = of_lane(over_lanes(parts > 1 ? items : 0u, 0u, Add{}), 63);
+        if (sixteenths == 9 && item >= all) return 0;
+        const uint32_t before = items_before(a.n_seqs, per, items), w = a.at_a_time;
+        const auto at = [&](uint32_t k) {
+            const uint64_t has = __ballot(before < k && k - before <= items);
+            return has ? of_lane(per, (uint32_t)__builtin_ctzll(has)) + 2 : 0;
+        };
+        const uint32_t bound = max(max(at(1), all > w ? at(w) + at(w + 1) : 0), all > 2 * w ? at(2 * w - 1) + at(2 * w) + at(2 * w + 1) : 0);
+        const float cost = fmaxf((float)bound, (total + 2.0f * (float)all) * a.by_parts) + (split ? 2.0f + 0.007f * (float)(split * a.c.kv_heads) : 0.0f);
+        if (cost < least) {
+            least = cost;
+            chosen = q;
+        }
+    }
+    return chosen;
+}
+
 // Finds work item `item` (kJoin: the tile of that number among those that are
 // split).  False where there is none.
 template <uint32_t kWaves, bool kSplit, bool kJoin>
 __device__ __forceinline__ bool find_piece(const ChunkArgs &a, uint32_t item, Piece *p) {
+#pragma clang fp contract(off)
     constexpr uint32_t kTile = kWaves * kWaveRows;
     const uint32_t lane = threadIdx.x & 63u;
     uint32_t q0 = 0, n_q = 0, n_k = 0, tiles = 0, steps = 0;
@@ -96,7 +139,9 @@ __device__ __forceinline__ bool find_piece(const ChunkArgs &a, uint32_t item, Pi
         steps = min((n_k + kPromptKeys - 1) / kPromptKeys, a.most_steps);
     };
     uint32_t quota = 0;
-    if (kSplit) {
+    if (kSplit && kJoin && kWaves == 4) {
+        quota = *a.quota;
+    } else if (kSplit) {
         float total = 0;
         for (uint32_t s0 = 0; s0 < a.n_seqs; s0 += 64) {
             look(s0);
@@ -105,6 +150,11 @@ __device__ __forceinline__ bool find_piece(const ChunkArgs &a, uint32_t item, Pi
         total = __uint_as_float(of_lane(__float_as_uint(over_lanes(total, 0.0f, Add{})), 63));
         // (above the quotient, whatever the sum's rounding: see chunk_split)
         quota = (uint32_t)fminf(total * a.by_parts * (1.0f + 0x1p-18f), 4.0e9f) + 1;
+        if (kWaves == 4) {
+            if (a.n_seqs > 1 && a.n_seqs <= kLevelled && quota >= kWorthLevelling && quota < 1u << 27) quota = level_out(a, tiles, steps, total, quota, item);
+            if (quota == 0) return false;
+            if (blockIdx.x == 0 && threadIdx.x == 0) *a.quota = quota;
+        }
     } else if (kWaves == 4 && a.n_seqs > 64) {
         uint32_t tile;
         const uint32_t s = sequence_of_slot(a.q_starts, a.n_seqs, item, a.group, 7, &tile);
@@ -117,9 +167,9 @@ __device__ __forceinline__ bool find_piece(const ChunkArgs &a, uint32_t item, Pi
         p->tile = tile, p->part = 0, p->parts = 1, p->per = ~0u, p->place = 0;
         return true;
     }
-    uint32_t items_before = 0, places_before = 0;
+    uint32_t sum_before = 0, places_before = 0;
     for (uint32_t s0 = 0; s0 < a.n_seqs; s0 += 64) {
-        if (!kSplit || a.n_seqs > 64 || s0 == 0) look(s0);
+        if (!kSplit || (kJoin && kWaves == 4) || a.n_seqs > 64) look(s0);
         uint32_t parts = kSplit ? max(1u, min((steps + quota / 2) / quota, steps >> a.least_shift)) : 1;
         // (a few parts more than run at a time would take as long as twice as many)
         if (kSplit && kWaves == 4 && a.n_seqs == 1 && tiles * parts > a.at_a_time && tiles <= a.at_a_time) parts = a.at_a_time / tiles;
@@ -129,14 +179,8 @@ __device__ __forceinline__ bool find_piece(const ChunkArgs &a, uint32_t item, Pi
         }
         const uint32_t places = parts > 1 ? tiles * parts : 0, items = kJoin ? (parts > 1 ? tiles : 0) : tiles * parts;
         const uint32_t items_to = over_lanes(items, 0u, Add{}), places_to = kSplit ? over_lanes(places, 0u, Add{}) : 0;
-        uint32_t before = items_before + items_to - items;
-        if (kWaves == 4 && kSplit && !kJoin && a.n_seqs <= 64) {
-            // the sequences with the longest parts first: one of them at the end
-            // would keep the others' compute units waiting
-            const uint32_t rank = (steps + parts - 1) / parts << 6 | lane;
-            before = 0;
-            for (uint32_t j = 0; j < a.n_seqs; ++j) before += of_lane(rank, j) > rank ? of_lane(items, j) : 0;
-        }
+        uint32_t before = sum_before + items_to - items;
+        if (kWaves == 4 && kSplit && !kJoin && a.n_seqs <= 64) before = items_before(a.n_seqs, (steps + parts - 1) / parts, items);
         const uint64_t found = __ballot(item >= before && item - before < items);
         if (found) {
             const uint32_t x = (uint32_t)__builtin_ctzll(found);
@@ -154,7 +198,7 @@ __device__ __forceinline__ bool find_piece(const ChunkArgs &a, uint32_t item, Pi
             // (starts that do not ascend may make more of them than there are places)
             return p->parts == 1 || p->place + p->parts <= a.places;
         }
-        items_before += of_lane(items_to, 63);
+        sum_before += of_lane(items_to, 63);
         places_before += of_lane(places_to, 63);
     }
     return false;

@@ -279,13 +279,14 @@ df11_status check_prompt_sizes(const df11_attend_prompt_args &a) {
 
 // What attend_chunk's workgroups need for dividing a call's work, whose lengths
 // the host does not know: the parts of equal size that it would be, as many as
-// workgroups run at a time, two for each compute unit, and the least steps of
-// one, four (64 queries on 2001 keys 18 us, with eight 22, with two 20).  A
-// tile's steps over the quota, rounded, are its parts: two from one and a half
-// on, so that all split tiles have at most four thirds of the parts asked for,
-// and so many places the workspace has.  (A quarter more parts, which level out
-// better, are a second round of workgroups where parts are equal: 256 queries
-// on 4256 keys 45 us and 38, four pieces on 8700 to 5000 keys 123 us and 131.)
+// workgroups run at a time, two for each compute unit (with heads of 64 three:
+// three pieces of up to 1000 on 10,000 134 us, divided by two 157), and the least
+// steps of one, four (64 queries on 2001 keys 18 us, with eight 22, with two 20).
+// A tile's steps over the quota, rounded, are its parts: two from one and a half
+// on, so that all split tiles have at most four thirds of the parts asked for;
+// with nine sixteenths of the quota (level_out) 2.4 times as many, and so many
+// places the workspace has.  (A quarter more parts for all are a second round of
+// workgroups where parts are equal: 256 queries on 4256 keys 45 us and 38.)
 // Sequences of many are taken whole: each workgroup would read all their
 // lengths.
 //
@@ -323,15 +324,15 @@ ChunkSplit chunk_split(const df11_attend_chunk_args &a, int dev) {
     const Window w = window_of(a.window, a.sinks, positions);
     if (w.keys) s.most_steps = (uint32_t)((w.keys + (s.tile_rows - 1) / group + 1 + 2 * (kPromptKeys - 1)) / kPromptKeys + ceil_div(w.sinks, kPromptKeys));
     const uint64_t steps = std::min<uint64_t>(ceil_div(positions, kPromptKeys), s.most_steps);
-    const uint64_t parts = 256 / s.tile_rows * compute_units(dev) / a.cache.n_kv_heads, of_tile = steps >> s.least_shift;
+    const uint64_t parts = (s.tile_rows == 256 ? 1 : a.cache.head_dim == 64 ? 3 : 2) * compute_units(dev) / a.cache.n_kv_heads, of_tile = steps >> s.least_shift;
     if (a.n_q == 0 || a.n_seqs == 0 || a.n_seqs > kChunkMostPlanned || parts < 2 || of_tile < 2) return s;
     s.parts = (uint32_t)parts;
-    s.places = (uint32_t)std::min(s.tile_rows == 256 ? 3 * parts : 4 * parts / 3, chunk_tile_slots(a) * of_tile);
+    s.places = (uint32_t)std::min(s.tile_rows == 256 ? 3 * parts : 5 * parts / 2, chunk_tile_slots(a) * of_tile);
     return s;
 }
 
 uint64_t chunk_bytes(const df11_attend_chunk_args &a, const ChunkSplit &s) {
-    return (uint64_t)s.places * a.cache.n_kv_heads * s.tile_rows * (a.cache.head_dim + 2) * sizeof(float);
+    return s.places ? (uint64_t)s.places * a.cache.n_kv_heads * s.tile_rows * (a.cache.head_dim + 2) * sizeof(float) + 16 : 0;
 }
 
 df11_status check_chunk_sizes(const df11_attend_chunk_args &a) {
@@ -557,6 +558,7 @@ extern "C" df11_status df11_attend_chunk(const df11_attend_chunk_args *a, int hi
     c.by_parts = s.parts ? 1.0f / s.parts : 0;
     c.part = (float *)a->workspace;
     c.part_ml = c.part + (uint64_t)s.places * kv * s.tile_rows * d;
+    c.quota = (uint32_t *)(c.part_ml + (uint64_t)s.places * kv * s.tile_rows * 2);
     return launched(launch_attend_chunk(c, d, a->cache.store == DF11_KV_INT8, stream), "attend_chunk");
 }
 

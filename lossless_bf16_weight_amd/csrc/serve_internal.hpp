@@ -104,6 +104,7 @@ struct ChunkArgs {
     uint32_t places, least_shift;        // parts of a kv head's tiles that the workspace holds (0: none are split); log2 of the least steps of one
     float by_parts;                      // 1 / the parts that a kv head's work is divided into
     float *part, *part_ml;               // [place][kv_head][wave][register / 4][lane][4], then [place][kv_head][wave][row][2]
+    uint32_t *quota;                     // the first kernel's, for the one that joins
 };
 
 constexpr uint32_t kWriteChunks = 512;   // 16-byte chunks of rows that a workgroup of kv_write takes

@@ -83,7 +83,7 @@ def test_many_kv_heads():
     df11.attend_chunk(q, c.cache, c.pages, U.starts_of(new).to(DEV), c.lens, out)
     torch.cuda.synchronize()
     U.within(out, *CU.chunk64(q, c.cache, c.table, new, lens, d ** -0.5), "many kv heads")
-    assert df11.chunk_workspace(43, 2, h, hk, d, 16, 1 << 12) == 0
+    assert df11.chunk_workspace(43, 2, 1000, 500, d, 16, 1 << 12) == 0
 
 
 def test_broadcast_and_strided_inputs():

@@ -99,3 +99,23 @@ def test_a_captured_graph_follows_the_length():
         go()
         torch.cuda.synchronize()
         assert torch.equal(out, first)
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("new,lens,h,hk,d", [([200, 130, 64], [9000, 7000, 5000], 8, 2, 128), ([300, 1, 100, 0], [6100, 6000, 2000, 3000], 8, 1, 64),
+                                             ([150] * 8, [2500 - 250 * i for i in range(8)], 8, 2, 64), ([90] * 9, [3100 - 300 * i for i in range(9)], 8, 2, 128),
+                                             ([1000, 2], [12000, 12000], 4, 4, 128)])
+def test_several_long_sequences(new, lens, h, hk, d, int8):
+    """Parts of unequal sequences, up to eight of which are evened out."""
+    log(f"several {new} of {lens} heads {h}/{hk} head_dim {d} int8 {int8}")
+    c = CU.Cached(lens, hk, d, 64, int8, seed=sum(lens))
+    q = CU.rand((sum(new), h, d), 5)
+    size = df11.chunk_workspace(len(q), len(new), h, hk, d, 64, c.pages.shape[1])
+    memory = torch.full((size + 4096,), 0xFF, dtype=torch.uint8, device=DEV)
+    want, bound = CU.chunk64(q, c.cache, c.table, new, lens, d ** -0.5)
+    for _ in range(2):
+        out = torch.full_like(q, 7.0)
+        df11.attend_chunk(q, c.cache, c.pages, U.starts_of(new).to(DEV), c.lens, out, workspace=memory[:size])
+        torch.cuda.synchronize()
+        U.within(out, want, bound, new)
+        assert bool((memory[size:] == 0xFF).all())

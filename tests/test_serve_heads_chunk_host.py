@@ -132,11 +132,11 @@ def test_workspaces():
     assert df11.chunk_workspace(64, 1000, 32, 8, 128, 16, 512) == 0
     need = df11.chunk_workspace(64, 1, 32, 8, 128, 16, 512)
     tile = 128 * 130 * 4
-    most = 2 * 256 // 8 * 4 // 3 * 8 * tile
-    assert need and need % (8 * tile) == 0 and need <= most
+    most = 2 * 256 // 8 * 5 // 2 * 8 * tile + 16
+    assert need and need % (8 * tile) == 16 and need <= most
     assert df11.chunk_workspace(64, 1, 32, 8, 128, 16, 1 << 20) == most
     assert df11.chunk_workspace(640, 2, 32, 8, 128, 16, 1 << 20) == most
-    assert df11.chunk_workspace(640, 1, 32, 8, 128, 16, 1 << 20) == 3 * 256 * 2 * tile       # (tiles of 256 rows)
+    assert df11.chunk_workspace(640, 1, 32, 8, 128, 16, 1 << 20) == 3 * 256 * 2 * tile + 16      # (tiles of 256 rows)
     assert df11.chunk_workspace(64, 1, 32, 8, 128, 16, 1 << 20, 100, 4) == 0       # (a window of few steps)
     good = dict(GOOD["df11_attend_chunk"], **{"table.width": 4096, "window": 0})
     need = df11.chunk_workspace(5, 2, 4, 2, 128, 16, 4096)
