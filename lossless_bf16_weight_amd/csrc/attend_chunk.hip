@@ -30,7 +30,7 @@
 // PFLOP/s, where a 16,384-square product reaches 1.31), a prompt of 16,384 in a
 // window of 4096 905 to 929 us (1.05); heads of 64 575 to 595 us, of as many
 // exponentials.  Codes cost the vector units, which hide behind the products of
-// words: 1063 us, and six pieces of up to 701 queries 331 to 354 us for 284.  Four
+// words: 1063 us, and six pieces of up to 701 queries 331 to 361 us for 284.  Four
 // pieces of up to 512 behind up to 8192 with 28 single tokens take 156 to 176 us, for 520 MB, most of
 // them the tokens' (alone 96 us, 5.2 TB/s); 64 queries on 2001 keys 17.5 us, a
 // chain of reads, four steps and the join.
@@ -96,8 +96,10 @@ __device__ __forceinline__ uint32_t items_before(uint32_t n_seqs, uint32_t per, 
 // written and joined of it.  Up to eight sequences gain by it (three pieces of up
 // to 1000 on 10,000 keys 226 us, by the quota 250; six of the 8-bit case 354 and
 // 368), where parts are long; with 32 the search costs as much (28 single tokens
-// 105 us and 96).  0: no quota makes `item` one.
+// 105 us and 96; of eight 185 and 179).  0: no quota makes `item` one.
 __device__ __forceinline__ uint32_t level_out(const ChunkArgs &a, uint32_t tiles, uint32_t steps, float total, uint32_t quota, uint32_t item) {
+    const uint32_t smallest = (quota * 9 + 15) / 16;
+    if (!__any(tiles && steps + smallest / 2 >= 2 * smallest)) return quota;      // (all tiles are whole)
     float least = __builtin_inff();
     uint32_t chosen = 0;
     for (uint32_t sixteenths = 9; sixteenths <= 16; sixteenths += sixteenths == 9 ? 4 : 3) {
@@ -151,7 +153,7 @@ __device__ __forceinline__ bool find_piece(const ChunkArgs &a, uint32_t item, Pi
         // (above the quotient, whatever the sum's rounding: see chunk_split)
         quota = (uint32_t)fminf(total * a.by_parts * (1.0f + 0x1p-18f), 4.0e9f) + 1;
         if (kWaves == 4) {
-            if (a.n_seqs > 1 && a.n_seqs <= kLevelled && quota >= kWorthLevelling && quota < 1u << 27) quota = level_out(a, tiles, steps, total, quota, item);
+            if (a.n_seqs > 1 && a.n_seqs <= kLevelled && a.n_q > a.n_seqs && quota >= kWorthLevelling && quota < 1u << 27) quota = level_out(a, tiles, steps, total, quota, item);
             if (quota == 0) return false;
             if (blockIdx.x == 0 && threadIdx.x == 0) *a.quota = quota;
         }
