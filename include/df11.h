@@ -468,8 +468,9 @@ typedef struct {
  * its weight (head_dim BF16 words) is not NULL, x * weight / sqrt(mean(x^2) +
  * eps), and rotated, into q_out and k_out.  All in 32 bits, rounded once.
  * eps: finite, at least 2^-100.  q_out may be q and k_out may be k (the same
- * pointer and strides); they overlap nothing else.  Finite values of any size
- * are normed as the formula says. */
+ * pointer and strides); they overlap nothing else.  Finite values,
+ * weights and eps of any size are normed as the formula says, but an element
+ * below 2^-126 times the root may count as 0. */
 typedef struct {
     df11_rotation rotation;
     df11_rows q, k, q_out, k_out;

@@ -129,26 +129,29 @@ __global__ __launch_bounds__(kThreads, 8) void heads_kernel(HeadsArgs a) {
 #pragma unroll
             for (int x = 0; x < 16; ++x) sum = __builtin_fmaf(y[x], y[x], sum);
             sum = row_sum<kLanes>(sum);
-            float eps = a.eps;
-            if (!(sum < __builtin_inff())) {
-                // squares that pass 32 bits (or an infinity): of values 2^-100 as
-                // large, and eps 2^-200 of itself
-                sum = 0, eps = 0;
+            float mean = __builtin_fmaf(sum, 1.0f / D, a.eps);
+            if (!(mean < __builtin_inff())) {
+                // squares that pass 32 bits, alone or with eps (or an infinity): of
+                // values 2^-68 as large, whose sum stays below 2^127
+                sum = 0;
 #pragma unroll
                 for (int x = 0; x < 16; ++x) {
-                    y[x] *= 0x1p-100f;
+                    y[x] *= 0x1p-68f;
                     sum = __builtin_fmaf(y[x], y[x], sum);
                 }
                 sum = row_sum<kLanes>(sum);
+                mean = __builtin_fmaf(sum, 1.0f / D, a.eps * 0x1p-68f * 0x1p-68f);
             }
-            const float by = __builtin_amdgcn_rsqf(__builtin_fmaf(sum, 1.0f / D, eps));
+            const float by = __builtin_amdgcn_rsqf(mean);
+            // (first of value and root, which is at most the root of D: a weight times
+            // the root may pass 32 bits where the result does not)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const u32x4 eight = *reinterpret_cast<const u32x4 *>(weights[wave] + (is_q ? 0 : D) + (x ? at1 : at0));
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    y[8 * x + 2 * i] *= by * low(eight[i]);
-                    y[8 * x + 2 * i + 1] *= by * high(eight[i]);
+                    y[8 * x + 2 * i] = y[8 * x + 2 * i] * by * low(eight[i]);
+                    y[8 * x + 2 * i + 1] = y[8 * x + 2 * i + 1] * by * high(eight[i]);
                 }
             }
         }
