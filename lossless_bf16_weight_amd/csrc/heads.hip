@@ -140,7 +140,7 @@ __global__ __launch_bounds__(kThreads, 8) void heads_kernel(HeadsArgs a) {
                     sum = __builtin_fmaf(y[x], y[x], sum);
                 }
                 sum = row_sum<kLanes>(sum);
-                mean = __builtin_fmaf(sum, 1.0f / D, a.eps * 0x1p-68f * 0x1p-68f);
+                mean = __builtin_fmaf(sum, 1.0f / D, a.eps_scaled);
             }
             const float by = __builtin_amdgcn_rsqf(mean);
             // (first of value and root, which is at most the root of D: a weight times

@@ -159,6 +159,7 @@ df11_status heads_args(HeadsArgs *h, const df11_rotation &r, const void *q_weigh
     h->q_weight = (const uint16_t *)q_weight;
     h->k_weight = (const uint16_t *)k_weight;
     h->eps = eps;
+    h->eps_scaled = eps * 0x1p-68f * 0x1p-68f;
     h->n_tokens = (uint32_t)n_tokens;
     return DF11_OK;
 }

@@ -60,7 +60,7 @@ struct HeadsArgs {
     uint32_t n_tokens, heads, kv_heads;
     uint32_t pairs, n_axes;
     uint32_t parts, run;                 // waves a token, steps of each
-    float factor, eps;
+    float factor, eps, eps_scaled;       // (the last: times 2^-136)
 };
 
 struct TokenArgs {
