@@ -410,8 +410,8 @@ typedef struct {
 /* A paged cache in the caller's memory: k and v are n_pages x n_kv_heads x
  * page_size x head_dim elements, BF16 words or (DF11_KV_INT8) signed bytes;
  * with bytes, k_scale and v_scale are n_pages x n_kv_heads x page_size floats
- * (else NULL), and element x stands for code * scale (a scale is not
- * negative).  page_size: a power of two from 16 to 1024; head_dim: 64 or 128; all 16-byte aligned; fewer than
+ * (else NULL), and element x stands for code * scale.  page_size: a power of
+ * two from 16 to 1024; head_dim: 64 or 128; all 16-byte aligned; fewer than
  * 2^32 rows (n_pages * n_kv_heads * page_size).  Slot page * page_size + i is
  * position i of a page. */
 typedef struct {

@@ -673,7 +673,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_chunk_kernel(ChunkArgs 
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         if constexpr (kInt8 && kCareful) {
-                            const u32x2 two = two_operands(e[2 * i], e[2 * i + 1]);
+                            const u32x2 two = two_operands<true>(e[2 * i], e[2 * i + 1]);
                             p[2 * g + i] = two.x;
                             p_low[2 * g + i] = two.y;
                         } else {

@@ -101,7 +101,7 @@ __device__ __forceinline__ void column_update(const uint8_t *tile, uint32_t lane
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const u32x2 two = two_operands(e[2 * i], e[2 * i + 1]);
+            const u32x2 two = two_operands<kInt8>(e[2 * i], e[2 * i + 1]);
             p[2 * t + i] = two.x;
             p_low[2 * t + i] = two.y;
         }

@@ -11,6 +11,7 @@ namespace df11 {
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+typedef short i16x2 __attribute__((ext_vector_type(2)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef int i32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
@@ -28,14 +29,27 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
 }
 
-// Two weights from 0 on as sums of two BF16 operands each (.x, .y), the first of
-// them the BF16 number before the one that the weight begins with: what is left
-// for the second is then above zero and within 2^-14 of the weight as a BF16,
-// and a value that is infinite times both is that infinity (times 0 or less it
-// would make the result NaN).
+// Two weights as sums of two BF16 operands each (.x, .y), within 2^-14 of the
+// weight as a BF16.
+// Words: weights are from 0 on, and the first operand is the BF16 number before
+// the one that the weight begins with: what is left for the second is then above
+// zero, and a value that is infinite times both is that infinity (times 0 or less
+// it would make the result NaN).
+// 8 bits: weights have the values' scales in them, of either sign or infinite, and
+// values are finite codes: the first operand is what the weight begins with, at
+// most the largest finite number, so that the second is what is left (by one
+// minimum for each sign; the step before it, of signed words, took 1 to 7% longer:
+// 16 prompts of up to 1024 tokens 113.5 us, heads of 64 75.0, and 109.3, 70.3).
+template <bool kInt8>
 __device__ __forceinline__ u32x2 two_operands(float a, float b) {
     const uint32_t cut = __float_as_uint(a) >> 16 | (__float_as_uint(b) & 0xFFFF0000u);
-    const uint32_t w = __builtin_bit_cast(uint32_t, __builtin_elementwise_sub_sat(__builtin_bit_cast(u16x2, cut), u16x2{1, 1}));
+    uint32_t w;
+    if constexpr (kInt8) {
+        w = __builtin_bit_cast(uint32_t, __builtin_elementwise_min(__builtin_bit_cast(i16x2, cut), i16x2{0x7F7F, 0x7F7F}));
+        w = __builtin_bit_cast(uint32_t, __builtin_elementwise_min(__builtin_bit_cast(u16x2, w), u16x2{0xFF7F, 0xFF7F}));
+    } else {
+        w = __builtin_bit_cast(uint32_t, __builtin_elementwise_sub_sat(__builtin_bit_cast(u16x2, cut), u16x2{1, 1}));
+    }
     return u32x2{w, pack_bf16(a - __uint_as_float(w << 16), b - __uint_as_float(w & 0xFFFF0000u))};
 }
 

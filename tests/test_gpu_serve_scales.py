@@ -1,6 +1,6 @@
-"""Attention over a cache in 8 bits whose scales are of either sign (a code times
-its scale is the value, whatever the sign), with scores so far apart that weights
-are 0 in 32 bits: against the definition in 64 bits (serve_chunk_util.py)."""
+"""Attention over a cache in 8 bits whose scales are of either sign, or infinite (a
+code times its scale is the value, whatever that is), with scores so far apart that
+weights are 0 in 32 bits: against the definition in 64 bits (serve_chunk_util.py)."""
 import pytest
 import torch
 
@@ -68,3 +68,27 @@ def test_results_stay_with_scales_that_are_not_negative():
         go(c.cache, a)
         go(turned, b)
         assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_infinite_scales_of_values(sign, d):
+    """Codes other than 0 times an infinite scale are infinities, for the rows that
+    see them."""
+    new, lens = [40, 1], [300, 2500]
+    log(f"scales of {sign} infinity, heads of {d}")
+    c = _signed(lens, 2, d, 16, 7)
+    for s, key in ((0, 280), (1, 2000)):
+        page, at = int(c.table[s, key // 16]), key % 16
+        c.cache.v[page, 1, at] = torch.arange(1, d + 1, dtype=torch.int8, device=DEV)
+        c.cache.v_scale[page, 1, at] = sign * float("inf")
+    q = CU.rand((sum(new), 8, d), 8)
+    for window in (0, 100):
+        want, bound = CU.chunk64(q, c.cache, c.table, new, lens, d ** -0.5, True, window, 0)
+        out = torch.full_like(q, 7.0)
+        df11.attend_chunk(q, c.cache, c.pages, U.starts_of(new).to(DEV), c.lens, out, window=window)
+        U.within(out, want, bound, ("chunk", window))
+        assert bool(torch.isinf(want).any()) and not bool(torch.isinf(want).all())
+        out = torch.full_like(q[-1:], 7.0)
+        df11.attend_token(q[-1:], c.cache, c.pages[1:], c.lens[1:], out, window=window)
+        U.within(out, want[-1:], bound[-1:], ("token", window))
