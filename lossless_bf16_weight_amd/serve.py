@@ -121,7 +121,7 @@ class DecoderStack:
 
         try:
             positions, slots = self._grow(new)
-            at = positions.to(torch.int32)
+            at = None if self.rotation is None else positions.to(torch.int32)
             self.loop.run(layer)
         except BaseException:
             self.lens, self.free = held
@@ -134,11 +134,15 @@ class DecoderStack:
         have tokens in the cache attend to those too."""
         after = [a + n for a, n in zip(self.lens, new)]
         cached = any(self.lens)
-        q_starts, k_starts = self._starts(new), self._starts(after)
-        lens = torch.tensor(after, dtype=torch.int32, device=self.device)
+        q_starts = self._starts(new)
+        over_pages = self.rotation is not None or self.window > 0
+        if over_pages:
+            lens = torch.tensor(after, dtype=torch.int32, device=self.device)
+        else:
+            k_starts = self._starts(after)
 
         def attend(l, q, k, v):
-            if self.rotation is not None or self.window:
+            if over_pages:
                 out = torch.empty_like(q)
                 attend_chunk(q, self.caches[l], self.pages, q_starts, lens, out, window=self.window, sinks=self.sinks)
                 return out
