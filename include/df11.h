@@ -579,9 +579,15 @@ df11_status df11_attend_prompt(const df11_attend_prompt_args *args, int hip_devi
  * Otherwise all.  A sequence may have one query or all its tokens, or none.
  * scale, workspace and out as for df11_attend_token; weights are rounded as in
  * df11_attend_prompt (with 8 bits, of queries over few keys, as in
- * df11_attend_token).  The division of the work follows lens, on the device: a
- * table wider than the lengths costs workspace, hardly any time.  Starts that do
- * not ascend give undefined rows of out, and harm nothing else. */
+ * df11_attend_token).  The division of the work follows lens, on the device, but
+ * the table's width tells what the host has to know: up to 448 positions nothing
+ * is split, with no workspace and no second kernel (4 us of a small call); and one
+ * sequence of 2048 rows (n_q * n_heads / n_kv_heads) and more in a table of four
+ * times n_q positions is taken for a piece behind a long prefix, which makes a
+ * whole prompt in such a table up to 1.7 times slower.  So give the columns in use
+ * (row_stride stays); several sequences behind one table cost workspace by its
+ * width, hardly any time.  Starts that do not ascend give undefined rows of
+ * out, and harm nothing else. */
 typedef struct {
     df11_kv_cache cache;
     df11_page_table table;

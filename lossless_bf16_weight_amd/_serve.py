@@ -373,7 +373,8 @@ def attend_chunk(q: torch.Tensor, cache: KVCache, pages: torch.Tensor, q_starts:
     p, with a window above 0 of these only j > p - window and the first `sinks`.
     A row that sees no key is zero; rows behind the last sequence are left
     alone.  starts: int32 [sequences + 1].  scale, workspace: as for
-    attend_token."""
+    attend_token.  The table's width is taken for how long a single sequence
+    is: give the columns in use, pages[:, :entries]."""
     dev, hk, d, c = _cache_fields(cache)
     n, h, qr = _rows(q, "q", dev, d)
     _, _, orow = _rows(out, "out", dev, d, n, h)

@@ -297,8 +297,10 @@ df11_status check_prompt_sizes(const df11_attend_prompt_args &a) {
 // 993; 1500 on 17,500 413 and 471; in 8 bits, where codes are converted half as
 // often too, 1090 and 1187); and as they are nearly equal, the workgroups choose
 // the parts that end soonest, among up to three times as many as run at a time.
-// The length the host has from the table: a table of four times the queries is
-// taken for a long prefix (2048 on 8248 246 us and 250, 1024 on 4124 95 and 98;
+// The length the host has from the table, of which callers give the columns in use
+// (in one of 8192 positions a whole prompt of 512 tokens takes 25.6 us, in its own
+// 18.1, of 2048 65 and 56): a table of four times the queries is taken for a long
+// prefix (2048 on 8248 246 us and 250, 1024 on 4124 95 and 98;
 // 2048 on 6144 184 and 183, on 4096 125 and 118, on 2048 68 and 60; 256 on 4256 39
 // and 36).  Tiles of a whole prompt even out from 16,384 rows on (4096 tokens 151
 // us and 160, 6000 306 and 299, 8192 520 and 530).  Of several sequences the

@@ -138,13 +138,16 @@ class DecoderStack:
         over_pages = self.rotation is not None or self.window > 0
         if over_pages:
             lens = torch.tensor(after, dtype=torch.int32, device=self.device)
+            # (attend_chunk takes the width for how long a single sequence is: in a
+            # table of 8192 positions a first prompt of 512 took 25.6 us instead of 18.1)
+            pages = self.pages[:, :max(1, -(-max(after, default=0) // self.page_size))]
         else:
             k_starts = self._starts(after)
 
         def attend(l, q, k, v):
             if over_pages:
                 out = torch.empty_like(q)
-                attend_chunk(q, self.caches[l], self.pages, q_starts, lens, out, window=self.window, sinks=self.sinks)
+                attend_chunk(q, self.caches[l], pages, q_starts, lens, out, window=self.window, sinks=self.sinks)
                 return out
             if cached:     # what came before is in the cache
                 k, v = (torch.empty(sum(after), self.kv_heads, self.d, dtype=q.dtype, device=q.device) for _ in range(2))

@@ -73,3 +73,27 @@ def test_a_pass_makes_what_it_uses(rotation, window, calls):
     assert mode.casts == (2 if rotation else 0)
     names = {name for name, _, _ in log}
     assert names == {"kv_append" if rotation else "kv_write", "attend_token"} | ({"attend_chunk"} if rotation or window else {"attend_prompt", "kv_read"})
+
+
+@pytest.mark.parametrize("rotation,window", [(True, 0), (True, 8), (False, 8)])
+def test_prompts_attend_over_the_entries_in_use(rotation, window, calls):
+    """attend_chunk takes the table's width for the length of a single sequence:
+    it is given the columns that the longest sequence uses, of the stack's own table."""
+    log, _ = calls
+    s = _stack(rotation, window, max_len=8192)
+    after = [0, 0]
+    for new in ([3, 2], [13, 0], [1, 40], [0, 0], [0, 100]):
+        s.prompt(_rows(sum(new)), new)
+        after = [a + n for a, n in zip(after, new)]
+        name, args, _ = log[-1]
+        pages, lens = args[2], args[4]
+        assert name == "attend_chunk" and lens.tolist() == after
+        assert pages.shape == (2, -(-max(after) // PAGE)) and pages.data_ptr() == s.pages.data_ptr() and pages.stride() == s.pages.stride()
+        for i, n in enumerate(after):
+            at = torch.arange(n)
+            assert torch.equal(pages[i, at // PAGE], s.pages[i, at // PAGE])
+    empty = _stack(rotation, window)
+    empty.prompt(_rows(0), [0, 0])
+    assert log[-1][1][2].shape == (2, 1)
+    with pytest.raises(RuntimeError):      # (more than the table holds)
+        empty.prompt(_rows(1000), [1000, 0])
