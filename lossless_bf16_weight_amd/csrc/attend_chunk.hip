@@ -438,7 +438,7 @@ __device__ __forceinline__ void attend_single(const ChunkArgs &a, const Piece &p
 }
 
 template <int D, bool kInt8, bool kSplit, uint32_t kWaves>
-__global__ __launch_bounds__(64 * kWaves, 2) void attend_chunk_kernel(ChunkArgs a) {
+__global__ __launch_bounds__(64 * kWaves, kWaves == 4 && D == 64 ? 3 : 2) void attend_chunk_kernel(ChunkArgs a) {
     constexpr uint32_t kThreads = 64 * kWaves, kTile = kWaves * kWaveRows;
     constexpr int kChunks = D / 8;                           // 16-byte chunks of a row of words
     constexpr int kLoads = kPromptKeys * kChunks / kThreads; // chunks of words a thread stages
