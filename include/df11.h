@@ -388,11 +388,11 @@ df11_status df11_nf12_decode_batch(const void *const *host_headers, const void *
  * over the keys j that the row sees; a row that sees none, or whose scores
  * are all minus infinity, is zero.  What a row does not see (a later key, the
  * rest of a page, another sequence's rows) does not reach it, be it infinite
- * or NaN.  Products are of BF16 operands (attend_prompt rounds the weights p_j
- * to BF16; attend_token takes them as the sum of two); scores, maxima, sums
+ * or NaN.  Products are of BF16 operands (attend_prompt and most of attend_chunk
+ * round the weights p_j to BF16; attend_token takes them as the sum of two); scores, maxima, sums
  * and accumulators are in 32 bits, and the result is rounded once.  Where the
  * scores are finite in 32 bits, finite values give finite results, whatever
- * their size and the number of keys (but attend_prompt's rounded weights may
+ * their size and the number of keys (but rounded weights may
  * take a result within 2^-8 of the largest BF16 number to infinity).  Results
  * do not depend on other work on the GPU: sums are taken in a fixed order. */
 
@@ -577,9 +577,11 @@ df11_status df11_attend_prompt(const df11_attend_prompt_args *args, int hip_devi
  * n + i and sees the keys j <= p; with a window above 0, of these only j > p -
  * window and j < sinks (a window needs the flag; sinks without one do nothing).
  * Otherwise all.  A sequence may have one query or all its tokens, or none.
- * scale, workspace and out as for df11_attend_token; weights are rounded as in
- * df11_attend_prompt (with 8 bits, of queries over few keys, as in
- * df11_attend_token).  The division of the work follows lens, on the device, but
+ * scale, workspace and out as for df11_attend_token; weights are rounded to
+ * BF16 once, as in df11_attend_prompt (with 8 bits times the value's scale), but
+ * for sequences of one query over up to 16 heads a kv head, and with 8 bits for
+ * tiles of 128 or 256 rows that see keys in at most eight steps of 64, which have
+ * two operands a weight as in df11_attend_token.  The division of the work follows lens, on the device, but
  * the table's width tells what the host has to know: up to 448 positions nothing
  * is split, with no workspace and no second kernel (4 us of a small call); and one
  * sequence of 2048 rows (n_q * n_heads / n_kv_heads) and more in a table of four

@@ -65,7 +65,10 @@ __device__ __forceinline__ uint32_t of_lane(uint32_t x, uint32_t lane) { return 
 // has two steps' time beside its own, and what is written and joined of it.
 // Tiles behind a long prefix are equal, and their parts take whole rounds;
 // where the first tiles are short (`least` steps, of `steps`), these even the
-// end out.  (Few tiles have many parts, where rounding is harmless.)
+// end out.  (Few tiles have many parts, where rounding is harmless.)  Coefficients
+// need not be exact: with none, half or twice of the join's 0.028, or none or twice
+// of the two steps, 16 drawn pieces of 520 to 5000 tokens behind 1500 to 50,000 take
+// 0.99 to 1.01 of the time on average.
 __device__ __forceinline__ uint32_t parts_of_one(const ChunkArgs &a, uint32_t tiles, uint32_t least, uint32_t steps, uint32_t otherwise) {
 #pragma clang fp contract(off)      // (both kernels are to find the same)
     if (tiles * 8 < a.at_a_time) return otherwise;
@@ -93,10 +96,13 @@ __device__ __forceinline__ uint32_t items_before(uint32_t n_seqs, uint32_t per, 
 // each) end soonest, as far as these lower bounds say: the average, the longest
 // part, and for one more than run at a time (or than twice as many) the two (three)
 // that share a place.  A part has two steps' time beside its own, and what is
-// written and joined of it.  Up to eight sequences gain by it (three pieces of up
-// to 1000 on 10,000 keys 226 us, by the quota 250; six of the 8-bit case 354 and
-// 368), where parts are long; with 32 the search costs as much (28 single tokens
-// 105 us and 96; of eight 185 and 179).  0: no quota makes `item` one.
+// written and joined of it (0 or twice of the join's 0.007: within 2%).  A call of up
+// to eight sequences gains or loses by it: of 17 drawn ones each of 2 to 8 sequences,
+// pieces of 20 to 1500 behind 300 to 16,000 tokens, from 14% less to 18% more than by
+// the quota, 0.5% more on average (six of up to 701 on up to 12,701 in 8 bits 328 us
+// and 346, with heads of 64 209 and 196).  With the search 10 to 16 sequences take 2
+// to 5% more, 12 and 32 that have single tokens among them 5 and 13%.  0: no quota
+// makes `item` one.
 __device__ __forceinline__ uint32_t level_out(const ChunkArgs &a, uint32_t tiles, uint32_t steps, float total, uint32_t quota, uint32_t item) {
     const uint32_t smallest = (quota * 9 + 15) / 16;
     if (!__any(tiles && steps + smallest / 2 >= 2 * smallest)) return quota;      // (all tiles are whole)
@@ -581,6 +587,11 @@ __global__ __launch_bounds__(64 * kWaves, kWaves == 4 && D == 64 ? 3 : 2) void a
     // One step's keys.  kCareful: values that are infinite or NaN at keys which
     // only some rows see do not reach the others; in 8 bits (where values are
     // finite) a weight is the sum of two operands, as in attend_columns.hpp.
+    // Else a weight is rounded to one operand (errors of 0.0018 to 0.0023 of the
+    // norm, of two operands 0.0013 to 0.0017): a second one is as many products
+    // again with V, where products bound it (64 queries on 2001 keys 18.2 us, with
+    // two operands 20.7; 2048 on 32,049 897 us and 1291, in 8 bits 1041 and 1424;
+    // 16 prompts of up to 1024 tokens 91 and 110).
     const auto step = [&](auto careful, uint32_t key0, const uint8_t *kt, const uint8_t *vt, const float *sc) __attribute__((always_inline)) {
         constexpr bool kCareful = decltype(careful)::value;
         if (key0 >= wave_end || (key0 + kPromptKeys <= wave_begin && key0 >= a.sinks)) return;

@@ -17,14 +17,14 @@
 // sixteen) at a time.  Their sines it computes once, a pair a lane, and keeps
 // them and the weights in LDS, as eight waves for each SIMD have no registers
 // for them (with each lane's eight pairs and the weights in registers, five
-// waves for each SIMD: 15,183 tokens with norms 72.9 us and 67.8, heads of 64
-// 43.9 and 38.6, 5,520 tokens in 8 bits with their read 44.1 and 40.3).
+// waves for each SIMD, 15,183 tokens with norms took 7% longer, with heads of 64
+// 14%, 5,520 tokens in 8 bits with their read 9%).
 // Results are stored through the caches, though alone they are 8% faster past
 // them: the attention that reads them next is later by more.
 //
 // Measured with 32 heads over 8 kv heads of 128: 15,183 tokens with norms and
-// three axes 68 us (311 MB, 4.6 TB/s; heads of 64 4.0 TB/s), 20,288 tokens into
-// the cache 102.6 us (499 MB, 4.86 TB/s; a copy of 2 GiB reaches 4.95).
+// three axes 61 us (311 MB, 5.1 TB/s; heads of 64 38 us, 4.1 TB/s), 20,288 tokens
+// into the cache 97 us (499 MB, 5.1 TB/s; a copy of 2 GiB reaches 4.95).
 #include "serve_device.hpp"
 #include "serve_internal.hpp"
 

@@ -139,8 +139,9 @@ df11_status check_norms(const void *q_weight, const void *k_weight, float eps) {
 // What rotate_heads and kv_append share: the rotation, the norms, and the
 // waves.  A wave takes rows of one token, 64 lanes of 16 elements a step: three
 // steps, which are faster than a token's five or six (15,183 tokens with norms
-// 63.4 us and 67.9, 20,288 into the cache 99.3 and 102.4) and mostly than two (66
-// and 97.9); fewer where tokens are few, for as many waves as run at a time.
+// 60.9 us and 66.6, 20,288 into the cache 97.1 and 101.6) and mostly than two (63.0
+// and 97.3; 5,520 in 8 bits with their read 38.4 and 40.1, but 20,288 with heads of
+// 64 57.0 and 55.5); fewer where tokens are few, for as many waves as run at a time.
 df11_status heads_args(HeadsArgs *h, const df11_rotation &r, const void *q_weight, const void *k_weight, float eps, uint64_t n_tokens,
                        uint32_t rows, uint32_t head_dim, int dev) {
     const uint64_t steps = ceil_div((uint64_t)rows * head_dim, 64 * 16);
@@ -282,14 +283,17 @@ df11_status check_prompt_sizes(const df11_attend_prompt_args &a) {
 // the host does not know: the parts of equal size that it would be, as many as
 // workgroups run at a time, two for each compute unit (with heads of 64 three:
 // three pieces of up to 1000 on 10,000 134 us, divided by two 157), and the least
-// steps of one, four (64 queries on 2001 keys 18 us, with eight 22, with two 20).
+// steps of one, four (64 queries on 2001 keys 17.9 us, with two 18.7, with eight 20.8;
+// 36 single pieces of 16 to 200 on 700 to 30,000 keys take 2% less with two and 6%
+// more with eight, 18 calls of 2, 4 and 16 sequences 3% more and 3% less).
 // A tile's steps over the quota, rounded, are its parts: two from one and a half
 // on, so that all split tiles have at most four thirds of the parts asked for;
 // with nine sixteenths of the quota (level_out) 2.4 times as many, and so many
 // places the workspace has.  (A quarter more parts for all are a second round of
 // workgroups where parts are equal: 256 queries on 4256 keys 45 us and 38.)
-// Sequences of many are taken whole: each workgroup would read all their
-// lengths.
+// More than 512 sequences are taken whole, for each workgroup reads all their
+// lengths: a piece of 500 on 16,000 beside 511 of 20 tokens takes 262 us, beside 512
+// 466 (76 and 77 without it, alone 145).
 //
 // Behind a long prefix the tiles of a single sequence of 2048 rows and more have
 // 256 rows and eight waves, one workgroup for each compute unit, which read keys
