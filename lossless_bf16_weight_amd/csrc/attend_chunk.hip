@@ -28,9 +28,9 @@
 // Long pieces are bound by the matrix units at the card's power limit: 2048
 // queries of 32 heads over 8 of 128 on 32,049 keys take 915 to 943 us (1.12
 // PFLOP/s, where a 16,384-square product reaches 1.31), a prompt of 16,384 in a
-// window of 4096 905 to 929 us (1.05); heads of 64 575 to 595 us, of as many
+// window of 4096 905 to 943 us (1.05); heads of 64 575 to 595 us, of as many
 // exponentials.  Codes cost the vector units, which hide behind the products of
-// words: 1063 us, and six pieces of up to 701 queries 331 to 361 us for 284.  Four
+// words: 1063 us, and six pieces of up to 701 queries 328 to 361 us for 284.  Four
 // pieces of up to 512 behind up to 8192 with 28 single tokens take 156 to 176 us, for 520 MB, most of
 // them the tokens' (alone 96 us, 5.2 TB/s); 64 queries on 2001 keys 17.5 us, a
 // chain of reads, four steps and the join.
